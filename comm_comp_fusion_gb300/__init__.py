@@ -41,8 +41,13 @@ EXPORTS = ("xs_attn_a2a", "xs_attn", "xs_a2a_permute", "xs_a2a_permute_inverse",
            "xs_device_status", "xs_selftest_wait_timeout", "xs_version", "xs_attn_a2a_trace", "xs_attn_trace_layout",
            "xs_attn_causal_a2a", "xs_attn_causal", "xs_attn_a2a_q8", "xs_attn_q8",
            "xs_attn_a2a_qkv8", "xs_attn_qkv8", "xs_attn_a2a_host", "xs_attn_host",
+           "xs_rope", "xs_attn_window", "xs_attn_window_a2a", "xs_attn_window_workspace_size", "xs_cache_append",
+           "xs_attn_paged", "xs_attn_paged_workspace_size",
            # include/xs_burst.h
            "xs_burst_rec_bytes", "xs_burst_gap")
+
+
+XS_ROPE_HALVES, XS_ROPE_INVERSE, XS_ROPE_IN_SEQ, XS_ROPE_OUT_SEQ = 1, 2, 4, 8
 
 
 class XsError(RuntimeError):
@@ -106,6 +111,20 @@ def _load() -> ctypes.CDLL:
     lib.xs_attn_workspace_size.restype = i
     lib.xs_attn_a2a_noalloc.argtypes = [vp, vp, vp, vp, i, i, i, i, i, f, vp]
     lib.xs_attn_a2a_noalloc.restype = i
+    lib.xs_rope.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, ctypes.POINTER(i),
+                            ctypes.POINTER(ctypes.c_double), i, vp]
+    lib.xs_rope.restype = i
+    for fn in (lib.xs_attn_window, lib.xs_attn_window_a2a):
+        fn.argtypes = [vp, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, sz, vp]
+        fn.restype = i
+    lib.xs_attn_window_workspace_size.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
+    lib.xs_attn_window_workspace_size.restype = i
+    lib.xs_cache_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp]
+    lib.xs_cache_append.restype = i
+    lib.xs_attn_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, i, i, i, vp, sz, vp]
+    lib.xs_attn_paged.restype = i
+    lib.xs_attn_paged_workspace_size.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
+    lib.xs_attn_paged_workspace_size.restype = i
     lib.xs_last_error.argtypes = []
     lib.xs_last_error.restype = ctypes.c_char_p
     lib.xs_device_status.argtypes = [vp, i]
@@ -295,6 +314,110 @@ def attn_causal(q, k, v, out, B, S, H, D, P, scale, stream=None, check=True):
     st = lib.xs_attn_causal(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, S, H, D, P, float(scale),
                             _stream(stream, q, out))
     return _check(st) if check else st
+
+
+def _dense(x, name, numel, itemsize):
+    """A tensor argument of the calls below must be contiguous, of `itemsize`-byte elements and at least `numel` of them
+    (raw addresses are taken as they are)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_contiguous() or x.element_size() != itemsize or x.numel() < numel:
+        raise ValueError(f"{name}: {numel} contiguous elements of {itemsize} bytes are needed, got "
+                         f"{tuple(x.shape)} {x.dtype}{'' if x.is_contiguous() else ' (not contiguous)'}")
+    return x.data_ptr()
+
+
+class RopeAxes:
+    """How a head's elements turn with the token's place (``axis_dims``, ``freqs`` of ``xs_rope``): elements per axis
+    and one frequency in radians per pair; ``halves`` pairs elements half an axis apart instead of neighbours."""
+
+    def __init__(self, axis_dims, freqs, halves=False):
+        self.axis_dims, self.freqs, self.halves = tuple(axis_dims), tuple(freqs), bool(halves)
+        if len(self.freqs) != sum(self.axis_dims) // 2:
+            raise ValueError(f"{sum(self.axis_dims) // 2} frequencies are needed, got {len(self.freqs)}")
+        self._dims = (ctypes.c_int * len(self.axis_dims))(*self.axis_dims)
+        self._freqs = (ctypes.c_double * max(1, len(self.freqs)))(*self.freqs)
+
+    @classmethod
+    def powers(cls, axis_dims, theta=10000.0, scale=1.0, halves=False):
+        """The usual frequencies: ``scale * theta ** (-2 i / d)`` for pair i of an axis of d elements."""
+        return cls(axis_dims, [scale * theta ** (-2.0 * i / d) for d in axis_dims for i in range(d // 2)], halves)
+
+
+def rope(q, k, q_out, k_out, pos, B, S, H, Hk, D, P, axes, seq_in=False, seq_out=False, inverse=False, pos_batches=None,
+         stream=None, check=True):
+    """Rotary positions of q and k (``xs_rope``); ``axes`` is a ``RopeAxes``. ``k`` and ``k_out`` may be None with
+    Hk = 0. ``pos``: int32 [B or 1][S][axes]; ``pos_batches`` defaults to B unless ``pos`` is a tensor of one batch."""
+    n = len(axes.axis_dims)
+    if pos_batches is None:
+        pos_batches = 1 if not isinstance(pos, int) and pos is not None and pos.numel() == S * n else B
+    flags = ((XS_ROPE_HALVES if axes.halves else 0) | (XS_ROPE_INVERSE if inverse else 0)
+             | (XS_ROPE_IN_SEQ if seq_in else 0) | (XS_ROPE_OUT_SEQ if seq_out else 0))
+    nq, nk = B * S * H * D, B * S * Hk * D
+    st = lib.xs_rope(_dense(q, "q", nq, 2), _dense(k, "k", nk, 2), _dense(q_out, "q_out", nq, 2),
+                     _dense(k_out, "k_out", nk, 2), _dense(pos, "pos", pos_batches * S * n, 4), pos_batches, B, S, H, Hk,
+                     D, P, n, axes._dims, axes._freqs, flags, _stream(stream, q, q_out))
+    return _check(st) if check else st
+
+
+def _window(fn, q, k, v, out, B, S, H, D, P, scale, left, right, sinks, workspace, workspace_bytes, stream, check):
+    n = B * S * H * D
+    st = fn(_dense(q, "q", n, 2), _dense(k, "k", n, 2), _dense(v, "v", n, 2), _dense(out, "out", n, 2), B, S, H, D, P,
+            float(scale), left, right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+            _stream(stream, q, out))
+    return _check(st) if check else st
+
+
+def attn_window(q, k, v, out, B, S, H, D, P, scale, left=-1, right=0, sinks=0, workspace=None, workspace_bytes=None,
+                stream=None, check=True):
+    """Attention through a sliding window with sinks (``xs_attn_window``), head-partitioned output; -1: no limit on
+    that side. ``workspace=None`` works on whole query tiles only."""
+    return _window(lib.xs_attn_window, q, k, v, out, B, S, H, D, P, scale, left, right, sinks, workspace,
+                   workspace_bytes, stream, check)
+
+
+def attn_window_a2a(q, k, v, out, B, S, H, D, P, scale, left=-1, right=0, sinks=0, workspace=None, workspace_bytes=None,
+                    stream=None, check=True):
+    """``attn_window`` with the All-to-All scatter (``xs_attn_window_a2a``), sequence-partitioned output."""
+    return _window(lib.xs_attn_window_a2a, q, k, v, out, B, S, H, D, P, scale, left, right, sinks, workspace,
+                   workspace_bytes, stream, check)
+
+
+def attn_window_workspace_size(B, S, H, D, P) -> int:
+    """``xs_attn_window_workspace_size`` for the current device, in bytes."""
+    n = ctypes.c_size_t(0)
+    _check(lib.xs_attn_window_workspace_size(B, S, H, D, P, ctypes.byref(n)))
+    return n.value
+
+
+def cache_append(k, v, k_pages, v_pages, page_table, q_start, kv_len, N, T, Hk, D, page, n_pages, max_pages,
+                 stream=None, check=True):
+    """Writes the new tokens' keys and values into their pages (``xs_cache_append``)."""
+    rows, pool = T * Hk * D, n_pages * page * Hk * D
+    st = lib.xs_cache_append(_dense(k, "k", rows, 2), _dense(v, "v", rows, 2), _dense(k_pages, "k_pages", pool, 2),
+                             _dense(v_pages, "v_pages", pool, 2), _dense(page_table, "page_table", N * max_pages, 4),
+                             _dense(q_start, "q_start", N + 1, 4), _dense(kv_len, "kv_len", N, 4), N, T, Hk, D, page,
+                             n_pages, max_pages, _stream(stream, k, k_pages))
+    return _check(st) if check else st
+
+
+def attn_paged(q, k_pages, v_pages, page_table, q_start, kv_len, out, N, T, H, Hk, D, page, n_pages, max_pages, scale,
+               left=-1, right=0, sinks=0, workspace=None, workspace_bytes=None, stream=None, check=True):
+    """Attention of the packed new tokens over a paged cache (``xs_attn_paged``); the workspace is required."""
+    rows, pool = T * H * D, n_pages * page * Hk * D
+    st = lib.xs_attn_paged(_dense(q, "q", rows, 2), _dense(k_pages, "k_pages", pool, 2),
+                           _dense(v_pages, "v_pages", pool, 2), _dense(page_table, "page_table", N * max_pages, 4),
+                           _dense(q_start, "q_start", N + 1, 4), _dense(kv_len, "kv_len", N, 4),
+                           _dense(out, "out", rows, 2), N, T, H, Hk, D, page, n_pages, max_pages, float(scale), left,
+                           right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
+    return _check(st) if check else st
+
+
+def attn_paged_workspace_size(N, T, H, Hk, D) -> int:
+    """``xs_attn_paged_workspace_size`` for the current device, in bytes."""
+    n = ctypes.c_size_t(0)
+    _check(lib.xs_attn_paged_workspace_size(N, T, H, Hk, D, ctypes.byref(n)))
+    return n.value
 
 
 def attn_a2a_trace(q, k, v, out, B, S, H, D, P, scale, trace, trace_bytes=None, stream=None, check=True):

@@ -491,6 +491,26 @@ namespace xs {
 // Records `message` as this thread's last error and returns `status`; for the
 // other translation units of the library.
 int report_error(int status, const char *message) { return (int)fail((xs_status)status, "%s", message); }
+
+// The checks above, for the calls in xs_ops_api.cpp.
+int api_fail(int status, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return (int)fail((xs_status)status, "%s", buf);
+}
+int api_cuda_error(const char *what, cudaError_t e) { return (int)fail_cuda(what, e); }
+int api_device(int *dev, int *num_sms) {
+    DeviceInfo info;
+    const xs_status st = current_device(dev, &info);
+    *num_sms = info.num_sms;
+    return (int)st;
+}
+int api_device_pointer(const void *ptr, int dev, const char *name) { return (int)check_device_pointer(ptr, dev, name); }
+int api_shape(int B, int S, int H, int D, int P, size_t *bytes) { return (int)check_shape(B, S, H, D, P, true, bytes); }
+bool api_overlaps(const void *a, size_t na, const void *b, size_t nb) { return overlaps(a, na, b, nb); }
 }  // namespace xs
 
 extern "C" {

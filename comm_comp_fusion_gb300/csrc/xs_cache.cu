@@ -1,0 +1,59 @@
+// xs_cache.cu -- writes the keys and values of new tokens into the pages of a
+// paged cache.
+//
+// Token i of sequence n has place kv_len[n] - q_len[n] + i; its row goes to row
+// place % page of page page_table[n][place / page]. A pure copy, bound by HBM
+// for prompts and by latency for single tokens: one warp copies one token's K
+// and V rows (Hk * D elements each) and looks its sequence up while the first
+// loads are on their way.
+#include "xs_internal.h"
+
+namespace xs {
+
+constexpr int kAppendWarps = 4;
+
+__global__ void __launch_bounds__(32 * kAppendWarps) cache_append_kernel(const AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const uint4 *k = p.k + (int64_t)t * p.chunks, *v = p.v + (int64_t)t * p.chunks;
+    constexpr int U = 4;
+    uint4 kr[U], vr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = u * 32 + lane;
+        if (c < p.chunks) {
+            kr[u] = k[c];
+            vr[u] = v[c];
+        }
+    }
+    const CacheRow at = find_sequence(p.q_start, p.N, p.T, t, lane);
+    if (at.seq < 0) return;  // a row of no sequence
+    const int64_t cap = (int64_t)p.max_pages * p.page;
+    const int64_t len = p.kv_len[at.seq];
+    const int64_t place = len - at.q_len + at.i;
+    if (place < 0 || place >= cap) return;
+    const int pg = (int)(place / p.page);
+    const int id = p.table[(int64_t)at.seq * p.max_pages + pg];
+    if (id < 0 || id >= p.n_pages) return;
+    const int64_t row = ((int64_t)id * p.page + (place - (int64_t)pg * p.page)) * p.chunks;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = u * 32 + lane;
+        if (c < p.chunks) {
+            p.k_pages[row + c] = kr[u];
+            p.v_pages[row + c] = vr[u];
+        }
+    }
+    for (int c = U * 32 + lane; c < p.chunks; c += 32) {
+        p.k_pages[row + c] = k[c];
+        p.v_pages[row + c] = v[c];
+    }
+}
+
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream) {
+    cache_append_kernel<<<(unsigned)((p.T + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace xs

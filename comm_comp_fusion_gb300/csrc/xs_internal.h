@@ -138,4 +138,90 @@ void fastdiv_magic(uint32_t d, uint32_t *m, uint32_t *s);
 cudaError_t launch_permute(const void *in, void *out, const PermParams &p, bool inverse, int num_sms,
                            cudaStream_t stream);
 
+// ------------------------------------------------------------ rotary positions
+constexpr int kRopeMaxPairs = 128, kRopeMaxUnits = 32, kRopeMaxAxes = 4;
+struct RopeParams {
+    const uint16_t *q, *k;  // k NULL: none (Hk = 0)
+    uint16_t *q_out, *k_out;
+    const int *pos;         // [pos batches][S][n_axes]
+    int64_t pos_batch;      // S, or 0 when every batch shares the positions
+    int B, S, H, Hk, Hl, Hkl, Sl, D;
+    int n_axes, n_pairs;
+    int units;              // units of work per row (rope_kernel)
+    int tile;               // tokens per block
+    bool seq_in, seq_out, inverse;
+    uint32_t mU, sU, mH, sH, mSl, sSl;  // magic numbers: division by units, H + Hk, Sl
+    uint64_t frac[kRopeMaxPairs];       // frequency in turns, a 64-bit binary fraction
+    uint8_t axis[kRopeMaxPairs];
+    uint8_t unit_first[kRopeMaxUnits], unit_half[kRopeMaxUnits];  // pairs half an axis apart: see rope_kernel
+};
+cudaError_t launch_rope(RopeParams &p, bool halves, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ paged cache
+struct AppendParams {
+    const uint4 *k, *v;
+    uint4 *k_pages, *v_pages;
+    const int *table, *q_start, *kv_len;
+    int N, T, chunks;  // chunks: 16-byte chunks of a token's Hk * D elements
+    int page, n_pages, max_pages;
+};
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+
+// ------------------------------------------------------------ window and paged attention
+struct SpanParams {
+    const uint16_t *q, *k, *v;  // k, v: the page pools when paged
+    uint16_t *out;
+    const int *table, *q_start, *kv_len;  // table NULL: whole sequences, head-partitioned
+    int N, T, H, Hk, G;         // whole sequences: T = B * S rows of H heads
+    int page, n_pages, max_pages;
+    int B, S, P, Hl, Sl, head_out;  // whole sequences only
+    int left, right, sinks;     // at most 2^30 each
+    float scale_log2;
+};
+size_t span_workspace_bytes(int D, int num_sms);
+cudaError_t launch_span(int D, const SpanParams &p, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ host helpers of the C ABI (xs_api.cpp)
+// Each records the thread's last error and returns a status (0: fine).
+int api_fail(int status, const char *fmt, ...);
+int api_cuda_error(const char *what, cudaError_t e);
+int api_device(int *dev, int *num_sms);
+int api_device_pointer(const void *ptr, int dev, const char *name);
+int api_shape(int B, int S, int H, int D, int P, size_t *bytes);
+bool api_overlaps(const void *a, size_t na, const void *b, size_t nb);
+
 }  // namespace xs
+
+#ifdef __CUDACC__
+namespace xs {
+
+// The sequence that packed row t belongs to, its place among the sequence's new
+// tokens and their number; seq = -1 for a row of none. Bounds of q_start are
+// cut to [0, T], so no table leads outside the packed rows. All 32 lanes of a
+// warp call it with the same t: each round narrows N to N / 32 with one load
+// per lane.
+struct CacheRow {
+    int seq, i, q_len;
+};
+__device__ __forceinline__ CacheRow find_sequence(const int *q_start, int N, int T, int t, int lane) {
+    int lo = 0, n = N + 1;  // the last of q_start[lo .. lo + n) that is at most t
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool ok = lane * step < n && q_start[at] <= t;
+        const uint32_t votes = __ballot_sync(0xffffffffu, ok);
+        const int hit = votes ? 31 - __clz((int)votes) : 0;
+        n = min(step, n - hit * step);
+        lo += hit * step;
+    }
+    CacheRow r{-1, 0, 0};
+    if (lo >= N) return r;
+    const int a = min(max(q_start[lo], 0), T), b = min(max(q_start[lo + 1], 0), T);
+    if (t < a || t >= b) return r;
+    r.seq = lo;
+    r.i = t - a;
+    r.q_len = b - a;
+    return r;
+}
+
+}  // namespace xs
+#endif

@@ -317,6 +317,126 @@ xs_status xs_attn_a2a_trace(const void *q, const void *k, const void *v, void *o
  * shapes on the current device. */
 xs_status xs_attn_trace_layout(int B, int S, int H, int D, int P, int *ctas, int *items_per_cta, size_t *bytes);
 
+/*
+ * The operators around the fused attention. The X-Stage paper has no
+ * counterpart to them: a video DiT turns q and k by rotary positions before
+ * attention, long sequences attend through a window, and an autoregressive
+ * model keeps its keys and values in a paged cache. The common rules above hold
+ * unless a call says otherwise. None of these calls synchronises, allocates or
+ * keeps anything between calls, so each can be captured into a CUDA graph and
+ * replayed; calls (or replays) that may run at the same time must not share a
+ * workspace or write the same memory.
+ */
+
+/*
+ * Rotary positions with one to four axes (time, height and width of a video
+ * token, or the place in a text) for queries and keys.
+ *   q, q_out : [..][H][D] bf16; k, k_out: the same with Hk heads (Hk = 0: no keys,
+ *            k and k_out are ignored). Head-partitioned [P][B][S][H/P][D], or
+ *            sequence-partitioned [P][B][S/P][H][D] where the flags say so;
+ *            with XS_ROPE_IN_SEQ and not XS_ROPE_OUT_SEQ the call is also the
+ *            pre-attention All-to-All (xs_a2a_permute_inverse) of its input.
+ *   pos    : device, [pos_batches][S][n_axes] int32, token s's place on each axis
+ *            (any 32-bit value). pos_batches = B, or 1 for positions that all
+ *            batches share.
+ *   axis_dims, freqs : HOST arrays, read before the call returns. Axis a turns
+ *            axis_dims[a] elements of each head, axes in order from element 0;
+ *            elements past their sum are copied unchanged. freqs holds
+ *            sum(axis_dims) / 2 frequencies in radians per unit of place, one per
+ *            pair in order (commonly theta^(-2 i / axis_dims[a]) for the axis's
+ *            pair i); |freqs| <= 1e6.
+ *   flags  : XS_ROPE_HALVES: an axis's pair i is its elements i and
+ *            i + axis_dims[a] / 2 (otherwise 2i and 2i + 1). XS_ROPE_INVERSE: turn
+ *            by the negative angle, which undoes the call and is also its
+ *            gradient (d q_out -> d q).
+ * The pair (x, y) at place p becomes (x cos pf - y sin pf, x sin pf + y cos pf),
+ * in fp32, rounded to bf16 once. Angles are reduced exactly, so far places are
+ * as accurate as near ones.
+ * q_out may be q and k_out may be k when the layouts in and out are the same (or
+ * P = 1); any other overlap is XS_ERR_ALIAS. Extra rules: axis_dims even, in
+ * multiples of 16 with XS_ROPE_HALVES (XS_ERR_UNSUPPORTED otherwise), their sum at
+ * most D; Hk % P == 0; H + Hk <= 65536; pos 4-byte aligned.
+ */
+enum { XS_ROPE_HALVES = 1, XS_ROPE_INVERSE = 2, XS_ROPE_IN_SEQ = 4, XS_ROPE_OUT_SEQ = 8 };
+xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const int32_t *pos, int pos_batches, int B,
+                  int S, int H, int Hk, int D, int P, int n_axes, const int *axis_dims, const double *freqs, int flags,
+                  void *stream);
+
+/*
+ * Attention through a sliding window with sinks, over whole sequences. Token i
+ * of a head sees key token j of the same sequence iff
+ *     j <= i + right   and   (j >= i - left  or  j < sinks):
+ * the `left` tokens before it, itself, the `right` tokens after it, and, within
+ * the same right end, the first `sinks` tokens of the sequence. -1 for left or
+ * right sets no limit on that side: (left -1, right 0) is causal attention,
+ * (left w, right w) a two-sided window, (left w, right 0) a causal window.
+ *   q, k, v, out, scale : as for xs_attn (xs_attn_window, head-partitioned out)
+ *            and xs_attn_a2a (xs_attn_window_a2a, All-to-All scatter); the second
+ *            is bit-identical to xs_a2a_permute of the first. K/V tiles that no
+ *            token of a query tile sees are skipped.
+ *   workspace, workspace_bytes : device memory, 256-byte aligned, of at least
+ *            xs_attn_window_workspace_size bytes; it needs no initialisation. With
+ *            it the work is split evenly over the SMs, pieces of a query tile
+ *            meeting in the workspace. NULL (with 0): whole query tiles only.
+ * left, right >= -1, sinks >= 0. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
+ */
+xs_status xs_attn_window(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,
+                         float scale, int left, int right, int sinks, void *workspace, size_t workspace_bytes,
+                         void *stream);
+xs_status xs_attn_window_a2a(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,
+                             float scale, int left, int right, int sinks, void *workspace, size_t workspace_bytes,
+                             void *stream);
+xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_t *bytes);
+
+/*
+ * A paged key/value cache. A pool holds n_pages pages of `page` tokens each:
+ *   k_pages, v_pages : [n_pages][page][Hk][D] bf16.
+ * Each of N sequences has a row of the page table, and new tokens of all
+ * sequences are packed one after the other:
+ *   page_table : device [N][max_pages] int32; key j of sequence n is row j % page
+ *            of page page_table[n][j / page]. Entries that no key of the
+ *            sequence needs are not looked at and may hold anything.
+ *   q_start : device [N + 1] int32, ascending from 0: sequence n's new tokens are the
+ *            packed rows q_start[n] .. q_start[n + 1] - 1 (none if equal). Rows from
+ *            q_start[N] up to T belong to no sequence.
+ *   kv_len : device [N] int32, keys of each sequence, its new tokens included:
+ *            new token i stands at place kv_len[n] - (q_start[n + 1] - q_start[n]) + i.
+ * All three are read by the kernels, so a captured call follows them when they
+ * change between replays. They are not checked on the host. What they name
+ * outside the pool, the table or the packed rows is never accessed: keys in
+ * pages outside 0 .. n_pages - 1 are undefined in attention and are not written by
+ * the append, and lengths are cut to max_pages * page keys.
+ * page: a power of two from 16 to 1024; max_pages * page <= 2^30; D = 64, 96 or 128.
+ *
+ * xs_cache_append writes the new tokens' keys and values,
+ *   k, v : [T][Hk][D] bf16,
+ * into their pages. Everything else in the pools stays as it is. Two tokens must
+ * not land in one row (pages shared by two sequences are only for reading).
+ */
+xs_status xs_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, const int32_t *page_table,
+                          const int32_t *q_start, const int32_t *kv_len, int N, int T, int Hk, int D, int page,
+                          int n_pages, int max_pages, void *stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their own keys too: append
+ * first). The token at place i sees the keys 0 .. kv_len[n] - 1 of its sequence
+ * under the rule of xs_attn_window; (-1, 0, 0) is causal attention over the
+ * whole cache, for a chunk of a prompt or for single new tokens.
+ *   q, out : [T][H][D] bf16; query head h reads key head h / (H / Hk). Rows of no
+ *            sequence are left as they are in out. A token that sees no key
+ *            (kv_len shorter than the new tokens) gets zeros.
+ *   workspace, workspace_bytes : required (unless the call is empty), as for
+ *            xs_attn_window, of xs_attn_paged_workspace_size bytes.
+ * K and V of a sequence's own kv_len tokens must be finite; what lies behind them
+ * in the last page, and in pages the window has passed, may hold anything.
+ * H % Hk == 0 and H / Hk <= 128.
+ */
+xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                        const int32_t *q_start, const int32_t *kv_len, void *out, int N, int T, int H, int Hk, int D,
+                        int page, int n_pages, int max_pages, float scale, int left, int right, int sinks,
+                        void *workspace, size_t workspace_bytes, void *stream);
+xs_status xs_attn_paged_workspace_size(int N, int T, int H, int Hk, int D, size_t *bytes);
+
 /* Human-readable description of the last non-OK status returned on this host
  * thread (empty string if none). The pointer stays valid until the next call
  * on this thread. */

@@ -1,0 +1,364 @@
+"""The paged cache: writing new tokens into pages (xs_cache_append) and attention of new tokens over it (xs_attn_paged),
+against 64 bits; the operators in a row as a serving loop calls them; refusals."""
+import numpy as np
+import pytest
+
+from span_testlib import attend, bf16, check, seen_mask, values
+from xs_testlib import from_dev, guarded, to_dev
+
+NAN = 0x7FC1
+
+
+class Batch:
+    """A cache with scattered pages. Whatever no sequence owns holds NaN; table entries past a sequence's pages hold
+    numbers far outside the pool."""
+
+    def __init__(self, q_len, kv_len, H, Hk, D, page, spare=0, seed=0, sigma=1.0, evict=0):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.q_len, self.kv, self.H, self.Hk, self.D, self.page = q_len, kv_len, H, Hk, D, page
+        self.N, self.T = len(q_len), sum(q_len) + spare
+        need = [-(-n // page) for n in kv_len]
+        self.max_pages, self.n_pages = max(max(need), 1) + 1, sum(need) + 2
+        ids = rng.permutation(self.n_pages)
+        table = rng.choice(np.array([-1, -2 ** 31, 2 ** 31 - 1, self.n_pages]), (self.N, self.max_pages))
+        kp = np.full((self.n_pages, page, Hk, D), NAN, np.uint16)
+        vp = np.full((self.n_pages, page, Hk, D), NAN, np.uint16)
+        self.k, self.v, at = [], [], 0
+        for n in range(self.N):
+            kb, k = bf16(rng, (kv_len[n], Hk, D), sigma)
+            vb, v = bf16(rng, (kv_len[n], Hk, D))
+            self.k.append(k)
+            self.v.append(v)
+            for j in range(need[n]):
+                i = int(ids[at])
+                at += 1
+                table[n, j] = i
+                m = min(page, kv_len[n] - j * page)
+                kp[i, :m], vp[i, :m] = kb[j * page:j * page + m], vb[j * page:j * page + m]
+            for j in range(evict):  # pages that a window has passed: their entries may hold anything
+                table[n, j] = (-7, 2 ** 31 - 1)[j % 2]
+        self.qb, self.q = bf16(rng, (self.T, H, D), sigma)
+        self.table = torch.from_numpy(table.astype(np.int32)).cuda()
+        self.q_start = torch.tensor(np.concatenate(([0], np.cumsum(q_len))), dtype=torch.int32, device="cuda")
+        self.kv_len = torch.tensor(kv_len, dtype=torch.int32, device="cuda")
+        self.dq, self.kp, self.vp = to_dev(self.qb), to_dev(kp), to_dev(vp)
+        self.out = guarded(self.T * H * D)
+        import comm_comp_fusion_gb300 as xs
+        self.ws = guarded(xs.attn_paged_workspace_size(self.N, self.T, H, Hk, D), torch.uint8)
+
+    def call(self, left=-1, right=0, sinks=0, out=None, **kw):
+        import comm_comp_fusion_gb300 as xs
+        return xs.attn_paged(self.dq, self.kp, self.vp, self.table, self.q_start, self.kv_len,
+                             self.out if out is None else out, self.N, self.T, self.H, self.Hk, self.D, self.page,
+                             self.n_pages, self.max_pages, self.D ** -0.5, left, right, sinks, self.ws, **kw)
+
+    def verify(self, left=-1, right=0, sinks=0, what=""):
+        import torch
+        import comm_comp_fusion_gb300 as xs
+        torch.cuda.synchronize()
+        assert xs.device_status() == xs.XS_OK, xs.last_error()
+        got = from_dev(self.out).reshape(self.T, self.H, self.D)
+        G, t = self.H // self.Hk, 0
+        for n, (ql, kl) in enumerate(zip(self.q_len, self.kv)):
+            pos = np.arange(kl - ql, kl)
+            seen = seen_mask(pos, kl, left, right, sinks)
+            for h in range(self.H):
+                ref, bound = attend(self.q[t:t + ql, h], self.k[n][:, h // G], self.v[n][:, h // G], seen, self.D ** -0.5)
+                check(got[t:t + ql, h], ref, bound, f"{what} sequence {n} head {h}")
+                assert (got[t:t + ql, h][~seen.any(-1)] == 0).all()
+            t += ql
+        assert (got[t:] == 0xFFFF).all(), "rows of no sequence were written"
+
+
+CASES = [  # q_len, kv_len, H, Hk, D, page, spare, (left, right, sinks)
+    ([1], [1], 1, 1, 64, 16, 0, (-1, 0, 0)),
+    ([1], [1], 8, 1, 128, 16, 3, (-1, 0, 0)),
+    ([1, 1, 1], [17, 128, 129], 8, 2, 128, 16, 0, (-1, 0, 0)),
+    ([1] * 5, [300, 5, 1111, 64, 257], 6, 2, 96, 32, 2, (-1, 0, 0)),      # three heads a key head
+    ([1] * 3, [4100, 33, 900], 32, 8, 128, 64, 0, (-1, 0, 0)),
+    ([1], [20000], 4, 4, 64, 128, 0, (-1, 0, 0)),                          # split many times
+    ([1] * 70, list(range(1, 1400, 20)), 2, 1, 64, 16, 0, (-1, 0, 0)),     # more sequences than a warp's lanes
+    ([1, 1], [3000, 2000], 16, 1, 64, 16, 0, (255, 0, 4)),                 # window with sinks
+    ([5, 0, 2, 0], [5, 77, 600, 0], 4, 2, 128, 16, 1, (-1, 0, 0)),         # no new tokens, empty sequences
+    ([33], [33], 7, 1, 64, 32, 0, (-1, 0, 0)),                             # seven heads a key head: 126 rows of a tile
+    ([300], [1000], 4, 4, 128, 64, 5, (-1, 0, 0)),
+    ([257, 1, 128], [257, 700, 1500], 8, 4, 96, 256, 9, (-1, 0, 0)),
+    ([200, 64], [900, 64], 10, 2, 64, 16, 0, (100, 0, 30)),
+    ([200, 64], [900, 500], 4, 2, 128, 1024, 0, (100, 37, 0)),             # two-sided window
+    ([150], [650], 4, 2, 128, 16, 0, (-1, -1, 0)),                         # a chunk that sees all of itself
+    ([9, 40], [3, 39], 4, 2, 128, 16, 2, (-1, 0, 0)),                      # fewer keys than new tokens: rows without any
+    ([9], [0], 4, 2, 64, 16, 0, (-1, -1, 0)),
+    ([3], [400], 128, 1, 64, 16, 0, (-1, 0, 0)),                           # 128 heads a key head
+    ([600], [2500], 5, 1, 128, 32, 0, (700, 0, 140)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_paged_matches_64_bits(case):
+    q_len, kv_len, H, Hk, D, page, spare, span = CASES[case]
+    b = Batch(q_len, kv_len, H, Hk, D, page, spare, seed=case)
+    b.call(*span)
+    b.verify(*span, what=str(CASES[case][2:]))
+    b.out.fill_(-1)
+    b.ws.fill_(255)
+    b.call(*span)
+    b.verify(*span, what="again, workspace of ones")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", (64, 96, 128))
+def test_paged_passed_pages_may_hold_anything(D):
+    """Pages that no token's window reaches are not looked at, whatever their table entries say."""
+    b = Batch([3], [1000], 4, 2, D, 16, seed=5, evict=55)   # the first key seen is 997 - 100 = 897, page 56
+    b.call(100, 0, 0)
+    b.verify(100, 0, 0)
+
+
+@pytest.mark.gpu
+def test_paged_peaked_scores():
+    b = Batch([1, 40], [2000, 700], 8, 2, 128, 16, seed=3, sigma=4.0)
+    b.call()
+    b.verify()
+
+
+@pytest.mark.gpu
+def test_paged_graph_follows_lengths():
+    """A captured call follows table, lengths and starts that change between replays; two captured calls take turns in
+    one workspace."""
+    import torch
+    b = Batch([1, 1, 1], [700, 300, 1000], 8, 2, 128, 16, seed=7)
+    c = Batch([60, 5], [500, 1200], 8, 2, 128, 32, seed=8)
+    c.ws = b.ws
+    graphs = []
+    for x in (b, c):
+        x.call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.call()
+        graphs.append(g)
+    for kv in ([700, 300, 1000], [1, 290, 513], [128, 127, 640]):
+        b.kv = kv
+        b.kv_len.copy_(torch.tensor(kv, dtype=torch.int32))
+        full = (b.k, b.v)
+        b.k, b.v = ([a[:n] for a, n in zip(x, kv)] for x in full)
+        for x, g in zip((b, c), graphs):
+            x.out.fill_(-1)
+            g.replay()
+            x.verify()
+        b.k, b.v = full
+
+
+@pytest.mark.gpu
+def test_paged_pool_past_32_bits():
+    """Pages more than 2^31 elements into the pool."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    Hk, D, page = 8, 128, 256
+    n_pages = 2 ** 31 // (Hk * D * page) + 8
+    kp, vp = (torch.empty(n_pages * page * Hk * D, dtype=torch.int16, device="cuda") for _ in range(2))
+    b = Batch([7], [700], 16, Hk, D, page, seed=2)
+    last = torch.arange(n_pages - 1, n_pages - 4, -1, dtype=torch.int32, device="cuda")
+    old = b.table[0, :3].clone()
+    for dst, src in ((kp, b.kp), (vp, b.vp)):
+        dst.view(n_pages, -1)[last.long()] = src.view(b.n_pages, -1)[old.long()]
+    b.table[0, :3] = last
+    b.kp, b.vp, b.n_pages = kp, vp, n_pages
+    b.call()
+    b.verify()
+    k = to_dev(bf16(np.random.default_rng(0), (7, Hk, D))[0])
+    xs.cache_append(k, k, kp, vp, b.table, b.q_start, b.kv_len, 1, 7, Hk, D, page, n_pages, b.max_pages)
+    rows = vp.view(n_pages, page, Hk * D)[int(last[2]), 700 - 512 - 7:700 - 512]
+    assert torch.equal(rows.reshape(-1), k.reshape(-1))
+
+
+# ------------------------------------------------------------------ append
+
+APPEND = [  # q_len, kv_len, Hk, D, page, spare
+    ([1], [1], 1, 64, 16, 0),
+    ([1, 1, 1], [17, 16, 300], 8, 128, 16, 2),
+    ([5, 0, 40, 1], [5, 9, 100, 64], 3, 96, 32, 7),
+    ([300, 77], [1000, 77], 4, 128, 64, 0),
+    ([1] * 100, list(range(1, 301, 3)), 1, 64, 16, 0),
+    ([2] * 40, list(range(2, 82, 2)), 40, 128, 1024, 1),     # more than 512 chunks a token
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", range(len(APPEND)))
+def test_append_writes_exactly_its_rows(case):
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    q_len, kv_len, Hk, D, page, spare = APPEND[case]
+    b = Batch(q_len, kv_len, Hk, Hk, D, page, spare, seed=case)
+    rng = np.random.default_rng(99)
+    kb, vb = bf16(rng, (b.T, Hk, D))[0], bf16(rng, (b.T, Hk, D))[0]
+    kp, vp = guarded(b.kp.numel()), guarded(b.vp.numel())
+    kp.copy_(b.kp.view(-1))
+    vp.copy_(b.vp.view(-1))
+    xs.cache_append(to_dev(kb), to_dev(vb), kp, vp, b.table, b.q_start, b.kv_len, b.N, b.T, Hk, D, page, b.n_pages,
+                    b.max_pages)
+    torch.cuda.synchronize()
+    table = b.table.cpu().numpy()
+    for got, old, new in ((kp, b.kp, kb), (vp, b.vp, vb)):
+        want, t = from_dev(old).reshape(b.n_pages, page, Hk, D).copy(), 0
+        for n in range(b.N):
+            for i in range(q_len[n]):
+                place = kv_len[n] - q_len[n] + i
+                want[table[n, place // page], place % page] = new[t + i]
+            t += q_len[n]
+        assert np.array_equal(from_dev(got).reshape(want.shape), want)
+
+
+@pytest.mark.gpu
+def test_append_and_attention_ignore_bad_metadata():
+    """Table entries, starts and lengths that lead outside the pool, the table or the packed rows touch nothing."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    b = Batch([2, 3, 2], [40, 60, 20], 4, 2, 64, 16, spare=2, seed=1)
+    kp, vp = guarded(b.kp.numel()), guarded(b.vp.numel())
+    kp.fill_(0)
+    vp.fill_(0)
+    new = to_dev(bf16(np.random.default_rng(0), (b.T, 2, 64))[0])
+    good = b.table.clone(), b.q_start.clone(), b.kv_len.clone()
+    for what in range(5):
+        b.table, b.q_start, b.kv_len = (x.clone() for x in good)
+        if what == 0:
+            b.table.fill_(2 ** 31 - 1)
+        elif what == 1:
+            b.table.fill_(-1)
+        elif what == 2:
+            b.kv_len.copy_(torch.tensor([2 ** 31 - 1, -5, 10 ** 6], dtype=torch.int32))
+            b.table.fill_(b.n_pages)
+        elif what == 3:
+            b.q_start.copy_(torch.tensor([9, 100, 10 ** 9, 2 ** 31 - 1], dtype=torch.int32))
+        else:
+            b.q_start.copy_(torch.tensor([-7, -3, -1, 0], dtype=torch.int32))
+        xs.cache_append(new, new, kp, vp, b.table, b.q_start, b.kv_len, b.N, b.T, 2, 64, 16, b.n_pages, b.max_pages)
+        b.call()
+        torch.cuda.synchronize()
+        assert xs.device_status() == xs.XS_OK, xs.last_error()
+        assert not kp.any() and not vp.any()
+
+
+# ------------------------------------------------------------------ in a row
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("span", ((-1, 0, 0), (150, 0, 4)))
+def test_serving_loop_equals_whole_sequence(span):
+    """A prompt in chunks and then single tokens, each step turning q and k, appending and attending over the cache,
+    against rotary positions and windowed attention over the whole sequences at once."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    N, S, H, D, page = 2, 430, 4, 128, 16
+    steps = [200, 129, 90] + [1] * 11
+    assert sum(steps) == S
+    rng = np.random.default_rng(31)
+    (qb, _), (kb, _), (vb, _) = (bf16(rng, (N, S, H, D)) for _ in range(3))
+    ax = xs.RopeAxes.powers((D,), halves=True)
+    pos = torch.arange(S, dtype=torch.int32, device="cuda").view(1, S, 1)
+    q, k, v = to_dev(qb), to_dev(kb), to_dev(vb)
+    qr, kr, want = (guarded(q.numel()) for _ in range(3))
+    xs.rope(q, k, qr, kr, pos, N, S, H, H, D, 1, ax)
+    xs.attn_window(qr, kr, v, want, N, S, H, D, 1, D ** -0.5, *span)
+    max_pages = -(-S // page)
+    n_pages = N * max_pages
+    kp, vp = guarded(n_pages * page * H * D), guarded(n_pages * page * H * D)   # NaN to begin with
+    table = torch.randperm(n_pages, device="cuda").to(torch.int32).view(N, max_pages)
+    got = torch.zeros((N, S, H, D), dtype=torch.int16, device="cuda")
+    done = 0
+    for n_new in steps:
+        T = N * n_new
+        part = [x.view(N, S, H, D)[:, done:done + n_new].reshape(T, H, D).contiguous() for x in (q, k, v)]
+        at = pos[:, done:done + n_new].expand(N, n_new, 1).contiguous()
+        xs.rope(part[0], part[1], part[0], part[1], at, 1, T, H, H, D, 1, ax, pos_batches=1)
+        q_start = torch.arange(0, T + 1, n_new, dtype=torch.int32, device="cuda")
+        kv_len = torch.full((N,), done + n_new, dtype=torch.int32, device="cuda")
+        xs.cache_append(part[1], part[2], kp, vp, table, q_start, kv_len, N, T, H, D, page, n_pages, max_pages)
+        out = guarded(T * H * D)
+        ws = guarded(xs.attn_paged_workspace_size(N, T, H, H, D), torch.uint8)
+        xs.attn_paged(part[0], kp, vp, table, q_start, kv_len, out, N, T, H, H, D, page, n_pages, max_pages, D ** -0.5,
+                      *span, workspace=ws)
+        got[:, done:done + n_new] = out.view(N, n_new, H, D)
+        done += n_new
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    qv, kv_ = (values(from_dev(x).reshape(N, S, H, D)) for x in (qr, kr))
+    vv = values(vb)
+    seen = seen_mask(np.arange(S), S, *span)
+    for bits in (from_dev(got), from_dev(want).reshape(N, S, H, D)):
+        for n in range(N):
+            for h in range(H):
+                ref, bound = attend(qv[n, :, h], kv_[n, :, h], vv[n, :, h], seen, D ** -0.5)
+                check(bits[n, :, h], ref, bound, f"sequence {n} head {h}")
+
+
+# ------------------------------------------------------------------ refusals
+
+Q, KP, VP, TAB, QS, KL, O, W = (0x10000000 * i for i in range(1, 9))
+
+
+def test_paged_refusals():
+    import __graft_entry__
+    __graft_entry__.build()
+    import torch
+    import comm_comp_fusion_gb300 as xs
+
+    def attn(q=Q, kp=KP, tab=TAB, qs=QS, o=O, N=2, T=10, H=8, Hk=2, D=128, page=16, n_pages=50, max_pages=20, scale=0.1,
+             left=-1, right=0, sinks=0, ws=W, nb=1 << 27):
+        return xs.attn_paged(q, kp, VP, tab, qs, KL, o, N, T, H, Hk, D, page, n_pages, max_pages, scale, left, right,
+                             sinks, ws, nb, check=False)
+
+    def app(q=Q, kp=KP, tab=TAB, qs=QS, o=O, **kw):
+        a = dict(N=2, T=10, Hk=2, D=128, page=16, n_pages=50, max_pages=20)
+        a.update({n: x for n, x in kw.items() if n in a})
+        return xs.cache_append(q, o, kp, VP, tab, qs, KL, a["N"], a["T"], a["Hk"], a["D"], a["page"], a["n_pages"],
+                               a["max_pages"], check=False)
+
+    for f in (attn, app):
+        assert f(q=0) == xs.XS_ERR_NULL and f(tab=0) == xs.XS_ERR_NULL and f(qs=0) == xs.XS_ERR_NULL
+        assert f(N=-1) == xs.XS_ERR_SHAPE and f(T=-1) == xs.XS_ERR_SHAPE and f(Hk=0) == xs.XS_ERR_SHAPE
+        assert f(n_pages=0) == xs.XS_ERR_SHAPE and f(max_pages=0) == xs.XS_ERR_SHAPE
+        assert f(max_pages=1 << 27) == xs.XS_ERR_SHAPE and f(n_pages=2 ** 31 - 1, page=1024) == xs.XS_ERR_SHAPE
+        assert f(T=2 ** 31 - 1) == xs.XS_ERR_SHAPE and f(N=1 << 21) == xs.XS_ERR_SHAPE
+        assert f(D=256) == xs.XS_ERR_UNSUPPORTED and f(page=8) == xs.XS_ERR_UNSUPPORTED
+        assert f(page=48) == xs.XS_ERR_UNSUPPORTED and f(page=2048) == xs.XS_ERR_UNSUPPORTED
+        assert f(q=Q + 2) == xs.XS_ERR_ALIGN and f(kp=KP + 8) == xs.XS_ERR_ALIGN and f(tab=TAB + 2) == xs.XS_ERR_ALIGN
+        assert f(N=0) == xs.XS_OK and f(T=0) == xs.XS_OK
+        if not torch.cuda.is_available():
+            assert f() in (xs.XS_ERR_CUDA, xs.XS_ERR_UNSUPPORTED)
+    assert app(kp=Q) == xs.XS_ERR_ALIAS and app(kp=VP + 16) == xs.XS_ERR_ALIAS and app(tab=KP + 64) == xs.XS_ERR_ALIAS
+    assert attn(o=Q + 16) == xs.XS_ERR_ALIAS and attn(o=KP) == xs.XS_ERR_ALIAS and attn(tab=O) == xs.XS_ERR_ALIAS
+    assert attn(H=7) == xs.XS_ERR_SHAPE and attn(H=0) == xs.XS_ERR_SHAPE and attn(H=258) == xs.XS_ERR_UNSUPPORTED
+    assert attn(scale=-1.0) == xs.XS_ERR_SHAPE and attn(scale=float("inf")) == xs.XS_ERR_SHAPE
+    assert attn(left=-2) == xs.XS_ERR_SHAPE and attn(right=-9) == xs.XS_ERR_SHAPE and attn(sinks=-1) == xs.XS_ERR_SHAPE
+    assert attn(ws=None, nb=0) == xs.XS_ERR_NULL and attn(ws=None, nb=8) == xs.XS_ERR_WORKSPACE
+    assert attn(ws=W + 128) == xs.XS_ERR_WORKSPACE and attn(ws=O) == xs.XS_ERR_WORKSPACE
+    assert attn(ws=None, nb=0, N=0) == xs.XS_OK
+    for bad in ((-1, 4, 4, 2, 64), (1, 4, 5, 2, 64), (1, 4, 4, 0, 64), (1, 4, 4, 2, 80)):
+        with pytest.raises(xs.XsError):
+            xs.attn_paged_workspace_size(*bad)
+    assert xs.attn_paged_workspace_size(0, 4, 4, 2, 64) == 0
+    t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    pool, i = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    for a, p, tab in ((t[:, :1], pool, i), (t, pool.float(), i), (t, pool[:1], i), (t, pool, i.long())):
+        with pytest.raises(ValueError):
+            xs.attn_paged(a, p, pool, tab, i, i, t, 1, 4, 2, 2, 64, 16, 2, 1, 0.1)
+        with pytest.raises(ValueError):
+            xs.cache_append(a, t, p, pool, tab, i, i, 1, 4, 2, 64, 16, 2, 1)
+
+
+@pytest.mark.gpu
+def test_paged_small_workspace_and_host_memory_are_refused():
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    b = Batch([1], [20], 2, 1, 64, 16)
+    b.ws = b.ws[:4096]
+    assert b.call(check=False) == xs.XS_ERR_WORKSPACE
+    b = Batch([1], [20], 2, 1, 64, 16)
+    b.kv_len = b.kv_len.cpu()
+    assert b.call(check=False) == xs.XS_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert (from_dev(b.out) == 0xFFFF).all()
