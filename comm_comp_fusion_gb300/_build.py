@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libxs.so")
 ROOT = os.path.dirname(PKG)
 
 SOURCES = ["xs_attn_d128.cu", "xs_attn_f8.cu", "xs_attn_d256.cu", "xs_attn_d96.cu", "xs_attn_d64.cu", "xs_attn.cu", "xs_permute.cu", "xs_api.cpp", "xs_schedule.cpp",
-           "xs_noalloc.cu", "xs_burst.cu", "xs_rope.cu", "xs_cache.cu", "xs_span.cu", "xs_ops_api.cpp"]
+           "xs_noalloc.cu", "xs_burst.cu", "xs_rope.cu", "xs_cache.cu", "xs_span.cu", "xs_span_d128.cu", "xs_span_d96.cu",
+           "xs_span_d64.cu", "xs_ops_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,7 +53,7 @@ def _compile(src: str) -> tuple[str, str]:
 
 
 def check_attention_registers(ptxas_log: str) -> None:
-    """Every attn_fwd_kernel instance must report exactly 128 registers."""
+    """Every attn_fwd_kernel and span_attn_kernel instance must report exactly 128 registers."""
     current = None
     seen = 0
     for line in ptxas_log.splitlines():
@@ -61,7 +62,7 @@ def check_attention_registers(ptxas_log: str) -> None:
             current = m.group(1)
             continue
         m = re.search(r"Used (\d+) registers", line)
-        if m and current and "attn_fwd_kernel" in current:
+        if m and current and ("attn_fwd_kernel" in current or "span_attn_kernel" in current):
             seen += 1
             if int(m.group(1)) != 128:
                 raise RuntimeError(f"{current} uses {m.group(1)} registers; the setmaxnreg split needs 128")

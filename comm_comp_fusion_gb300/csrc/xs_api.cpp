@@ -509,6 +509,23 @@ int api_device(int *dev, int *num_sms) {
     return (int)st;
 }
 int api_device_pointer(const void *ptr, int dev, const char *name) { return (int)check_device_pointer(ptr, dev, name); }
+// Tensor map over a 4-D bf16 tensor, 128-byte swizzle; rows outside it read as zeros.
+int api_tile_map(CUtensorMap *m, const void *ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                 const uint32_t (&box)[4], const char *name) {
+    EncodeTiledFn enc;
+    const xs_status st = get_encoder(&enc);
+    if (st) return (int)st;
+    cuuint64_t d[4], sr[3];
+    cuuint32_t b[4];
+    for (int i = 0; i < 4; ++i) d[i] = dims[i], b[i] = box[i];
+    for (int i = 0; i < 3; ++i) sr[i] = strides[i];
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), d, sr, b, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return (int)fail(XS_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, (int)r);
+    return 0;
+}
 int api_shape(int B, int S, int H, int D, int P, size_t *bytes) { return (int)check_shape(B, S, H, D, P, true, bytes); }
 bool api_overlaps(const void *a, size_t na, const void *b, size_t nb) { return overlaps(a, na, b, nb); }
 }  // namespace xs

@@ -168,18 +168,35 @@ struct AppendParams {
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 
 // ------------------------------------------------------------ window and paged attention
+struct SpanPieces;
 struct SpanParams {
-    const uint16_t *q, *k, *v;  // k, v: the page pools when paged
     uint16_t *out;
     const int *table, *q_start, *kv_len;  // table NULL: whole sequences, head-partitioned
     int N, T, H, Hk, G;         // whole sequences: T = B * S rows of H heads
     int page, n_pages, max_pages;
     int B, S, P, Hl, Sl, head_out;  // whole sequences only
-    int left, right, sinks;     // at most 2^30 each
+    int left, right, sinks;     // at most 2^29 each
     float scale_log2;
+    int tile_tok;               // tokens of a query tile: 128 / G
+    int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
+    int min_steps;              // fewest steps that a CTA is started for
+    float *rec;                 // workspace: 2 records a CTA (Rec<D>), then a SpanPieces a CTA; NULL: whole items
+    SpanPieces *pieces;
 };
+// TMA maps: q by query tile, k and v by 128-key tile or page (see xs_ops_api.cpp).
+struct SpanMaps {
+    CUtensorMap q, k, v;
+};
+// Workspace bytes, and its parts' places in p.
 size_t span_workspace_bytes(int D, int num_sms);
-cudaError_t launch_span(int D, const SpanParams &p, int num_sms, cudaStream_t stream);
+void span_workspace_parts(void *ws, int D, int num_sms, SpanParams *p);
+cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int num_sms, cudaStream_t stream);
+#define XS_DECLARE_SPAN_ENTRY(D)                                                                                \
+    cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream);     \
+    cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear);
+XS_DECLARE_SPAN_ENTRY(64)
+XS_DECLARE_SPAN_ENTRY(96)
+XS_DECLARE_SPAN_ENTRY(128)
 
 // ------------------------------------------------------------ host helpers of the C ABI (xs_api.cpp)
 // Each records the thread's last error and returns a status (0: fine).
@@ -187,6 +204,8 @@ int api_fail(int status, const char *fmt, ...);
 int api_cuda_error(const char *what, cudaError_t e);
 int api_device(int *dev, int *num_sms);
 int api_device_pointer(const void *ptr, int dev, const char *name);
+int api_tile_map(CUtensorMap *m, const void *ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                 const uint32_t (&box)[4], const char *name);
 int api_shape(int B, int S, int H, int D, int P, size_t *bytes);
 bool api_overlaps(const void *a, size_t na, const void *b, size_t nb);
 

@@ -56,7 +56,7 @@ uint64_t turns_fraction(double f) {
 int span_limits(int left, int right, int sinks, SpanParams *p) {
     if (left < -1 || right < -1) return api_fail(XS_ERR_SHAPE, "left and right must be >= 0, or -1 for no limit");
     if (sinks < 0) return api_fail(XS_ERR_SHAPE, "sinks must be >= 0");
-    const int far = 1 << 30;  // past every place
+    const int far = 1 << 29;  // past every place
     p->left = left < 0 || left > far ? far : left;
     p->right = right < 0 || right > far ? far : right;
     p->sinks = sinks > far ? far : sinks;
@@ -84,7 +84,7 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     int st = api_shape(B, S, H, D, P, &bytes);
     if (st) return st;
     if (D == 256) return api_fail(XS_ERR_UNSUPPORTED, "windowed attention takes D = 64, 96 or 128 (got D=256)");
-    if (S > (1 << 30)) return api_fail(XS_ERR_SHAPE, "S=%d exceeds 2^30", S);
+    if (S > (1 << 24)) return api_fail(XS_ERR_SHAPE, "S=%d exceeds 2^24", S);
     if ((st = check_scale(scale))) return st;
     SpanParams p{};
     if ((st = span_limits(left, right, sinks, &p))) return st;
@@ -103,11 +103,8 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
             return api_fail(XS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
         if ((st = api_device_pointer(ws, dev, "workspace"))) return st;
     }
-    p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint16_t *>(k);
-    p.v = static_cast<const uint16_t *>(v);
     p.out = static_cast<uint16_t *>(out);
-    p.T = B * S;
+    p.T = S;
     p.H = H;
     p.G = 1;
     p.B = B;
@@ -117,7 +114,19 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     p.Sl = S / P;
     p.head_out = a2a ? 0 : 1;
     p.scale_log2 = scale_log2(scale);
-    const cudaError_t e = launch_span(D, p, sms, static_cast<cudaStream_t>(stream));
+    p.tile_tok = 128;
+    p.heads = B * H;
+    p.n_pairs = (S + 255) / 256;
+    if (ws) span_workspace_parts(ws, D, sms, &p);
+    SpanMaps maps;
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.Hl, (uint64_t)S, (uint64_t)P * B};
+    const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.Hl * D * 2, (uint64_t)S * p.Hl * D * 2};
+    const uint32_t box[4] = {64, 1, 128, 1};
+    if ((st = api_tile_map(&maps.q, q, dims, strides, box, "q")) ||
+        (st = api_tile_map(&maps.k, k, dims, strides, box, "k")) ||
+        (st = api_tile_map(&maps.v, v, dims, strides, box, "v")))
+        return st;
+    const cudaError_t e = launch_span(D, maps, p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? (int)XS_OK : api_cuda_error("windowed attention launch", e);
 }
 
@@ -130,12 +139,13 @@ int check_cache(int N, int T, int Hk, int D, int page, int n_pages, int max_page
         return api_fail(XS_ERR_UNSUPPORTED, "the paged cache takes D = 64, 96 or 128 (got D=%d)", D);
     if (page < 16 || page > 1024 || (page & (page - 1)))
         return api_fail(XS_ERR_UNSUPPORTED, "page=%d is not a power of two from 16 to 1024", page);
-    if ((long long)max_pages * page > (1ll << 30))
-        return api_fail(XS_ERR_SHAPE, "max_pages * page = %lld exceeds 2^30 keys", (long long)max_pages * page);
+    if ((long long)max_pages * page > (1ll << 29))
+        return api_fail(XS_ERR_SHAPE, "max_pages * page = %lld exceeds 2^29 keys", (long long)max_pages * page);
     const unsigned long long rows = (unsigned long long)n_pages * page;
     if (Hk > (1 << 16) || rows * (unsigned long long)Hk * D * 2 >= (1ull << 40))
         return api_fail(XS_ERR_SHAPE, "a pool of %d pages exceeds 2^40 bytes", n_pages);
-    if (N > (1 << 20)) return api_fail(XS_ERR_SHAPE, "N=%d exceeds 2^20 sequences", N);
+    if (T > (1 << 29)) return api_fail(XS_ERR_SHAPE, "T=%d exceeds 2^29 rows", T);
+    if (N > (1 << 16)) return api_fail(XS_ERR_SHAPE, "N=%d exceeds 65536 sequences", N);
     *pool = (size_t)rows * Hk * D * 2;
     *table = (size_t)N * max_pages * sizeof(int);
     return 0;
@@ -334,9 +344,6 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
         return (xs_status)api_fail(XS_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed",
                                    workspace_bytes, need);
     if ((st = api_device_pointer(workspace, dev, "workspace"))) return (xs_status)st;
-    p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint16_t *>(k_pages);
-    p.v = static_cast<const uint16_t *>(v_pages);
     p.out = static_cast<uint16_t *>(out);
     p.table = page_table;
     p.q_start = q_start;
@@ -350,7 +357,22 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
     p.n_pages = n_pages;
     p.max_pages = max_pages;
     p.scale_log2 = scale_log2(scale);
-    const cudaError_t e = launch_span(D, p, sms, static_cast<cudaStream_t>(stream));
+    p.tile_tok = 128 / p.G;
+    p.heads = Hk;
+    span_workspace_parts(workspace, D, sms, &p);
+    SpanMaps maps;
+    const uint64_t d = (uint64_t)D * 2;
+    const uint64_t q_dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)Hk, (uint64_t)T};
+    const uint64_t q_strides[3] = {d, p.G * d, H * d};
+    const uint32_t q_box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.tile_tok};
+    const uint64_t kv_dims[4] = {(uint64_t)D, (uint64_t)Hk, (uint64_t)page, (uint64_t)n_pages};
+    const uint64_t kv_strides[3] = {d, Hk * d, page * Hk * d};
+    const uint32_t kv_box[4] = {64, 1, (uint32_t)(page < 128 ? page : 128), 1};
+    if ((st = api_tile_map(&maps.q, q, q_dims, q_strides, q_box, "q")) ||
+        (st = api_tile_map(&maps.k, k_pages, kv_dims, kv_strides, kv_box, "k_pages")) ||
+        (st = api_tile_map(&maps.v, v_pages, kv_dims, kv_strides, kv_box, "v_pages")))
+        return (xs_status)st;
+    const cudaError_t e = launch_span(D, maps, p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : (xs_status)api_cuda_error("paged attention launch", e);
 }
 

@@ -1,0 +1,1028 @@
+// xs_span_kernel.cuh -- attention over a span of keys per token on the tensor
+// cores: a sliding window with sinks over whole sequences (xs_attn_window), and
+// chunks of new tokens over a paged cache (xs_attn_paged, PAGED).
+//
+// Mathematics. The token at place i sees the key at place j iff
+//   j <= i + right  and  (j >= i - left  or  j < sinks),
+// and o = sum_j p_j v_j / sum_j p_j, p_j = 2^(s_j scale log2(e) - m) over the keys
+// it sees; a token that sees none gets zeros. S = Q K^T and P V run on tcgen05
+// with fp32 accumulators in tensor memory; row maxima, sums and O stay in fp32;
+// P is rounded to bf16 for the product with V (its rounding, 2^-9 relative on
+// average per weight, is below the output's own), the sums use the unrounded p.
+//
+// Rows. A query tile is 128 rows: 128 tokens of one head, or, with G query heads
+// per key head, floor(128 / G) tokens x G heads, so that the heads of a group
+// share the K/V tiles they read. An item is one key head of one sequence and
+// two query tiles; it walks the 128-key tiles that any of its tokens sees (first
+// those of the sinks, then the window's). Keys outside a row's own span are
+// masked in the tiles where some row has any.
+//   * Two tiles (pair): each K/V tile is used by both, one tile's softmax running
+//     under the other's MMAs.
+//   * One tile (dual; single new tokens and the last rows of a chunk): the even
+//     and the odd K/V tiles form two chains with an O of their own each, which
+//     the epilogue adds up. A chain's step is a long dependent sequence (MMA,
+//     softmax, MMA), so two of them are what keeps K/V streaming.
+//
+// Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
+// ordered by sequence, head and query rows, and each CTA takes an equal,
+// contiguous part. Lengths are read on the device: every CTA sums the steps per
+// sequence and finds its part by itself (span_schedule), so the call can be
+// captured and replayed with other lengths. An item that a part's border cuts
+// is computed in pieces; each piece writes its unnormalised O, row maxima and
+// sums to the workspace, and span_merge_kernel adds them up in piece order (no
+// atomics: the result is the same every time).
+//
+// Roles of the 512 threads (registers 48 / 176 / 176 / 112 a thread):
+//   warp 0      TMA producer: Q tiles, then K and V tiles into a 4-slot ring. Pages
+//               shorter than a tile take one box each, issued by as many lanes;
+//               page numbers are fetched three tiles ahead. Pages that no token
+//               sees are not read (their box lies outside the pool: zeros).
+//   warp 1      MMA issuer
+//   warp 2      tensor-memory allocator
+//   warp 3      (PAGED) zeroes the V rows behind the last key, which no one has
+//               written: a weight of 0 times NaN would still be NaN
+//   warps 4-11  softmax, one warpgroup per tile or chain, one thread per row
+//   warps 12-15 epilogue
+#pragma once
+
+#include "xs_attn_kernel.cuh"
+
+namespace xs {
+
+enum : int { BFIX_ASK = 26, BFIX_DONE = 27 };  // the issuer asks warp 3 to clear a V tile's end, and its answer
+enum SpanSite : uint32_t { kSiteFix = 13 };
+
+template <int D> struct SpanCfg : Cfg<D> {
+    using C = Cfg<D>;
+    static constexpr uint32_t kOffSched = C::kSmemUsed;  // SpanSched
+    static constexpr uint32_t kSmemAlloc = kOffSched + 64 + 1024;
+    static_assert(kSmemAlloc <= 232448, "shared memory budget");
+};
+
+// One CTA's part of the steps, found by span_schedule.
+struct SpanSched {
+    long long total, rem;  // steps of the call, of this CTA
+    int ctas;              // CTAs that share them
+    int seq, head, pair, j;
+};
+
+constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory
+
+struct SpanItem {
+    int ntok;    // tokens of the item's tiles
+    int tok0;    // first of them among the sequence's new tokens
+    int pos0;    // its place
+    int ns, w0;  // K/V tiles: 0 .. ns - 1, then w0, w0 + 1, ...
+    int n;       // steps
+    bool dual;
+    __device__ __forceinline__ int tile(int x) const { return x < ns ? x : w0 + x - ns; }
+};
+
+__device__ __forceinline__ SpanItem span_item(const SpanParams &p, int q_len, int keys, int pair) {
+    SpanItem it;
+    it.tok0 = pair * 2 * p.tile_tok;
+    it.ntok = min(2 * p.tile_tok, q_len - it.tok0);
+    it.pos0 = keys - q_len + it.tok0;
+    it.dual = it.ntok <= p.tile_tok;
+    const int hi = min(keys - 1, it.pos0 + it.ntok - 1 + p.right);
+    const int lo = max(0, it.pos0 - p.left) >> 7;
+    if (hi < 0) {  // no key at all: one step, fully masked
+        it.ns = it.w0 = 0;
+        it.n = 1;
+    } else {
+        it.ns = min((min(p.sinks, hi + 1) + 127) >> 7, lo);
+        it.w0 = lo;
+        it.n = it.ns + (hi >> 7) - lo + 1;
+    }
+    return it;
+}
+
+// New tokens and keys of a sequence, cut to what the packed rows and the table hold.
+template <bool PAGED>
+__device__ __forceinline__ void span_lengths(const SpanParams &p, int seq, int &q0, int &q_len, int &keys) {
+    if (!PAGED) {
+        q0 = 0;
+        q_len = keys = p.S;
+        return;
+    }
+    q0 = min(max(p.q_start[seq], 0), p.T);
+    q_len = max(0, min(max(p.q_start[seq + 1], 0), p.T) - q0);
+    keys = min(max(p.kv_len[seq], 0), p.max_pages * p.page);
+}
+
+__device__ __forceinline__ int span_pairs(const SpanParams &p, int q_len) {
+    return (q_len + 2 * p.tile_tok - 1) / (2 * p.tile_tok);
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
+// is a sequence (all its heads and query rows) or, for whole sequences, which
+// are all alike, a query tile pair.
+template <bool PAGED>
+__device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane) {
+    const int g = ch * 32 + lane;
+    if (!PAGED) return g < p.n_pairs ? (long long)span_item(p, p.S, p.S, g).n : 0ll;
+    int q0 = 0, q_len = 0, keys = 0;
+    if (g < p.N) span_lengths<true>(p, g, q0, q_len, keys);
+    const int pairs = span_pairs(p, q_len);
+    long long u = pairs == 1 ? (long long)span_item(p, q_len, keys, 0).n * p.heads : 0ll;
+    uint32_t todo = __ballot_sync(0xffffffffu, pairs > 1);  // these the whole warp sums up, one after the other
+    while (todo) {
+        const int src = __ffs((int)todo) - 1;
+        todo &= todo - 1;
+        const int ql = __shfl_sync(0xffffffffu, q_len, src), kl = __shfl_sync(0xffffffffu, keys, src);
+        const int np = span_pairs(p, ql);
+        long long s = 0;
+        for (int i = lane; i < np; i += 32) s += span_item(p, ql, kl, i).n;
+        s = warp_sum(s);
+        if (lane == src) u = s * p.heads;
+    }
+    return u;
+}
+
+// First step of CTA c's part, and the CTA whose part holds step u.
+__device__ __forceinline__ long long span_first(const SpanSched &s, int c) { return c * s.total / s.ctas; }
+__device__ __forceinline__ int span_cta_of(const SpanSched &s, long long u) {
+    return (int)(((u + 1) * s.ctas - 1) / s.total);
+}
+
+// In a run of 32 values (one per lane, in order) that start at step `base`, the
+// lane that holds step u, and the step its value starts at; base moves past the
+// run. -1: behind the run.
+__device__ __forceinline__ int span_locate(long long v, long long u, long long &base, long long &at, int lane) {
+    long long incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > u);
+    const int l = past ? __ffs((int)past) - 1 : -1;
+    at = base + __shfl_sync(0xffffffffu, incl - v, l < 0 ? 0 : l);
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    return l;
+}
+
+// Every CTA: the call's steps, how many CTAs share them and where this CTA's part
+// starts. `scratch` holds kSpanMaxChunks sums. Called by all threads, leaves
+// them synchronised.
+template <bool PAGED>
+__device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *out, long long *scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int groups = PAGED ? p.N : p.n_pairs, chunks = (groups + 31) / 32;
+    for (int ch = warp; ch < chunks; ch += warps) {
+        const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
+        if (lane == 0) scratch[ch] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long sum = 0;
+        for (int ch = lane; ch < chunks; ch += 32) sum += scratch[ch];
+        sum = warp_sum(sum);
+        SpanSched s;
+        s.total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
+        s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total / p.min_steps));
+        const int c = (int)blockIdx.x;
+        s.rem = 0;
+        s.seq = s.head = s.pair = s.j = 0;
+        if (c < s.ctas && s.total > 0) {
+            const long long u0 = span_first(s, c);
+            s.rem = span_first(s, c + 1) - u0;
+            long long u = u0, base = 0, at = 0;
+            if (!PAGED) {
+                s.head = (int)(u0 / sum);
+                u = u0 - s.head * sum;
+            }
+            int l = -1, ch = 0;
+            for (; l < 0 && ch < chunks; ch += 32)
+                l = span_locate(ch + lane < chunks ? scratch[ch + lane] : 0ll, u, base, at, lane);
+            ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
+            base = at;
+            l = span_locate(span_group_steps<PAGED>(p, ch, lane), u, base, at, lane);
+            if (!PAGED) {
+                s.pair = ch * 32 + l;
+                s.j = (int)(u - at);
+            } else {
+                s.seq = ch * 32 + l;
+                int q0, q_len, keys;
+                span_lengths<true>(p, s.seq, q0, q_len, keys);
+                const int np = span_pairs(p, q_len);
+                long long per_head = 0;
+                for (int i = lane; i < np; i += 32) per_head += span_item(p, q_len, keys, i).n;
+                per_head = warp_sum(per_head);
+                u -= at;
+                s.head = (int)(u / per_head);
+                u -= s.head * per_head;
+                base = 0;
+                l = -1;
+                int i = 0;
+                for (; l < 0 && i < np; i += 32)
+                    l = span_locate(i + lane < np ? (long long)span_item(p, q_len, keys, i + lane).n : 0ll, u, base, at, lane);
+                s.pair = i - 32 + l;
+                s.j = (int)(u - at);
+            }
+        }
+        if (lane == 0) *out = s;
+    }
+    __syncthreads();
+}
+
+// A role's walk through its CTA's part, one stretch (segment) of an item at a time.
+struct SpanSeg {
+    int j0, j1;  // steps of the item
+    int slot;    // workspace record of the segment if it is a piece (see span_merge_kernel)
+    int seq, head;
+    int q0, keys;  // of the sequence: its first packed row, its keys
+};
+struct SpanWalk {
+    long long rem;  // steps left (whole items: items left)
+    int seq, head, pair, j;
+    int q0, q_len, keys;
+    bool first;
+};
+template <bool PAGED>
+__device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
+    w.first = true;
+    w.seq = w.j = 0;
+    if (PAGED || p.rec) {
+        w.seq = s.seq;
+        w.j = s.j;
+        w.rem = s.rem;
+        w.head = s.head;
+        w.pair = s.pair;
+    } else {  // whole items, dealt round
+        const long long items = (long long)p.heads * p.n_pairs;
+        w.rem = ((long long)items - blockIdx.x + gridDim.x - 1) / gridDim.x;
+        w.head = (int)(blockIdx.x / p.n_pairs);
+        w.pair = (int)(blockIdx.x % p.n_pairs);
+    }
+    if (w.rem > 0) span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
+}
+template <bool PAGED>
+__device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, SpanSeg &g, SpanItem &it) {
+    if (w.rem <= 0) return false;
+    if (PAGED)
+        while (w.q_len == 0) {
+            if (++w.seq >= p.N) return false;
+            span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
+        }
+    it = span_item(p, w.q_len, w.keys, w.pair);
+    g.seq = w.seq;
+    g.head = w.head;
+    g.q0 = w.q0;
+    g.keys = w.keys;
+    g.slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
+    w.first = false;
+    if (PAGED || p.rec) {
+        g.j0 = w.j;
+        const int take = (int)min((long long)(it.n - w.j), w.rem);
+        g.j1 = w.j + take;
+        w.rem -= take;
+        w.j = g.j1;
+        if (w.j == it.n) {
+            w.j = 0;
+            if (++w.pair * 2 * p.tile_tok >= w.q_len) {
+                w.pair = 0;
+                if (++w.head == p.heads) {
+                    w.head = 0;
+                    w.q_len = PAGED ? 0 : w.q_len;  // the next sequence is looked up when it is needed
+                }
+            }
+        }
+    } else {
+        g.j0 = 0;
+        g.j1 = it.n;
+        --w.rem;
+        const long long item = (long long)w.head * p.n_pairs + w.pair + gridDim.x;
+        w.head = (int)(item / p.n_pairs);
+        w.pair = (int)(item - (long long)w.head * p.n_pairs);
+    }
+    return true;
+}
+
+// The first row of the segment's last K/V tile that no key has written, if its
+// box holds keys and such rows; -1 otherwise. (Boxes without keys are zeros.)
+__device__ __forceinline__ int span_fix_rows(const SpanSeg &g, const SpanItem &it, int box) {
+    const bool cut = g.j1 == it.n && it.tile(it.n - 1) == g.keys >> 7 && (g.keys & (box - 1));
+    return cut ? g.keys & 127 : -1;
+}
+
+// Element offset of the output row of token `tok` (of the sequence's new tokens,
+// packed rows from q0) and query head g of the group.
+template <int D, bool PAGED>
+__device__ __forceinline__ int64_t span_out_offset(const SpanParams &p, int head, int64_t q0, int tok, int g) {
+    if (PAGED) return ((q0 + tok) * p.H + (int64_t)head * p.G + g) * D;
+    const int hl = head % p.Hl, rb = head / p.Hl;
+    if (p.head_out) return (((int64_t)rb * p.S + tok) * p.Hl + hl) * D;
+    const int b = rb % p.B, r = rb / p.B;
+    const int rd = tok / p.Sl;
+    return ((((int64_t)rd * p.B + b) * p.Sl + (tok - rd * p.Sl)) * p.H + r * p.Hl + hl) * D;
+}
+
+// Bits of the 32 columns from col0 (relative to the tile) that a row sees: columns
+// a .. b, and those below s up to b.
+__device__ __forceinline__ uint32_t span_mask_word(int a, int b, int s, int col0) {
+    a -= col0;
+    b -= col0;
+    s -= col0;
+    const uint32_t le = b < 0 ? 0u : b >= 31 ? ~0u : (2u << b) - 1u;
+    const uint32_t ge = a <= 0 ? ~0u : a > 31 ? 0u : ~0u << a;
+    const uint32_t lt = s <= 0 ? 0u : s > 31 ? ~0u : (1u << s) - 1u;
+    return le & (ge | lt);
+}
+
+// Written by each CTA for span_merge_kernel: the item whose first piece is the
+// CTA's last segment (pieces 0: none).
+struct SpanPieces {
+    int pieces, slot, seq, head, tok0, ntok, q0, unused;
+};
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(512, 1)
+    span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
+    using C = SpanCfg<D>;
+    using R = Rec<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *sm = smem_raw + (base - raw);
+    const uint32_t sQ = base + C::kOffQ, sKV = base + C::kOffKV, sStage = base + C::kOffStage;
+    const uint32_t sBar = base + C::kOffBar;
+    float *row_ml = reinterpret_cast<float *>(sm + C::kOffL);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
+    volatile uint32_t *abort_flag = misc + 1;
+    SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSched);
+#define BAR(i) (sBar + 8u * (uint32_t)(i))
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(BAR(BQ_FULL + t), 1);
+            mbar_init(BAR(BQ_EMPTY + t), 1);
+            mbar_init(BAR(BS_FULL + t), 1);
+            mbar_init(BAR(BP_FULL + t), 4);
+            mbar_init(BAR(BO_FINAL + t), 1);
+            mbar_init(BAR(BO_FREE + t), 4);
+            mbar_init(BAR(BL_FULL + t), 4);
+            mbar_init(BAR(BL_EMPTY + t), 4);
+        }
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(BAR(BKV_FULL + s), 1);
+            mbar_init(BAR(BKV_EMPTY + s), 1);
+        }
+        mbar_init(BAR(B_DRAIN), 1);
+        mbar_init(BAR(BFIX_ASK), 1);
+        mbar_init(BAR(BFIX_DONE), 1);
+        misc[1] = 0u;
+        fence_mbar_init();
+        prefetch_tmap(&tm.q);
+        prefetch_tmap(&tm.k);
+        prefetch_tmap(&tm.v);
+    }
+    if (warp == 2) {
+        tmem_alloc(smem_u32(misc), C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (PAGED || p.rec)
+        span_schedule<PAGED>(p, sched, reinterpret_cast<long long *>(sm + C::kOffStage));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const int wg = warp >> 2;
+
+    if (wg == 0) {
+        setmaxnreg_dec<48>();
+        if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            uint32_t kv_it = 0, q_it[2] = {0u, 0u};
+            bool ok = true;
+            SpanWalk w;
+            span_walk_init<PAGED>(p, *sched, w);
+            SpanSeg g;
+            SpanItem it;
+            const int box = PAGED ? min(p.page, 128) : 128;  // rows of a box
+            while (ok && span_next<PAGED>(p, w, g, it)) {
+                for (int t = 0; t < (it.dual ? 1 : 2) && ok; ++t) {
+                    ok = warp_bwait(BAR(BQ_EMPTY + t), (q_it[t] & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+                    if (!ok) break;
+                    ++q_it[t];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(BAR(BQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
+                        const int tok = it.tok0 + t * p.tile_tok;
+#pragma unroll
+                        for (int db = 0; db < C::kNDB; ++db) {
+                            const uint32_t dst = sQ + t * C::kTile + db * C::kBlk;
+                            if (PAGED)
+                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, 0, g.head, g.q0 + tok);
+                            else
+                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, g.head % p.Hl, tok, g.head / p.Hl);
+                        }
+                    }
+                }
+                if (!ok) break;
+                // page of this lane's box of step x's tile; n_pages (outside the pool)
+                // where no token of the item sees any of its keys
+                const int lo = max(0, it.pos0 - p.left), hi = min(g.keys - 1, it.pos0 + it.ntok - 1 + p.right);
+                const int *table = PAGED ? p.table + (int64_t)g.seq * p.max_pages : nullptr;
+                auto page_of = [&](int x) -> int {
+                    if (!PAGED || lane * box >= 128 || x >= g.j1) return 0;
+                    const int k0 = it.tile(x) * 128 + lane * box;
+                    if (k0 > hi || (k0 + box <= lo && k0 >= p.sinks)) return p.n_pages;
+                    const int id = table[k0 / p.page];
+                    return id < 0 || id >= p.n_pages ? p.n_pages : id;
+                };
+                auto load_tile = [&](const CUtensorMap *m, int x, int page) {
+                    const uint32_t slot = kv_it % C::kSlots, ph = (kv_it / C::kSlots) & 1u;
+                    ok = warp_bwait(BAR(BKV_EMPTY + slot), ph ^ 1u, abort_flag, kSiteLoadKV);
+                    if (!ok) return;
+                    ++kv_it;
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(BKV_FULL + slot), C::kTile);
+                    __syncwarp();
+                    const int tile = it.tile(x);
+                    if (PAGED) {
+                        if (lane * box < 128) {
+                            const int row = (tile * 128 + lane * box) & (p.page - 1);
+                            const uint32_t dst = sKV + slot * C::kTile + (uint32_t)(lane * box) * 128u;
+#pragma unroll
+                            for (int db = 0; db < C::kNDB; ++db)
+                                tma_load_4d(dst + db * C::kBlk, m, BAR(BKV_FULL + slot), db * 64, g.head, row, page);
+                        }
+                    } else if (lane < C::kNDB) {
+                        tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(BKV_FULL + slot), lane * 64,
+                                    g.head % p.Hl, tile * 128, g.head / p.Hl);
+                    }
+                };
+                int pg0 = page_of(g.j0), pg1 = page_of(g.j0 + 1), pg2 = page_of(g.j0 + 2);
+                load_tile(&tm.k, g.j0, pg0);
+                if (ok && it.dual && g.j0 + 1 < g.j1) load_tile(&tm.k, g.j0 + 1, pg1);
+                for (int x = g.j0; ok && x < g.j1; ++x) {
+                    const int pg3 = page_of(x + 3);
+                    load_tile(&tm.v, x, pg0);
+                    const int la = it.dual ? 2 : 1;
+                    if (ok && x + la < g.j1) load_tile(&tm.k, x + la, it.dual ? pg2 : pg1);
+                    pg0 = pg1;
+                    pg1 = pg2;
+                    pg2 = pg3;
+                }
+            }
+            if (!ok) {  // let copies already in flight land before the CTA exits
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
+            }
+        } else if (PAGED && warp == 3) {
+            // ------------------------------------ V rows behind the last key: zeros
+            uint32_t kv_it = 0, fph = 0;
+            bool ok = true;
+            const int box = min(p.page, 128);
+            SpanWalk w;
+            span_walk_init<PAGED>(p, *sched, w);
+            SpanSeg g;
+            SpanItem it;
+            while (ok && span_next<PAGED>(p, w, g, it)) {
+                kv_it += 2u * (uint32_t)(g.j1 - g.j0);
+                const int rows = span_fix_rows(g, it, box);
+                if (rows < 0) continue;
+                const uint32_t slot = (kv_it - 1u) % C::kSlots;  // the segment's last V tile
+                ok = warp_bwait(BAR(BFIX_ASK), fph, abort_flag, kSiteFix);  // the tile is in
+                if (!ok) break;
+                fph ^= 1u;
+                for (int r = rows * 8 + lane; r < ((rows + box - 1) / box * box) * 8; r += 32)
+#pragma unroll
+                    for (int db = 0; db < C::kNDB; ++db)
+                        st_shared_v4(sKV + slot * C::kTile + db * C::kBlk + (uint32_t)r * 16u, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(BFIX_DONE));
+            }
+        } else if (warp == 1 && lane == 0) {
+            // -------------------------------------------------------- MMA issuer
+            constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0), idO = idesc_bf16_f32(128, D, 1);
+            const uint64_t dK = sdesc_sw128(0, 16, 1024);       // K-major, 128-byte rows
+            const uint64_t dV = sdesc_sw128(0, C::kBlk, 1024);  // MN-major V, 64-column blocks kBlk apart
+            auto issue_S = [&](int t, int qt, uint32_t slot) {
+                const uint64_t qa = dK + (opaque(sQ + qt * C::kTile) >> 4);
+                const uint64_t ka = dK + (opaque(sKV + slot * C::kTile) >> 4);
+                const uint32_t d = opaque(tmem + C::colS(t));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4;
+                    tc_mma_ss(d, qa + off, ka + off, idS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(BAR(BS_FULL + t));
+            };
+            auto issue_PV = [&](int t, uint32_t slot, bool acc) {
+                const uint64_t va = dV + (opaque(sKV + slot * C::kTile) >> 4);
+                const uint32_t d = opaque(tmem + C::colO(t)), a = opaque(tmem + C::colS(t));
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_ts(d, a + kk * 8, va + (kk * 2048 >> 4), idO, (acc || kk > 0) ? 1u : 0u);
+            };
+            uint32_t kv_it = 0, nit = 0, q_it0 = 0, q_it1 = 0, pph0 = 0, pph1 = 0, fph = 0;
+            bool ok = true;
+            SpanWalk w;
+            span_walk_init<PAGED>(p, *sched, w);
+            SpanSeg g;
+            SpanItem it;
+            const int box = PAGED ? min(p.page, 128) : 128;
+            auto wait_kv = [&](uint32_t &slot) {
+                slot = kv_it % C::kSlots;
+                ok = ok && bwait(BAR(BKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
+                ++kv_it;
+            };
+            for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
+                const int n = g.j1 - g.j0;
+                const bool fix = PAGED && span_fix_rows(g, it, box) >= 0;
+                ok = bwait(BAR(BQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
+                if (ok && !it.dual) ok = bwait(BAR(BQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
+                uint32_t ks, vs;
+                wait_kv(ks);
+                if (!ok) break;
+                tc_fence_after();
+                issue_S(0, 0, ks);
+                if (!it.dual) {
+                    issue_S(1, 1, ks);
+                } else if (n > 1) {
+                    tc_commit(BAR(BKV_EMPTY + ks));
+                    wait_kv(ks);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_S(1, 0, ks);
+                }
+                tc_commit(BAR(BKV_EMPTY + ks));
+                if (n <= (it.dual ? 2 : 1)) {
+                    tc_commit(BAR(BQ_EMPTY + 0));
+                    if (!it.dual) tc_commit(BAR(BQ_EMPTY + 1));
+                }
+                for (int x = 0; x < n; ++x) {
+                    wait_kv(vs);
+                    if (ok && fix && x == n - 1) {
+                        mbar_arrive(BAR(BFIX_ASK));
+                        ok = bwait(BAR(BFIX_DONE), fph, abort_flag, kSiteFix);
+                        fph ^= 1u;
+                    }
+                    if (!ok) break;
+                    if (it.dual) {
+                        const int t = x & 1;
+                        ok = bwait(BAR(BP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
+                        if (ok && x < 2) ok = bwait(BAR(BO_FREE + t), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                        if (!ok) break;
+                        if (t)
+                            pph1 ^= 1u;
+                        else
+                            pph0 ^= 1u;
+                        tc_fence_after();
+                        issue_PV(t, vs, x >= 2);
+                        tc_commit(BAR(BKV_EMPTY + vs));
+                        if (x + 2 >= n) tc_commit(BAR(BO_FINAL + t));
+                        if (x + 2 < n) {
+                            wait_kv(ks);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_S(t, 0, ks);
+                            tc_commit(BAR(BKV_EMPTY + ks));
+                            if (x + 3 == n) tc_commit(BAR(BQ_EMPTY + 0));
+                        }
+                        continue;
+                    }
+                    const bool more = x + 1 < n;
+                    ok = bwait(BAR(BP_FULL + 0), pph0, abort_flag, kSiteMmaP);
+                    if (ok && x == 0) ok = bwait(BAR(BO_FREE + 0), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                    if (!ok) break;
+                    pph0 ^= 1u;
+                    tc_fence_after();
+                    issue_PV(0, vs, x > 0);
+                    if (!more) tc_commit(BAR(BO_FINAL + 0));
+                    if (more) {
+                        wait_kv(ks);
+                        if (!ok) break;
+                        issue_S(0, 0, ks);
+                    }
+                    ok = bwait(BAR(BP_FULL + 1), pph1, abort_flag, kSiteMmaP);
+                    if (ok && x == 0) ok = bwait(BAR(BO_FREE + 1), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                    if (!ok) break;
+                    pph1 ^= 1u;
+                    tc_fence_after();
+                    issue_PV(1, vs, x > 0);
+                    tc_commit(BAR(BKV_EMPTY + vs));
+                    if (!more) tc_commit(BAR(BO_FINAL + 1));
+                    if (more) {
+                        issue_S(1, 1, ks);
+                        tc_commit(BAR(BKV_EMPTY + ks));
+                        if (x + 2 == n) {
+                            tc_commit(BAR(BQ_EMPTY + 0));
+                            tc_commit(BAR(BQ_EMPTY + 1));
+                        }
+                    }
+                }
+                if (ok && it.dual && n == 1) {  // the odd chain has no step
+                    ok = bwait(BAR(BO_FREE + 1), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                    if (ok) tc_commit(BAR(BO_FINAL + 1));
+                }
+            }
+            if (!ok) {  // wait (bounded) for MMAs in flight before tensor memory is released
+                tc_commit(BAR(B_DRAIN));
+                uint32_t dummy = 0;
+                const unsigned long long t0 = globaltimer_ns();
+                while (!mbar_try_wait(BAR(B_DRAIN), 0) && globaltimer_ns() - t0 < 200000000ull) ++dummy;
+            }
+        }
+        __syncwarp();
+    } else if (wg == 1 || wg == 2) {
+        // ------------------------------------------------------------- softmax
+        setmaxnreg_inc<176>();
+        const int t = wg - 1;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + C::colS(t);
+        const uint32_t tO = tmem + lane_base + C::colO(t);
+        const int row = (warp & 3) * 32 + lane;
+        const float sl2 = p.scale_log2;
+        uint32_t sph = 0, nit = 0;
+        bool ok = true;
+        SpanWalk w;
+        span_walk_init<PAGED>(p, *sched, w);
+        SpanSeg g;
+        SpanItem it;
+        for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
+            // places of this tile's first and last token, and of this row's
+            const int tt = it.dual ? 0 : t * p.tile_tok;
+            const int rows = min(it.ntok - tt, p.tile_tok) * p.G;
+            const int p_min = it.pos0 + tt, p_max = p_min + min(it.ntok - tt, p.tile_tok) - 1;
+            const bool row_ok = row < rows;
+            const int pos = p_min + (PAGED ? row / p.G : row);
+            const int row_lo = max(0, pos - p.left), row_hi = min(pos + p.right, g.keys - 1);
+            const int all_lo = p_max - p.left, all_hi = min(p_min + p.right, g.keys - 1);
+            const bool idle = (warp & 3) * 32 >= rows;  // no row of this warp exists
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            const int n = g.j1 - g.j0, step = it.dual ? 2 : 1;
+            for (int x = it.dual ? t : 0; x < n; x += step) {
+                ok = warp_bwait(BAR(BS_FULL + t), sph, abort_flag, kSiteSoftS);
+                if (!ok) break;
+                sph ^= 1u;
+                if (idle) {  // P keeps what S left there: only rows that do not exist read it
+                    if (lane == 0) mbar_arrive(BAR(BP_FULL + t));
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t sa[64], sb[64];  // this thread's row of S: columns 0-63, 64-127
+#define SV(i) u2f((i) < 64 ? sa[(i) & 63] : sb[(i) & 63])
+                const int c0 = it.tile(g.j0 + x) * 128;
+                // some row does not see every key of the tile
+                const bool masked = all_hi < c0 + 127 || (all_lo > c0 && p.sinks < c0 + 128);
+                auto load_scores = [&]() {
+                    tmem_ld64x2(tS, sa, sb);
+                    if (masked) {
+                        const uint32_t ninf = f2u(-INFINITY);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const uint32_t bits = span_mask_word(row_lo - c0, row_hi - c0, p.sinks - c0, 32 * h);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                uint32_t &s = h < 2 ? sa[(h & 1) * 32 + i] : sb[(h & 1) * 32 + i];
+                                s = (bits >> i) & 1u ? s : ninf;
+                            }
+                        }
+                    }
+                };
+                auto row_max = [&]() {
+                    float mx0 = fmaxf(u2f(sa[0]), u2f(sa[1])), mx1 = fmaxf(u2f(sa[2]), u2f(sa[3]));
+                    float mx2 = fmaxf(u2f(sa[4]), u2f(sa[5])), mx3 = fmaxf(u2f(sa[6]), u2f(sa[7]));
+#pragma unroll
+                    for (int i = 8; i < 64; i += 8) {
+                        mx0 = fmax3(mx0, u2f(sa[i + 0]), u2f(sa[i + 1]));
+                        mx1 = fmax3(mx1, u2f(sa[i + 2]), u2f(sa[i + 3]));
+                        mx2 = fmax3(mx2, u2f(sa[i + 4]), u2f(sa[i + 5]));
+                        mx3 = fmax3(mx3, u2f(sa[i + 6]), u2f(sa[i + 7]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; i += 8) {
+                        mx0 = fmax3(mx0, u2f(sb[i + 0]), u2f(sb[i + 1]));
+                        mx1 = fmax3(mx1, u2f(sb[i + 2]), u2f(sb[i + 3]));
+                        mx2 = fmax3(mx2, u2f(sb[i + 4]), u2f(sb[i + 5]));
+                        mx3 = fmax3(mx3, u2f(sb[i + 6]), u2f(sb[i + 7]));
+                    }
+                    return fmax3(mx0, mx1, fmaxf(mx2, mx3));
+                };
+                uint32_t pk[64];
+                float lstep = 0.f;
+                // p = exp2(s * scale*log2e - m); a row that has seen no key yet takes m = 0,
+                // its scores being -inf
+                auto exps = [&]() {
+                    const float me = m == -INFINITY ? 0.f : m;
+                    const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-me, -me);
+                    uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        const int e = 2 * i;
+                        float e0, e1, e2, e3;
+                        f2unpack(ffma2(f2pack(SV(e), SV(e + 1)), sc2, nm2), e0, e1);
+                        f2unpack(ffma2(f2pack(SV(e + 2), SV(e + 3)), sc2, nm2), e2, e3);
+                        e0 = ex2_approx(e0);
+                        e1 = ex2_approx(e1);
+                        e2 = ex2_approx(e2);
+                        e3 = ex2_approx(e3);
+                        acc0 = fadd2(acc0, f2pack(e0, e1));
+                        acc1 = fadd2(acc1, f2pack(e2, e3));
+                        pk[i] = pack_bf16x2(e0, e1);
+                        pk[i + 1] = pack_bf16x2(e2, e3);
+                    }
+                    float a0, a1;
+                    f2unpack(fadd2(acc0, acc1), a0, a1);
+                    lstep = a0 + a1;
+                };
+                load_scores();
+                if (first) m = row_max() * sl2;
+                exps();
+                // As in attn_fwd_kernel the max is taken at the first step and then kept
+                // while no row sum passes 256 (no p above 2^8); a row that has not seen a
+                // key before takes it at the first step where it does.
+                if (!first && __any_sync(0xffffffffu, row_ok && (m == -INFINITY || !(lstep <= 256.0f)))) {
+                    load_scores();
+                    const float mnew = row_max() * sl2;
+                    float alpha = 1.f;
+                    bool need = false;
+                    if (mnew > m + 8.0f) {  // also from m = -inf to any score
+                        alpha = ex2_approx(m - mnew);
+                        m = mnew;
+                        need = true;
+                    }
+                    if (__any_sync(0xffffffffu, need)) {
+                        // The commit that signalled S_t for this step also covers the
+                        // previous O_t += P V, so O_t is stable here.
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
+                            tmem_st32(tO + c, o);
+                        }
+                        l *= alpha;
+                    }
+                    exps();
+                }
+                first = false;
+                l += lstep;
+                {
+                    uint32_t h0[32], h1[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        h0[i] = pk[i];
+                        h1[i] = pk[32 + i];
+                    }
+                    tmem_st32(tS, h0);
+                    tmem_st32(tS + 32, h1);
+                }
+#undef SV
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(BP_FULL + t));
+            }
+            if (!ok) break;
+            ok = warp_bwait(BAR(BL_EMPTY + t), (nit & 1u) ^ 1u, abort_flag, kSiteSoftL);
+            if (!ok) break;
+            row_ml[t * 256 + row] = l;
+            row_ml[t * 256 + 128 + row] = m;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(BL_FULL + t));
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        setmaxnreg_dec<112>();
+        const int wq = warp & 3;
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const int row = wq * 32 + lane;
+        const uint32_t stage = sStage + wq * C::kStageWarp;
+        uint32_t nit = 0;
+        bool ok = true;
+        SpanPieces pieces{};
+        SpanWalk w;
+        span_walk_init<PAGED>(p, *sched, w);
+        SpanSeg g;
+        SpanItem it;
+        for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
+            const bool piece = g.j1 - g.j0 < it.n;
+            if (piece && g.j0 == 0) {
+                const long long end = span_first(*sched, (int)blockIdx.x + 1) + (it.n - g.j1);  // behind the item's last step
+                pieces = SpanPieces{span_cta_of(*sched, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, it.tok0,
+                                    it.ntok, g.q0, 0};
+            }
+            auto row_dst = [&](int t, int rows) -> int64_t {
+                if (row >= rows) return -1;
+                const int r = PAGED ? row / p.G : row;
+                return span_out_offset<D, PAGED>(p, g.head, g.q0, it.tok0 + t * p.tile_tok + r, PAGED ? row - r * p.G : 0);
+            };
+            auto release_o = [&](int t) {  // O_t fully read: the next item may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(BO_FREE + t));
+            };
+            // one tile's 32 columns from c0 on (f: its factors) to the output or the record
+            auto emit = [&](int t, int c0, const float (&f)[32], int64_t dst, bool any_row) {
+                if (!any_row) return;
+                if (piece) {
+                    if (dst < 0) return;
+                    float4 *o4 = reinterpret_cast<float4 *>(p.rec + (size_t)g.slot * R::kFloats) + (size_t)t * (D / 4) * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        o4[(size_t)(c0 / 4 + q) * 128 + row] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                    return;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    stage_chunk(stage, lane, (c0 % 64) / 8 + c, pack_bf16x2(f[8 * c + 0], f[8 * c + 1]),
+                                pack_bf16x2(f[8 * c + 2], f[8 * c + 3]), pack_bf16x2(f[8 * c + 4], f[8 * c + 5]),
+                                pack_bf16x2(f[8 * c + 6], f[8 * c + 7]));
+                if ((c0 + 32) % 64 == 0)
+                    flush_block<true>(p.out, stage, lane, dst, c0 / 64);
+                else if (c0 + 32 == D)  // the half block of D = 96
+                    flush_block<true, 4>(p.out, stage, lane, dst, c0 / 64);
+            };
+            auto take_ml = [&](int t, float &l, float &m) {
+                ok = warp_bwait(BAR(BO_FINAL + t), nit & 1u, abort_flag, kSiteEpiO) &&
+                     warp_bwait(BAR(BL_FULL + t), nit & 1u, abort_flag, kSiteEpiL);
+                if (!ok) return;
+                l = row_ml[t * 256 + row];
+                m = row_ml[t * 256 + 128 + row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(BL_EMPTY + t));
+                tc_fence_after();
+            };
+            auto put_ml = [&](int t, float m, float l) {
+                float *r = p.rec + (size_t)g.slot * R::kFloats + R::kML + t * 256 + row;
+                r[0] = m;
+                r[128] = l;
+            };
+            if (it.dual) {
+                float l0 = 0.f, m0 = 0.f, l1 = 0.f, m1 = 0.f;
+                take_ml(0, l0, m0);
+                if (ok) take_ml(1, l1, m1);
+                if (!ok) break;
+                const int rows = it.ntok * p.G;
+                const int64_t dst = row_dst(0, rows);
+                const bool any_row = wq * 32 < rows, two = g.j1 - g.j0 > 1;
+                const float m = fmaxf(m0, m1);
+                float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
+                float a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+                const float l = a0 * l0 + a1 * l1;
+                if (!piece) {
+                    const float inv = l > 0.f ? 1.0f / l : 0.f;
+                    a0 *= inv;
+                    a1 *= inv;
+                } else if (dst >= 0) {
+                    put_ml(0, m, l);
+                }
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    if (!any_row) continue;
+                    uint32_t o[32];
+                    float f[32];
+                    tmem_ld32(tmem + lane_base + C::colO(0) + c0, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = a0 > 0.f ? u2f(o[i]) * a0 : 0.f;
+                    if (two) {
+                        tmem_ld32(tmem + lane_base + C::colO(1) + c0, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = a1 > 0.f ? fmaf(u2f(o[i]), a1, f[i]) : f[i];
+                    }
+                    emit(0, c0, f, dst, true);
+                }
+                release_o(0);
+                release_o(1);
+                continue;
+            }
+            for (int t = 0; t < 2; ++t) {
+                float l = 0.f, m = 0.f;
+                take_ml(t, l, m);
+                if (!ok) break;
+                const int rows = min(it.ntok - t * p.tile_tok, p.tile_tok) * p.G;
+                const int64_t dst = row_dst(t, rows);
+                const bool any_row = wq * 32 < rows;
+                float inv = 1.f;
+                if (!piece)
+                    inv = l > 0.f ? 1.0f / l : 0.f;
+                else if (dst >= 0)
+                    put_ml(t, m, l);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    float f[32];
+                    tmem_ld32(tmem + lane_base + C::colO(t) + c0, o);
+                    if (c0 + 32 == D) release_o(t);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = u2f(o[i]) * inv;
+                    emit(t, c0, f, dst, any_row);
+                }
+            }
+        }
+        if ((PAGED || p.rec) && warp == 12 && lane == 0) p.pieces[blockIdx.x] = ok ? pieces : SpanPieces{};
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+#undef BAR
+}
+
+// Adds up the pieces of the item whose first piece is CTA blockIdx.x's last
+// segment: piece 0 in the record named by the CTA, piece i > 0 in the first
+// record of CTA blockIdx.x + i. One thread per row and 4 columns; the pieces'
+// loads go out eight at a time, their latency being all that this costs.
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__ SpanParams p) {
+    using R = Rec<D>;
+    const SpanPieces s = p.pieces[blockIdx.x];
+    if (s.pieces < 2) return;
+    const int rows0 = min(s.ntok, p.tile_tok) * p.G;  // rows of the first tile
+    const int rows = s.ntok * p.G;
+    constexpr int U = 8;
+    for (int i = (int)(blockIdx.y * 256 + threadIdx.x); i < rows * (D / 4); i += (int)gridDim.y * 256) {
+        // lanes hold neighbouring rows of one column group, as the records do
+        const int c4 = i / rows, r = i - c4 * rows;
+        const int t = r >= rows0 ? 1 : 0, row = t ? r - rows0 : r;
+        const size_t o_at = ((size_t)t * (D / 4) + c4) * 128 + row, ml_at = R::kML + t * 256 + row;
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < s.pieces; k0 += U) {
+            float m[U], l[U];
+            float4 o[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                m[u] = -INFINITY;
+                if (k0 + u >= s.pieces) continue;
+                const int slot = k0 + u == 0 ? s.slot : 2 * ((int)blockIdx.x + k0 + u);
+                const float *rec = p.rec + (size_t)slot * R::kFloats;
+                m[u] = rec[ml_at];
+                l[u] = rec[ml_at + 128];
+                o[u] = reinterpret_cast<const float4 *>(rec)[o_at];
+            }
+            float top = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+            if (top == -INFINITY) continue;  // no key seen yet
+            const float a = ex2_approx(M - top);
+            M = top;
+            L *= a;
+            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (m[u] == -INFINITY) continue;
+                const float b = ex2_approx(m[u] - top);
+                L = fmaf(b, l[u], L);
+                acc = make_float4(fmaf(b, o[u].x, acc.x), fmaf(b, o[u].y, acc.y), fmaf(b, o[u].z, acc.z), fmaf(b, o[u].w, acc.w));
+            }
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int tk = PAGED ? row / p.G : row;
+        const int64_t dst = span_out_offset<D, PAGED>(p, s.head, s.q0, s.tok0 + t * p.tile_tok + tk, PAGED ? row - tk * p.G : 0);
+        *reinterpret_cast<uint2 *>(p.out + dst + c4 * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+}
+
+template <int D, bool PAGED>
+static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
+    auto kern = span_attn_kernel<D, PAGED>;
+    static std::atomic<uint64_t> configured{0};  // devices where the shared-memory limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D>::kSmemAlloc);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    kern<<<grid, 512, SpanCfg<D>::kSmemAlloc, stream>>>(maps, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.rec) {
+        span_merge_kernel<D, PAGED><<<dim3((unsigned)grid, 8), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+#define XS_DEFINE_SPAN_ENTRY(D)                                                                                       \
+    cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
+        return p.table ? launch_span_one<D, true>(maps, p, grid, stream) : launch_span_one<D, false>(maps, p, grid, stream); \
+    }                                                                                                                 \
+    cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear) {                                          \
+        cudaError_t e = cudaMemcpyFromSymbol(value, g_xs_error, sizeof(unsigned int));                                \
+        if (e == cudaSuccess && clear && *value) {                                                                    \
+            const unsigned int zero = 0;                                                                              \
+            e = cudaMemcpyToSymbol(g_xs_error, &zero, sizeof(unsigned int));                                          \
+        }                                                                                                             \
+        return e;                                                                                                     \
+    }
+
+}  // namespace xs

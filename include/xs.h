@@ -378,7 +378,7 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
  *            xs_attn_window_workspace_size bytes; it needs no initialisation. With
  *            it the work is split evenly over the SMs, pieces of a query tile
  *            meeting in the workspace. NULL (with 0): whole query tiles only.
- * left, right >= -1, sinks >= 0. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
+ * left, right >= -1, sinks >= 0, S <= 2^24. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
  */
 xs_status xs_attn_window(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,
                          float scale, int left, int right, int sinks, void *workspace, size_t workspace_bytes,
@@ -406,7 +406,8 @@ xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_
  * outside the pool, the table or the packed rows is never accessed: keys in
  * pages outside 0 .. n_pages - 1 are undefined in attention and are not written by
  * the append, and lengths are cut to max_pages * page keys.
- * page: a power of two from 16 to 1024; max_pages * page <= 2^30; D = 64, 96 or 128.
+ * page: a power of two from 16 to 1024; max_pages * page <= 2^29; N <= 65536;
+ * T <= 2^29; D = 64, 96 or 128.
  *
  * xs_cache_append writes the new tokens' keys and values,
  *   k, v : [T][Hk][D] bf16,

@@ -322,7 +322,7 @@ def test_paged_refusals():
         assert f(N=-1) == xs.XS_ERR_SHAPE and f(T=-1) == xs.XS_ERR_SHAPE and f(Hk=0) == xs.XS_ERR_SHAPE
         assert f(n_pages=0) == xs.XS_ERR_SHAPE and f(max_pages=0) == xs.XS_ERR_SHAPE
         assert f(max_pages=1 << 27) == xs.XS_ERR_SHAPE and f(n_pages=2 ** 31 - 1, page=1024) == xs.XS_ERR_SHAPE
-        assert f(T=2 ** 31 - 1) == xs.XS_ERR_SHAPE and f(N=1 << 21) == xs.XS_ERR_SHAPE
+        assert f(T=2 ** 31 - 1) == xs.XS_ERR_SHAPE and f(N=(1 << 16) + 1) == xs.XS_ERR_SHAPE
         assert f(D=256) == xs.XS_ERR_UNSUPPORTED and f(page=8) == xs.XS_ERR_UNSUPPORTED
         assert f(page=48) == xs.XS_ERR_UNSUPPORTED and f(page=2048) == xs.XS_ERR_UNSUPPORTED
         assert f(q=Q + 2) == xs.XS_ERR_ALIGN and f(kp=KP + 8) == xs.XS_ERR_ALIGN and f(tab=TAB + 2) == xs.XS_ERR_ALIGN
