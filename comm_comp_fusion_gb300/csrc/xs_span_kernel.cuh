@@ -13,11 +13,14 @@
 // Rows. A query tile is 128 rows: 128 tokens of one head, or, with G query heads
 // per key head, floor(128 / G) tokens x G heads, so that the heads of a group
 // share the K/V tiles they read. An item is one key head of one sequence and
-// two query tiles; it walks the 128-key tiles that any of its tokens sees (first
-// those of the sinks, then the window's). Keys outside a row's own span are
-// masked in the tiles where some row has any.
+// two query tiles; it walks the 128-key tiles that any of its tokens sees, from
+// the window's last down to its first (with a causal mask every row then meets
+// a key of its own at once, which is what the running maximum wants), then the
+// sinks'. Keys outside a row's own span are masked in the tiles where some row
+// has any.
 //   * Two tiles (pair): each K/V tile is used by both, one tile's softmax running
-//     under the other's MMAs.
+//     under the other's MMAs. A K/V tile that only one of them sees (at the
+//     window's ends) costs the other nothing.
 //   * One tile (dual; single new tokens and the last rows of a chunk): the even
 //     and the odd K/V tiles form two chains with an O of their own each, which
 //     the epilogue adds up. A chain's step is a long dependent sequence (MMA,
@@ -38,24 +41,33 @@
 //               page numbers are fetched three tiles ahead. Pages that no token
 //               sees are not read (their box lies outside the pool: zeros).
 //   warp 1      MMA issuer
-//   warp 2      tensor-memory allocator
+//   warp 2      tensor-memory allocator, then the schedule: it walks the CTA's part
+//               and describes each stretch of an item (SpanSeg) in a ring in shared
+//               memory, ahead of the other roles
 //   warp 3      (PAGED) zeroes the V rows behind the last key, which no one has
 //               written: a weight of 0 times NaN would still be NaN
 //   warps 4-11  softmax, one warpgroup per tile or chain, one thread per row
 //   warps 12-15 epilogue
 #pragma once
 
+#include <climits>
+
 #include "xs_attn_kernel.cuh"
 
 namespace xs {
 
-enum : int { BFIX_ASK = 26, BFIX_DONE = 27 };  // the issuer asks warp 3 to clear a V tile's end, and its answer
-enum SpanSite : uint32_t { kSiteFix = 13 };
+// Further barriers: the issuer asks warp 3 to clear a V tile's end, and its
+// answer; the ring of segments (kSegs full, kSegs empty).
+constexpr int kSegs = 6;
+enum : int { BFIX_ASK = 26, BFIX_DONE = 27, BSEG = 32 };
+enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 
 template <int D> struct SpanCfg : Cfg<D> {
     using C = Cfg<D>;
-    static constexpr uint32_t kOffSched = C::kSmemUsed;  // SpanSched
-    static constexpr uint32_t kSmemAlloc = kOffSched + 64 + 1024;
+    static constexpr uint32_t kOffSched = C::kSmemUsed;      // SpanSched
+    static constexpr uint32_t kOffSegBar = kOffSched + 64;   // the segment ring's barriers
+    static constexpr uint32_t kOffSeg = kOffSegBar + 128;    // the segments
+    static constexpr uint32_t kSmemAlloc = kOffSeg + 96 * kSegs + 1024;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
 };
 
@@ -68,14 +80,18 @@ struct SpanSched {
 
 constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory
 
+constexpr float kSpanRise = 16384.0f;  // see the softmax
+
+// An item's K/V tiles by step y: hi, hi - 1, ... (nw of them, the window's), then
+// ns - 1, ..., 0 (those of the sinks that lie before it).
 struct SpanItem {
-    int ntok;    // tokens of the item's tiles
-    int tok0;    // first of them among the sequence's new tokens
-    int pos0;    // its place
-    int ns, w0;  // K/V tiles: 0 .. ns - 1, then w0, w0 + 1, ...
-    int n;       // steps
+    int ntok;  // tokens of the item's tiles
+    int tok0;  // first of them among the sequence's new tokens
+    int pos0;  // its place
+    int hi, nw, ns;
+    int n;     // steps
+    int s0, e1;  // pair: tile 0 takes part from step s0 on, tile 1 up to e1 and from nw on
     bool dual;
-    __device__ __forceinline__ int tile(int x) const { return x < ns ? x : w0 + x - ns; }
 };
 
 __device__ __forceinline__ SpanItem span_item(const SpanParams &p, int q_len, int keys, int pair) {
@@ -86,13 +102,18 @@ __device__ __forceinline__ SpanItem span_item(const SpanParams &p, int q_len, in
     it.dual = it.ntok <= p.tile_tok;
     const int hi = min(keys - 1, it.pos0 + it.ntok - 1 + p.right);
     const int lo = max(0, it.pos0 - p.left) >> 7;
-    if (hi < 0) {  // no key at all: one step, fully masked
-        it.ns = it.w0 = 0;
-        it.n = 1;
-    } else {
-        it.ns = min((min(p.sinks, hi + 1) + 127) >> 7, lo);
-        it.w0 = lo;
-        it.n = it.ns + (hi >> 7) - lo + 1;
+    it.s0 = it.ns = it.hi = 0;
+    it.n = it.nw = it.e1 = 1;  // no key at all: one step, fully masked
+    if (hi >= 0) {
+        it.hi = hi >> 7;
+        it.nw = it.hi - lo + 1;
+        const int sink_tiles = (min(p.sinks, hi + 1) + 127) >> 7;
+        it.ns = min(sink_tiles, lo);
+        it.n = it.nw + it.ns;
+        const int hi0 = max(0, min(keys - 1, it.pos0 + p.tile_tok - 1 + p.right)) >> 7;
+        const int lo1 = max(0, it.pos0 + p.tile_tok - p.left) >> 7;
+        it.s0 = it.hi - min(it.hi, max(hi0, lo));
+        it.e1 = sink_tiles > lo ? it.nw : it.hi - min(lo1, it.hi) + 1;
     }
     return it;
 }
@@ -232,19 +253,32 @@ __device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *ou
     __syncthreads();
 }
 
-// A role's walk through its CTA's part, one stretch (segment) of an item at a time.
-struct SpanSeg {
-    int j0, j1;  // steps of the item
-    int slot;    // workspace record of the segment if it is a piece (see span_merge_kernel)
-    int seq, head;
-    int q0, keys;  // of the sequence: its first packed row, its keys
-};
+// The walk through a CTA's part, one stretch (segment) of an item at a time.
 struct SpanWalk {
     long long rem;  // steps left (whole items: items left)
     int seq, head, pair, j;
     int q0, q_len, keys;
     bool first;
 };
+// What the roles need to know of a segment (96 bytes).
+struct SpanSeg {
+    int n;            // steps; 0: no segment, the roles are done
+    int j0;           // the item's step that it starts with
+    int dual, piece;  // piece: not the whole item
+    int hi, nw, ns, s0, e1;
+    int seq, head;
+    int q0, tok0, ntok;  // the sequence's first packed row; the item's first token, their number
+    int pos0, keys;      // the first token's place; the sequence's keys
+    int slot;            // workspace record of a piece
+    int fix;             // rows of the first V tile that hold keys, where the rest has to be cleared; -1: nothing to do
+    int lo, last;        // first key of the window, last key that any token sees
+    int pad[4];
+};
+static_assert(sizeof(SpanSeg) == 96, "segment ring");
+__device__ __forceinline__ int span_tile(const volatile SpanSeg &g, int y) {
+    const int nw = g.nw;
+    return y < nw ? g.hi - y : g.ns - 1 - (y - nw);
+}
 template <bool PAGED>
 __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
     w.first = true;
@@ -264,26 +298,37 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
     if (w.rem > 0) span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
 }
 template <bool PAGED>
-__device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, SpanSeg &g, SpanItem &it) {
+__device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, SpanSeg &g) {
     if (w.rem <= 0) return false;
     if (PAGED)
         while (w.q_len == 0) {
             if (++w.seq >= p.N) return false;
             span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
         }
-    it = span_item(p, w.q_len, w.keys, w.pair);
+    const SpanItem it = span_item(p, w.q_len, w.keys, w.pair);
+    const int w_keys = w.keys;
+    g.dual = it.dual;
+    g.hi = it.hi;
+    g.nw = it.nw;
+    g.ns = it.ns;
+    g.s0 = it.s0;
+    g.e1 = it.e1;
     g.seq = w.seq;
     g.head = w.head;
     g.q0 = w.q0;
+    g.tok0 = it.tok0;
+    g.ntok = it.ntok;
+    g.pos0 = it.pos0;
     g.keys = w.keys;
+    g.lo = max(0, it.pos0 - p.left);
+    g.last = min(w.keys - 1, it.pos0 + it.ntok - 1 + p.right);
     g.slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
     w.first = false;
     if (PAGED || p.rec) {
         g.j0 = w.j;
-        const int take = (int)min((long long)(it.n - w.j), w.rem);
-        g.j1 = w.j + take;
-        w.rem -= take;
-        w.j = g.j1;
+        g.n = (int)min((long long)(it.n - w.j), w.rem);
+        w.rem -= g.n;
+        w.j += g.n;
         if (w.j == it.n) {
             w.j = 0;
             if (++w.pair * 2 * p.tile_tok >= w.q_len) {
@@ -296,20 +341,17 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, Span
         }
     } else {
         g.j0 = 0;
-        g.j1 = it.n;
+        g.n = it.n;
         --w.rem;
         const long long item = (long long)w.head * p.n_pairs + w.pair + gridDim.x;
         w.head = (int)(item / p.n_pairs);
         w.pair = (int)(item - (long long)w.head * p.n_pairs);
     }
+    g.piece = g.n < it.n;
+    // rows behind the last key, in a box that holds keys (boxes without are zeros)
+    const int box = PAGED ? min(p.page, 128) : 128;
+    g.fix = PAGED && g.j0 == 0 && it.hi == w_keys >> 7 && (w_keys & (box - 1)) ? w_keys & 127 : -1;
     return true;
-}
-
-// The first row of the segment's last K/V tile that no key has written, if its
-// box holds keys and such rows; -1 otherwise. (Boxes without keys are zeros.)
-__device__ __forceinline__ int span_fix_rows(const SpanSeg &g, const SpanItem &it, int box) {
-    const bool cut = g.j1 == it.n && it.tile(it.n - 1) == g.keys >> 7 && (g.keys & (box - 1));
-    return cut ? g.keys & 127 : -1;
 }
 
 // Element offset of the output row of token `tok` (of the sequence's new tokens,
@@ -352,12 +394,15 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
     const uint32_t sQ = base + C::kOffQ, sKV = base + C::kOffKV, sStage = base + C::kOffStage;
-    const uint32_t sBar = base + C::kOffBar;
+    const uint32_t sBar = base + C::kOffBar, sSegBar = base + C::kOffSegBar;
     float *row_ml = reinterpret_cast<float *>(sm + C::kOffL);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
     volatile uint32_t *abort_flag = misc + 1;
     SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSched);
+    volatile SpanSeg *segs = reinterpret_cast<volatile SpanSeg *>(sm + C::kOffSeg);
 #define BAR(i) (sBar + 8u * (uint32_t)(i))
+#define SEG_FULL(i) (sSegBar + 8u * (uint32_t)(i))
+#define SEG_EMPTY(i) (sSegBar + 8u * (uint32_t)(kSegs + (i)))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
@@ -377,6 +422,10 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(BAR(B_DRAIN), 1);
         mbar_init(BAR(BFIX_ASK), 1);
         mbar_init(BAR(BFIX_DONE), 1);
+        for (int s = 0; s < kSegs; ++s) {
+            mbar_init(SEG_FULL(s), 1);
+            mbar_init(SEG_EMPTY(s), PAGED ? 15 : 14);  // producer, issuer, (V clearing,) 8 softmax warps, 4 epilogue warps
+        }
         misc[1] = 0u;
         fence_mbar_init();
         prefetch_tmap(&tm.q);
@@ -394,45 +443,96 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
     const int wg = warp >> 2;
+    // The roles walk the ring of segments alike.
+    uint32_t seg_it = 0;
+#define SEG (segs[seg_it % kSegs])
+#define SEG_WAIT(wait) wait(SEG_FULL(seg_it % kSegs), (seg_it / kSegs) & 1u, abort_flag, kSiteSeg)
+#define SEG_DONE()  /* after the warp's last look at the segment */      \
+    do {                                                                \
+        if (warp != 1) __syncwarp();                                    \
+        if (lane == 0) mbar_arrive(SEG_EMPTY(seg_it % kSegs));          \
+        ++seg_it;                                                       \
+    } while (0)
 
     if (wg == 0) {
         setmaxnreg_dec<48>();
-        if (warp == 0) {
-            // ------------------------------------------------------ TMA producer
-            uint32_t kv_it = 0, q_it[2] = {0u, 0u};
-            bool ok = true;
+        if (warp == 2) {
+            // ---------------------------------------------------------- schedule
+            SpanPieces pieces{};
             SpanWalk w;
             span_walk_init<PAGED>(p, *sched, w);
-            SpanSeg g;
-            SpanItem it;
+            for (bool more = true; more; ++seg_it) {
+                SpanSeg g;
+                more = span_next<PAGED>(p, w, g);
+                if (!more) g.n = 0;
+                if (more && g.piece && g.j0 == 0) {  // its first piece: this CTA's last segment
+                    const int left = g.nw + g.ns - g.n;
+                    const long long end = span_first(*sched, (int)blockIdx.x + 1) + left;  // behind the item's last step
+                    pieces = SpanPieces{span_cta_of(*sched, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, g.tok0,
+                                        g.ntok, g.q0, 0};
+                }
+                if (!warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg)) break;
+                if (lane == 0) {
+                    volatile SpanSeg &d = SEG;
+                    d.n = g.n;
+                    d.j0 = g.j0;
+                    d.dual = g.dual;
+                    d.piece = g.piece;
+                    d.hi = g.hi;
+                    d.nw = g.nw;
+                    d.ns = g.ns;
+                    d.s0 = g.s0;
+                    d.e1 = g.e1;
+                    d.seq = g.seq;
+                    d.head = g.head;
+                    d.q0 = g.q0;
+                    d.tok0 = g.tok0;
+                    d.ntok = g.ntok;
+                    d.pos0 = g.pos0;
+                    d.keys = g.keys;
+                    d.slot = g.slot;
+                    d.fix = g.fix;
+                    d.lo = g.lo;
+                    d.last = g.last;
+                    mbar_arrive(SEG_FULL(seg_it % kSegs));
+                }
+            }
+            if ((PAGED || p.rec) && lane == 0) p.pieces[blockIdx.x] = pieces;
+        } else if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0;
+            bool ok = true;
             const int box = PAGED ? min(p.page, 128) : 128;  // rows of a box
-            while (ok && span_next<PAGED>(p, w, g, it)) {
-                for (int t = 0; t < (it.dual ? 1 : 2) && ok; ++t) {
-                    ok = warp_bwait(BAR(BQ_EMPTY + t), (q_it[t] & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+            while (ok) {
+                ok = SEG_WAIT(warp_bwait);
+                volatile SpanSeg &g = SEG;
+                const int n = g.n, j0 = g.j0, head = g.head;
+                if (!ok || n == 0) break;
+                const bool dual = g.dual;
+                for (int t = 0; t < (dual ? 1 : 2) && ok; ++t) {
+                    ok = warp_bwait(BAR(BQ_EMPTY + t), ((t ? q_it1++ : q_it0++) & 1u) ^ 1u, abort_flag, kSiteLoadQ);
                     if (!ok) break;
-                    ++q_it[t];
                     if (lane == 0) {
                         mbar_arrive_expect_tx(BAR(BQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
-                        const int tok = it.tok0 + t * p.tile_tok;
+                        const int tok = g.q0 + g.tok0 + t * p.tile_tok;
 #pragma unroll
                         for (int db = 0; db < C::kNDB; ++db) {
                             const uint32_t dst = sQ + t * C::kTile + db * C::kBlk;
                             if (PAGED)
-                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, 0, g.head, g.q0 + tok);
+                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, 0, head, tok);
                             else
-                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, g.head % p.Hl, tok, g.head / p.Hl);
+                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
                         }
                     }
                 }
                 if (!ok) break;
                 // page of this lane's box of step x's tile; n_pages (outside the pool)
                 // where no token of the item sees any of its keys
-                const int lo = max(0, it.pos0 - p.left), hi = min(g.keys - 1, it.pos0 + it.ntok - 1 + p.right);
                 const int *table = PAGED ? p.table + (int64_t)g.seq * p.max_pages : nullptr;
                 auto page_of = [&](int x) -> int {
-                    if (!PAGED || lane * box >= 128 || x >= g.j1) return 0;
-                    const int k0 = it.tile(x) * 128 + lane * box;
-                    if (k0 > hi || (k0 + box <= lo && k0 >= p.sinks)) return p.n_pages;
+                    if (!PAGED || lane * box >= 128 || x >= n) return 0;
+                    const int k0 = span_tile(g, j0 + x) * 128 + lane * box;
+                    if (k0 > g.last || (k0 + box <= g.lo && k0 >= p.sinks)) return p.n_pages;
                     const int id = table[k0 / p.page];
                     return id < 0 || id >= p.n_pages ? p.n_pages : id;
                 };
@@ -443,32 +543,33 @@ __global__ void __launch_bounds__(512, 1)
                     ++kv_it;
                     if (lane == 0) mbar_arrive_expect_tx(BAR(BKV_FULL + slot), C::kTile);
                     __syncwarp();
-                    const int tile = it.tile(x);
+                    const int tile = span_tile(g, j0 + x);
                     if (PAGED) {
                         if (lane * box < 128) {
                             const int row = (tile * 128 + lane * box) & (p.page - 1);
                             const uint32_t dst = sKV + slot * C::kTile + (uint32_t)(lane * box) * 128u;
 #pragma unroll
                             for (int db = 0; db < C::kNDB; ++db)
-                                tma_load_4d(dst + db * C::kBlk, m, BAR(BKV_FULL + slot), db * 64, g.head, row, page);
+                                tma_load_4d(dst + db * C::kBlk, m, BAR(BKV_FULL + slot), db * 64, head, row, page);
                         }
                     } else if (lane < C::kNDB) {
                         tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(BKV_FULL + slot), lane * 64,
-                                    g.head % p.Hl, tile * 128, g.head / p.Hl);
+                                    head % p.Hl, tile * 128, head / p.Hl);
                     }
                 };
-                int pg0 = page_of(g.j0), pg1 = page_of(g.j0 + 1), pg2 = page_of(g.j0 + 2);
-                load_tile(&tm.k, g.j0, pg0);
-                if (ok && it.dual && g.j0 + 1 < g.j1) load_tile(&tm.k, g.j0 + 1, pg1);
-                for (int x = g.j0; ok && x < g.j1; ++x) {
+                int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
+                load_tile(&tm.k, 0, pg0);
+                if (ok && dual && n > 1) load_tile(&tm.k, 1, pg1);
+                for (int x = 0; ok && x < n; ++x) {
                     const int pg3 = page_of(x + 3);
                     load_tile(&tm.v, x, pg0);
-                    const int la = it.dual ? 2 : 1;
-                    if (ok && x + la < g.j1) load_tile(&tm.k, x + la, it.dual ? pg2 : pg1);
+                    const int la = dual ? 2 : 1;
+                    if (ok && x + la < n) load_tile(&tm.k, x + la, dual ? pg2 : pg1);
                     pg0 = pg1;
                     pg1 = pg2;
                     pg2 = pg3;
                 }
+                if (ok) SEG_DONE();
             }
             if (!ok) {  // let copies already in flight land before the CTA exits
                 const unsigned long long t0 = globaltimer_ns();
@@ -478,27 +579,25 @@ __global__ void __launch_bounds__(512, 1)
         } else if (PAGED && warp == 3) {
             // ------------------------------------ V rows behind the last key: zeros
             uint32_t kv_it = 0, fph = 0;
-            bool ok = true;
             const int box = min(p.page, 128);
-            SpanWalk w;
-            span_walk_init<PAGED>(p, *sched, w);
-            SpanSeg g;
-            SpanItem it;
-            while (ok && span_next<PAGED>(p, w, g, it)) {
-                kv_it += 2u * (uint32_t)(g.j1 - g.j0);
-                const int rows = span_fix_rows(g, it, box);
-                if (rows < 0) continue;
-                const uint32_t slot = (kv_it - 1u) % C::kSlots;  // the segment's last V tile
-                ok = warp_bwait(BAR(BFIX_ASK), fph, abort_flag, kSiteFix);  // the tile is in
-                if (!ok) break;
-                fph ^= 1u;
-                for (int r = rows * 8 + lane; r < ((rows + box - 1) / box * box) * 8; r += 32)
+            while (SEG_WAIT(warp_bwait)) {
+                const int n = SEG.n, rows = SEG.fix;
+                if (n == 0) break;
+                // the segment's first V tile follows its first one or two K tiles
+                const uint32_t slot = (kv_it + (SEG.dual && n > 1 ? 2u : 1u)) % C::kSlots;
+                kv_it += 2u * (uint32_t)n;
+                if (rows >= 0) {
+                    if (!warp_bwait(BAR(BFIX_ASK), fph, abort_flag, kSiteFix)) break;  // the tile is in
+                    fph ^= 1u;
+                    for (int r = rows * 8 + lane; r < ((rows + box - 1) / box * box) * 8; r += 32)
 #pragma unroll
-                    for (int db = 0; db < C::kNDB; ++db)
-                        st_shared_v4(sKV + slot * C::kTile + db * C::kBlk + (uint32_t)r * 16u, 0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(BFIX_DONE));
+                        for (int db = 0; db < C::kNDB; ++db)
+                            st_shared_v4(sKV + slot * C::kTile + db * C::kBlk + (uint32_t)r * 16u, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(BFIX_DONE));
+                }
+                SEG_DONE();
             }
         } else if (warp == 1 && lane == 0) {
             // -------------------------------------------------------- MMA issuer
@@ -523,60 +622,62 @@ __global__ void __launch_bounds__(512, 1)
                 for (int kk = 0; kk < 8; ++kk)
                     tc_mma_ts(d, a + kk * 8, va + (kk * 2048 >> 4), idO, (acc || kk > 0) ? 1u : 0u);
             };
-            uint32_t kv_it = 0, nit = 0, q_it0 = 0, q_it1 = 0, pph0 = 0, pph1 = 0, fph = 0;
+            uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0, pph0 = 0, pph1 = 0, fph = 0;
             bool ok = true;
-            SpanWalk w;
-            span_walk_init<PAGED>(p, *sched, w);
-            SpanSeg g;
-            SpanItem it;
-            const int box = PAGED ? min(p.page, 128) : 128;
             auto wait_kv = [&](uint32_t &slot) {
                 slot = kv_it % C::kSlots;
                 ok = ok && bwait(BAR(BKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
                 ++kv_it;
             };
-            for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
-                const int n = g.j1 - g.j0;
-                const bool fix = PAGED && span_fix_rows(g, it, box) >= 0;
-                ok = bwait(BAR(BQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
-                if (ok && !it.dual) ok = bwait(BAR(BQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
-                uint32_t ks, vs;
-                wait_kv(ks);
-                if (!ok) break;
+            auto wait_p = [&](int t, bool first) {  // P_t is in (and, at a tile's first step, O_t is free)
+                ok = bwait(BAR(BP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
+                if (ok && first) ok = bwait(BAR(BO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                if (t)
+                    pph1 ^= 1u;
+                else
+                    pph0 ^= 1u;
                 tc_fence_after();
-                issue_S(0, 0, ks);
-                if (!it.dual) {
-                    issue_S(1, 1, ks);
-                } else if (n > 1) {
-                    tc_commit(BAR(BKV_EMPTY + ks));
+            };
+            auto wait_v = [&](uint32_t &slot, bool fix) {
+                wait_kv(slot);
+                if (ok && fix) {
+                    mbar_arrive(BAR(BFIX_ASK));
+                    ok = bwait(BAR(BFIX_DONE), fph, abort_flag, kSiteFix);
+                    fph ^= 1u;
+                }
+            };
+            auto no_steps = [&](int t) {  // a tile or chain without a step in this segment
+                ok = bwait(BAR(BO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                if (ok) tc_commit(BAR(BO_FINAL + t));
+            };
+            while (ok) {
+                ok = SEG_WAIT(bwait);
+                volatile SpanSeg &g = SEG;
+                const int n = g.n;
+                if (!ok || n == 0) break;
+                const bool fix = PAGED && g.fix >= 0;
+                uint32_t ks, vs;
+                ok = bwait(BAR(BQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
+                if (g.dual) {
+                    // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
                     wait_kv(ks);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_S(1, 0, ks);
-                }
-                tc_commit(BAR(BKV_EMPTY + ks));
-                if (n <= (it.dual ? 2 : 1)) {
-                    tc_commit(BAR(BQ_EMPTY + 0));
-                    if (!it.dual) tc_commit(BAR(BQ_EMPTY + 1));
-                }
-                for (int x = 0; x < n; ++x) {
-                    wait_kv(vs);
-                    if (ok && fix && x == n - 1) {
-                        mbar_arrive(BAR(BFIX_ASK));
-                        ok = bwait(BAR(BFIX_DONE), fph, abort_flag, kSiteFix);
-                        fph ^= 1u;
-                    }
-                    if (!ok) break;
-                    if (it.dual) {
-                        const int t = x & 1;
-                        ok = bwait(BAR(BP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
-                        if (ok && x < 2) ok = bwait(BAR(BO_FREE + t), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                    issue_S(0, 0, ks);
+                    tc_commit(BAR(BKV_EMPTY + ks));
+                    if (n > 1) {
+                        wait_kv(ks);
                         if (!ok) break;
-                        if (t)
-                            pph1 ^= 1u;
-                        else
-                            pph0 ^= 1u;
                         tc_fence_after();
+                        issue_S(1, 0, ks);
+                        tc_commit(BAR(BKV_EMPTY + ks));
+                    }
+                    if (n <= 2) tc_commit(BAR(BQ_EMPTY + 0));
+                    for (int x = 0; x < n; ++x) {
+                        const int t = x & 1;
+                        wait_v(vs, fix && x == 0);
+                        if (ok) wait_p(t, x < 2);
+                        if (!ok) break;
                         issue_PV(t, vs, x >= 2);
                         tc_commit(BAR(BKV_EMPTY + vs));
                         if (x + 2 >= n) tc_commit(BAR(BO_FINAL + t));
@@ -588,42 +689,60 @@ __global__ void __launch_bounds__(512, 1)
                             tc_commit(BAR(BKV_EMPTY + ks));
                             if (x + 3 == n) tc_commit(BAR(BQ_EMPTY + 0));
                         }
-                        continue;
                     }
-                    const bool more = x + 1 < n;
-                    ok = bwait(BAR(BP_FULL + 0), pph0, abort_flag, kSiteMmaP);
-                    if (ok && x == 0) ok = bwait(BAR(BO_FREE + 0), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                    if (ok && n == 1) no_steps(1);
+                } else {
+                    if (ok) ok = bwait(BAR(BQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
+                    // steps (of the segment) of tile 0: from f0 on; of tile 1: below l1 and from m1 on
+                    const int f0 = max(g.s0 - g.j0, 0), l1 = min(g.e1 - g.j0, n), m1 = max(g.nw - g.j0, 0);
+                    auto on1 = [&](int x) { return x < l1 || x >= m1; };
+                    const int first1 = l1 > 0 ? 0 : m1, last1 = m1 < n ? n - 1 : l1 - 1;
+                    wait_kv(ks);
                     if (!ok) break;
-                    pph0 ^= 1u;
                     tc_fence_after();
-                    issue_PV(0, vs, x > 0);
-                    if (!more) tc_commit(BAR(BO_FINAL + 0));
-                    if (more) {
-                        wait_kv(ks);
+                    if (f0 == 0) issue_S(0, 0, ks);
+                    if (on1(0)) issue_S(1, 1, ks);
+                    tc_commit(BAR(BKV_EMPTY + ks));
+                    if (n == 1) {
+                        tc_commit(BAR(BQ_EMPTY + 0));
+                        tc_commit(BAR(BQ_EMPTY + 1));
+                    }
+                    for (int x = 0; x < n; ++x) {
+                        const bool more = x + 1 < n;
+                        wait_v(vs, fix && x == 0);
                         if (!ok) break;
-                        issue_S(0, 0, ks);
-                    }
-                    ok = bwait(BAR(BP_FULL + 1), pph1, abort_flag, kSiteMmaP);
-                    if (ok && x == 0) ok = bwait(BAR(BO_FREE + 1), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
-                    if (!ok) break;
-                    pph1 ^= 1u;
-                    tc_fence_after();
-                    issue_PV(1, vs, x > 0);
-                    tc_commit(BAR(BKV_EMPTY + vs));
-                    if (!more) tc_commit(BAR(BO_FINAL + 1));
-                    if (more) {
-                        issue_S(1, 1, ks);
-                        tc_commit(BAR(BKV_EMPTY + ks));
-                        if (x + 2 == n) {
-                            tc_commit(BAR(BQ_EMPTY + 0));
-                            tc_commit(BAR(BQ_EMPTY + 1));
+                        if (x >= f0) {
+                            wait_p(0, x == f0);
+                            if (!ok) break;
+                            issue_PV(0, vs, x > f0);
+                            if (!more) tc_commit(BAR(BO_FINAL + 0));
+                        }
+                        if (more) {
+                            wait_kv(ks);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (x + 1 >= f0) issue_S(0, 0, ks);
+                        }
+                        if (on1(x)) {
+                            wait_p(1, x == first1);
+                            if (!ok) break;
+                            issue_PV(1, vs, x > first1);
+                            if (x == last1) tc_commit(BAR(BO_FINAL + 1));
+                        }
+                        tc_commit(BAR(BKV_EMPTY + vs));
+                        if (more) {
+                            if (on1(x + 1)) issue_S(1, 1, ks);
+                            tc_commit(BAR(BKV_EMPTY + ks));
+                            if (x + 2 == n) {
+                                tc_commit(BAR(BQ_EMPTY + 0));
+                                tc_commit(BAR(BQ_EMPTY + 1));
+                            }
                         }
                     }
+                    if (ok && f0 >= n) no_steps(0);
+                    if (ok && l1 <= 0 && m1 >= n) no_steps(1);
                 }
-                if (ok && it.dual && n == 1) {  // the odd chain has no step
-                    ok = bwait(BAR(BO_FREE + 1), (nit & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
-                    if (ok) tc_commit(BAR(BO_FINAL + 1));
-                }
+                if (ok) SEG_DONE();
             }
             if (!ok) {  // wait (bounded) for MMAs in flight before tensor memory is released
                 tc_commit(BAR(B_DRAIN));
@@ -642,26 +761,54 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t tO = tmem + lane_base + C::colO(t);
         const int row = (warp & 3) * 32 + lane;
         const float sl2 = p.scale_log2;
-        uint32_t sph = 0, nit = 0;
+        uint32_t sph = 0;
         bool ok = true;
-        SpanWalk w;
-        span_walk_init<PAGED>(p, *sched, w);
-        SpanSeg g;
-        SpanItem it;
-        for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
-            // places of this tile's first and last token, and of this row's
-            const int tt = it.dual ? 0 : t * p.tile_tok;
-            const int rows = min(it.ntok - tt, p.tile_tok) * p.G;
-            const int p_min = it.pos0 + tt, p_max = p_min + min(it.ntok - tt, p.tile_tok) - 1;
-            const bool row_ok = row < rows;
-            const int pos = p_min + (PAGED ? row / p.G : row);
+        while (ok) {
+            ok = SEG_WAIT(warp_bwait);
+            volatile SpanSeg &g = SEG;
+            if (!ok || g.n == 0) break;
+            const int tt = g.dual ? 0 : t * p.tile_tok;  // tokens before this tile
+            const int toks = min(g.ntok - tt, p.tile_tok);
+            // places of this row's token, and the first and last key it may see
+            const int pos = g.pos0 + tt + (PAGED ? row / p.G : row);
+            const bool row_ok = row < toks * p.G;
             const int row_lo = max(0, pos - p.left), row_hi = min(pos + p.right, g.keys - 1);
-            const int all_lo = p_max - p.left, all_hi = min(p_min + p.right, g.keys - 1);
-            const bool idle = (warp & 3) * 32 >= rows;  // no row of this warp exists
+            const bool idle = (warp & 3) * 32 >= toks * p.G;  // no row of this warp exists
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            const int n = g.j1 - g.j0, step = it.dual ? 2 : 1;
-            for (int x = it.dual ? t : 0; x < n; x += step) {
+            // This tile's (chain's) steps and K/V tiles: c, c - step, ... down to c_end, then
+            // the sinks' from ns - 1 on. Some row misses a key of tile c if its keys pass
+            // all_hi, or begin before all_lo without being sinks.
+            int steps, c, c_end = g.hi - g.nw + 1;
+            const int step = g.dual ? 2 : 1;
+            {
+                const int n = g.n, j0 = g.j0, nw = g.nw;
+                int y = j0;  // the first step's
+                if (g.dual) {
+                    steps = (n + 1 - t) >> 1;
+                    y += t;
+                } else if (t == 0) {
+                    y = max(j0, g.s0);
+                    steps = j0 + n - y;
+                } else {
+                    const int e1 = g.e1;
+                    steps = max(0, min(e1, j0 + n) - j0) + max(0, j0 + n - max(nw, j0));
+                    if (y >= e1) y = max(y, nw);
+                    c_end = g.hi - e1 + 1;
+                }
+                c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
+                if (y >= nw) c_end = INT_MIN;
+            }
+            const int all_hi = min(g.pos0 + tt + p.right, g.keys - 1) - 127, all_lo = g.pos0 + tt + toks - 1 - p.left;
+#pragma unroll 1
+            for (; steps > 0; --steps) {
+                const int c0 = c * 128;
+                const bool masked = c0 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
+                c -= step;
+                if (c < c_end) {
+                    c += g.ns - c_end;
+                    c_end = INT_MIN;
+                }
                 ok = warp_bwait(BAR(BS_FULL + t), sph, abort_flag, kSiteSoftS);
                 if (!ok) break;
                 sph ^= 1u;
@@ -672,9 +819,8 @@ __global__ void __launch_bounds__(512, 1)
                 tc_fence_after();
                 uint32_t sa[64], sb[64];  // this thread's row of S: columns 0-63, 64-127
 #define SV(i) u2f((i) < 64 ? sa[(i) & 63] : sb[(i) & 63])
-                const int c0 = it.tile(g.j0 + x) * 128;
-                // some row does not see every key of the tile
-                const bool masked = all_hi < c0 + 127 || (all_lo > c0 && p.sinks < c0 + 128);
+                uint32_t pk[64];
+                float lstep = 0.f;
                 auto load_scores = [&]() {
                     tmem_ld64x2(tS, sa, sb);
                     if (masked) {
@@ -707,10 +853,8 @@ __global__ void __launch_bounds__(512, 1)
                         mx2 = fmax3(mx2, u2f(sb[i + 4]), u2f(sb[i + 5]));
                         mx3 = fmax3(mx3, u2f(sb[i + 6]), u2f(sb[i + 7]));
                     }
-                    return fmax3(mx0, mx1, fmaxf(mx2, mx3));
+                    return fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
                 };
-                uint32_t pk[64];
-                float lstep = 0.f;
                 // p = exp2(s * scale*log2e - m); a row that has seen no key yet takes m = 0,
                 // its scores being -inf
                 auto exps = [&]() {
@@ -737,22 +881,22 @@ __global__ void __launch_bounds__(512, 1)
                     lstep = a0 + a1;
                 };
                 load_scores();
-                if (first) m = row_max() * sl2;
+                if (first) m = row_max();
                 exps();
-                // As in attn_fwd_kernel the max is taken at the first step and then kept
-                // while no row sum passes 256 (no p above 2^8); a row that has not seen a
-                // key before takes it at the first step where it does.
-                if (!first && __any_sync(0xffffffffu, row_ok && (m == -INFINITY || !(lstep <= 256.0f)))) {
+                // The row max is taken at the first step and then kept while no row sum
+                // passes kSpanRise: p, l and O are floating point, so a maximum that lags by
+                // up to 2^14 costs no precision, and a first tile with only a few keys in it
+                // (a causal diagonal) seldom has to be put right. A row that has not seen a
+                // key before takes its max at the first step where it does.
+                if (!first && __any_sync(0xffffffffu, row_ok && (m == -INFINITY || !(lstep <= kSpanRise)))) {
                     load_scores();
-                    const float mnew = row_max() * sl2;
+                    const float mnew = row_max();
                     float alpha = 1.f;
-                    bool need = false;
-                    if (mnew > m + 8.0f) {  // also from m = -inf to any score
+                    if (mnew > m) {
                         alpha = ex2_approx(m - mnew);
                         m = mnew;
-                        need = true;
                     }
-                    if (__any_sync(0xffffffffu, need)) {
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
                         // The commit that signalled S_t for this step also covers the
                         // previous O_t += P V, so O_t is stable here.
 #pragma unroll 1
@@ -786,12 +930,13 @@ __global__ void __launch_bounds__(512, 1)
                 if (lane == 0) mbar_arrive(BAR(BP_FULL + t));
             }
             if (!ok) break;
-            ok = warp_bwait(BAR(BL_EMPTY + t), (nit & 1u) ^ 1u, abort_flag, kSiteSoftL);
+            ok = warp_bwait(BAR(BL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
             if (!ok) break;
             row_ml[t * 256 + row] = l;
             row_ml[t * 256 + 128 + row] = m;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(BL_FULL + t));
+            SEG_DONE();
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -800,24 +945,17 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const int row = wq * 32 + lane;
         const uint32_t stage = sStage + wq * C::kStageWarp;
-        uint32_t nit = 0;
         bool ok = true;
-        SpanPieces pieces{};
-        SpanWalk w;
-        span_walk_init<PAGED>(p, *sched, w);
-        SpanSeg g;
-        SpanItem it;
-        for (; ok && span_next<PAGED>(p, w, g, it); ++nit) {
-            const bool piece = g.j1 - g.j0 < it.n;
-            if (piece && g.j0 == 0) {
-                const long long end = span_first(*sched, (int)blockIdx.x + 1) + (it.n - g.j1);  // behind the item's last step
-                pieces = SpanPieces{span_cta_of(*sched, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, it.tok0,
-                                    it.ntok, g.q0, 0};
-            }
+        while (ok) {
+            ok = SEG_WAIT(warp_bwait);
+            volatile SpanSeg &g = SEG;
+            if (!ok || g.n == 0) break;
+            const bool piece = g.piece;
+            float *rec = p.rec + (size_t)g.slot * R::kFloats;
             auto row_dst = [&](int t, int rows) -> int64_t {
                 if (row >= rows) return -1;
                 const int r = PAGED ? row / p.G : row;
-                return span_out_offset<D, PAGED>(p, g.head, g.q0, it.tok0 + t * p.tile_tok + r, PAGED ? row - r * p.G : 0);
+                return span_out_offset<D, PAGED>(p, g.head, g.q0, g.tok0 + t * p.tile_tok + r, PAGED ? row - r * p.G : 0);
             };
             auto release_o = [&](int t) {  // O_t fully read: the next item may overwrite it
                 tc_fence_before();
@@ -829,7 +967,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (!any_row) return;
                 if (piece) {
                     if (dst < 0) return;
-                    float4 *o4 = reinterpret_cast<float4 *>(p.rec + (size_t)g.slot * R::kFloats) + (size_t)t * (D / 4) * 128;
+                    float4 *o4 = reinterpret_cast<float4 *>(rec) + (size_t)t * (D / 4) * 128;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         o4[(size_t)(c0 / 4 + q) * 128 + row] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
@@ -846,8 +984,8 @@ __global__ void __launch_bounds__(512, 1)
                     flush_block<true, 4>(p.out, stage, lane, dst, c0 / 64);
             };
             auto take_ml = [&](int t, float &l, float &m) {
-                ok = warp_bwait(BAR(BO_FINAL + t), nit & 1u, abort_flag, kSiteEpiO) &&
-                     warp_bwait(BAR(BL_FULL + t), nit & 1u, abort_flag, kSiteEpiL);
+                ok = warp_bwait(BAR(BO_FINAL + t), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     warp_bwait(BAR(BL_FULL + t), seg_it & 1u, abort_flag, kSiteEpiL);
                 if (!ok) return;
                 l = row_ml[t * 256 + row];
                 m = row_ml[t * 256 + 128 + row];
@@ -856,18 +994,17 @@ __global__ void __launch_bounds__(512, 1)
                 tc_fence_after();
             };
             auto put_ml = [&](int t, float m, float l) {
-                float *r = p.rec + (size_t)g.slot * R::kFloats + R::kML + t * 256 + row;
-                r[0] = m;
-                r[128] = l;
+                rec[R::kML + t * 256 + row] = m;
+                rec[R::kML + t * 256 + 128 + row] = l;
             };
-            if (it.dual) {
+            if (g.dual) {
                 float l0 = 0.f, m0 = 0.f, l1 = 0.f, m1 = 0.f;
                 take_ml(0, l0, m0);
                 if (ok) take_ml(1, l1, m1);
                 if (!ok) break;
-                const int rows = it.ntok * p.G;
+                const int rows = g.ntok * p.G;
                 const int64_t dst = row_dst(0, rows);
-                const bool any_row = wq * 32 < rows, two = g.j1 - g.j0 > 1;
+                const bool any_row = wq * 32 < rows, two = g.n > 1;
                 const float m = fmaxf(m0, m1);
                 float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
                 float a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
@@ -896,33 +1033,33 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 release_o(0);
                 release_o(1);
-                continue;
-            }
-            for (int t = 0; t < 2; ++t) {
-                float l = 0.f, m = 0.f;
-                take_ml(t, l, m);
-                if (!ok) break;
-                const int rows = min(it.ntok - t * p.tile_tok, p.tile_tok) * p.G;
-                const int64_t dst = row_dst(t, rows);
-                const bool any_row = wq * 32 < rows;
-                float inv = 1.f;
-                if (!piece)
-                    inv = l > 0.f ? 1.0f / l : 0.f;
-                else if (dst >= 0)
-                    put_ml(t, m, l);
+            } else {
+                for (int t = 0; t < 2; ++t) {
+                    float l = 0.f, m = 0.f;
+                    take_ml(t, l, m);
+                    if (!ok) break;
+                    const int rows = min(g.ntok - t * p.tile_tok, p.tile_tok) * p.G;
+                    const int64_t dst = row_dst(t, rows);
+                    const bool any_row = wq * 32 < rows;
+                    float inv = 1.f;
+                    if (!piece)
+                        inv = l > 0.f ? 1.0f / l : 0.f;
+                    else if (dst >= 0)
+                        put_ml(t, m, l);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    float f[32];
-                    tmem_ld32(tmem + lane_base + C::colO(t) + c0, o);
-                    if (c0 + 32 == D) release_o(t);
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        float f[32];
+                        tmem_ld32(tmem + lane_base + C::colO(t) + c0, o);
+                        if (c0 + 32 == D) release_o(t);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = u2f(o[i]) * inv;
-                    emit(t, c0, f, dst, any_row);
+                        for (int i = 0; i < 32; ++i) f[i] = u2f(o[i]) * inv;
+                        emit(t, c0, f, dst, any_row);
+                    }
                 }
             }
+            if (ok) SEG_DONE();
         }
-        if ((PAGED || p.rec) && warp == 12 && lane == 0) p.pieces[blockIdx.x] = ok ? pieces : SpanPieces{};
     }
 
     tc_fence_before();
@@ -932,6 +1069,11 @@ __global__ void __launch_bounds__(512, 1)
         tmem_dealloc(tmem, C::kTmemCols);
     }
 #undef BAR
+#undef SEG_FULL
+#undef SEG_EMPTY
+#undef SEG
+#undef SEG_WAIT
+#undef SEG_DONE
 }
 
 // Adds up the pieces of the item whose first piece is CTA blockIdx.x's last
