@@ -168,7 +168,7 @@ def _stream(stream, *tensors):
     for t in tensors:
         if hasattr(t, "is_cuda") and t.is_cuda:
             import torch
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(t.get_device())  # torch.cuda.current_stream, without its object
     return None
 
 

@@ -179,7 +179,8 @@ struct SpanParams {
     float scale_log2;
     int tile_tok;               // tokens of a query tile: 128 / G
     int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
-    int min_steps;              // fewest steps that a CTA is started for
+    int min_steps_log2;         // fewest steps that a CTA is started for
+    int merge_y;                // blocks per item in the merge
     float *rec;                 // workspace: 2 records a CTA (Rec<D>), then a SpanPieces a CTA; NULL: whole items
     SpanPieces *pieces;
 };

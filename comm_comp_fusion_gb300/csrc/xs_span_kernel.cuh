@@ -74,9 +74,12 @@ template <int D> struct SpanCfg : Cfg<D> {
 // One CTA's part of the steps, found by span_schedule.
 struct SpanSched {
     long long total, rem;  // steps of the call, of this CTA
-    int ctas;              // CTAs that share them
+    long long q;           // total / ctas, and the remainder
+    uint32_t r;
+    int ctas;              // CTAs that share the steps
     int seq, head, pair, j;
 };
+static_assert(sizeof(SpanSched) <= 64, "its place in shared memory");
 
 constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory
 
@@ -132,18 +135,18 @@ __device__ __forceinline__ void span_lengths(const SpanParams &p, int seq, int &
 }
 
 __device__ __forceinline__ int span_pairs(const SpanParams &p, int q_len) {
-    return (q_len + 2 * p.tile_tok - 1) / (2 * p.tile_tok);
-}
-
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
+    const int t2 = 2 * p.tile_tok;
+    return q_len <= t2 ? (q_len > 0) : (q_len + t2 - 1) / t2;
 }
 
 // Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
 // is a sequence (all its heads and query rows) or, for whole sequences, which
-// are all alike, a query tile pair.
+// are all alike, a query tile pair of one head. T: see span_schedule.
+template <typename T> __device__ __forceinline__ T warp_sum(T v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
 template <bool PAGED>
 __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane) {
     const int g = ch * 32 + lane;
@@ -166,20 +169,20 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
     return u;
 }
 
-// First step of CTA c's part, and the CTA whose part holds step u.
-__device__ __forceinline__ long long span_first(const SpanSched &s, int c) { return c * s.total / s.ctas; }
-__device__ __forceinline__ int span_cta_of(const SpanSched &s, long long u) {
-    return (int)(((u + 1) * s.ctas - 1) / s.total);
+// First step of CTA c's part: floor(c * total / ctas), with the quotient and
+// remainder of total / ctas (T is 32 bits wide unless the total is not).
+template <typename T> __device__ __forceinline__ T span_first(T q, uint32_t r, int ctas, int c) {
+    return (T)c * q + (T)((uint32_t)c * r / (uint32_t)ctas);
 }
 
 // In a run of 32 values (one per lane, in order) that start at step `base`, the
 // lane that holds step u, and the step its value starts at; base moves past the
 // run. -1: behind the run.
-__device__ __forceinline__ int span_locate(long long v, long long u, long long &base, long long &at, int lane) {
-    long long incl = v;
+template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &base, T &at, int lane) {
+    T incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        const T o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, base + incl > u);
@@ -189,68 +192,102 @@ __device__ __forceinline__ int span_locate(long long v, long long u, long long &
     return l;
 }
 
+// Where CTA c's part begins, by one warp. `mine`: the steps of this lane's group
+// in the only chunk, when there is one; otherwise the chunks' sums are in `sums`.
+template <typename T, bool PAGED>
+__device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, long long sum, long long mine, int chunks,
+                                          const long long *sums, int lane) {
+    const int c = (int)blockIdx.x;
+    const T total = (T)s.total, q = total / (T)s.ctas;
+    const uint32_t r = (uint32_t)(total - q * (T)s.ctas);
+    s.q = (long long)q;
+    s.r = r;
+    const T u0 = span_first<T>(q, r, s.ctas, c);
+    s.rem = (long long)(span_first<T>(q, r, s.ctas, c + 1) - u0);
+    T u = u0, base = 0, at = 0;
+    if (!PAGED) {
+        s.head = (int)(u0 / (T)sum);
+        u = u0 - (T)s.head * (T)sum;
+    }
+    int l = -1, ch = 0;
+    if (chunks > 1) {
+        for (; l < 0 && ch < chunks; ch += 32)
+            l = span_locate<T>(ch + lane < chunks ? (T)sums[ch + lane] : (T)0, u, base, at, lane);
+        ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
+        base = at;
+        mine = span_group_steps<PAGED>(p, ch, lane);
+    }
+    l = span_locate<T>((T)mine, u, base, at, lane);
+    u -= at;
+    if (!PAGED) {
+        s.pair = ch * 32 + l;
+        s.j = (int)u;
+        return;
+    }
+    s.seq = ch * 32 + l;
+    int q0, q_len, keys;
+    span_lengths<true>(p, s.seq, q0, q_len, keys);
+    const int np = span_pairs(p, q_len);
+    if (np == 1) {
+        const T n = (T)span_item(p, q_len, keys, 0).n;
+        s.head = (int)(u / n);
+        s.j = (int)(u - (T)s.head * n);
+        return;
+    }
+    T per_head = 0;
+    for (int i = lane; i < np; i += 32) per_head += (T)span_item(p, q_len, keys, i).n;
+    per_head = warp_sum(per_head);
+    s.head = (int)(u / per_head);
+    u -= (T)s.head * per_head;
+    base = 0;
+    l = -1;
+    int i = 0;
+    for (; l < 0 && i < np; i += 32)
+        l = span_locate<T>(i + lane < np ? (T)span_item(p, q_len, keys, i + lane).n : (T)0, u, base, at, lane);
+    s.pair = i - 32 + l;
+    s.j = (int)(u - at);
+}
+
 // Every CTA: the call's steps, how many CTAs share them and where this CTA's part
-// starts. `scratch` holds kSpanMaxChunks sums. Called by all threads, leaves
-// them synchronised.
+// starts, in *out. `sums` holds kSpanMaxChunks sums. Called by all threads and
+// followed by a barrier. One warp does it all while there are few groups.
 template <bool PAGED>
-__device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *out, long long *scratch) {
+__device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *out, long long *sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int groups = PAGED ? p.N : p.n_pairs, chunks = (groups + 31) / 32;
-    for (int ch = warp; ch < chunks; ch += warps) {
-        const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
-        if (lane == 0) scratch[ch] = s;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        long long sum = 0;
-        for (int ch = lane; ch < chunks; ch += 32) sum += scratch[ch];
-        sum = warp_sum(sum);
-        SpanSched s;
-        s.total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
-        s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total / p.min_steps));
-        const int c = (int)blockIdx.x;
-        s.rem = 0;
-        s.seq = s.head = s.pair = s.j = 0;
-        if (c < s.ctas && s.total > 0) {
-            const long long u0 = span_first(s, c);
-            s.rem = span_first(s, c + 1) - u0;
-            long long u = u0, base = 0, at = 0;
-            if (!PAGED) {
-                s.head = (int)(u0 / sum);
-                u = u0 - s.head * sum;
-            }
-            int l = -1, ch = 0;
-            for (; l < 0 && ch < chunks; ch += 32)
-                l = span_locate(ch + lane < chunks ? scratch[ch + lane] : 0ll, u, base, at, lane);
-            ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
-            base = at;
-            l = span_locate(span_group_steps<PAGED>(p, ch, lane), u, base, at, lane);
-            if (!PAGED) {
-                s.pair = ch * 32 + l;
-                s.j = (int)(u - at);
-            } else {
-                s.seq = ch * 32 + l;
-                int q0, q_len, keys;
-                span_lengths<true>(p, s.seq, q0, q_len, keys);
-                const int np = span_pairs(p, q_len);
-                long long per_head = 0;
-                for (int i = lane; i < np; i += 32) per_head += span_item(p, q_len, keys, i).n;
-                per_head = warp_sum(per_head);
-                u -= at;
-                s.head = (int)(u / per_head);
-                u -= s.head * per_head;
-                base = 0;
-                l = -1;
-                int i = 0;
-                for (; l < 0 && i < np; i += 32)
-                    l = span_locate(i + lane < np ? (long long)span_item(p, q_len, keys, i + lane).n : 0ll, u, base, at, lane);
-                s.pair = i - 32 + l;
-                s.j = (int)(u - at);
-            }
+    if (chunks > 1) {
+        for (int ch = warp; ch < chunks; ch += warps) {
+            const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
+            if (lane == 0) sums[ch] = s;
         }
-        if (lane == 0) *out = s;
+        __syncthreads();
     }
-    __syncthreads();
+    if (warp != 3) return;
+    long long mine = 0, sum = 0;
+    if (chunks > 1) {
+        for (int ch = lane; ch < chunks; ch += 32) sum += sums[ch];
+    } else {
+        sum = mine = span_group_steps<PAGED>(p, 0, lane);
+    }
+    sum = warp_sum(sum);
+    SpanSched s;
+    s.total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
+    s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total >> p.min_steps_log2));
+    s.rem = s.q = 0;
+    s.r = 0;
+    s.seq = s.head = s.pair = s.j = 0;
+    if ((int)blockIdx.x < s.ctas && s.total > 0) {
+        if (s.total < (1ll << 31))
+            span_find<uint32_t, PAGED>(p, s, sum, mine, chunks, sums, lane);
+        else
+            span_find<unsigned long long, PAGED>(p, s, sum, mine, chunks, sums, lane);
+    }
+    if (lane == 0) *out = s;
+}
+
+// The CTA whose part holds step u.
+__device__ __forceinline__ int span_cta_of(const SpanSched &s, long long u) {
+    return (int)(((u + 1) * s.ctas - 1) / s.total);
 }
 
 // The walk through a CTA's part, one stretch (segment) of an item at a time.
@@ -443,6 +480,7 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
     const int wg = warp >> 2;
+    if (PAGED || p.rec) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // span_merge_kernel may be set up
     // The roles walk the ring of segments alike.
     uint32_t seg_it = 0;
 #define SEG (segs[seg_it % kSegs])
@@ -467,7 +505,8 @@ __global__ void __launch_bounds__(512, 1)
                 if (!more) g.n = 0;
                 if (more && g.piece && g.j0 == 0) {  // its first piece: this CTA's last segment
                     const int left = g.nw + g.ns - g.n;
-                    const long long end = span_first(*sched, (int)blockIdx.x + 1) + left;  // behind the item's last step
+                    const long long end = span_first<unsigned long long>(sched->q, sched->r, sched->ctas, (int)blockIdx.x + 1) +
+                                          left;  // behind the item's last step
                     pieces = SpanPieces{span_cta_of(*sched, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, g.tok0,
                                         g.ntok, g.q0, 0};
                 }
@@ -1083,6 +1122,7 @@ __global__ void __launch_bounds__(512, 1)
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__ SpanParams p) {
     using R = Rec<D>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the attention kernel is done from here on
     const SpanPieces s = p.pieces[blockIdx.x];
     if (s.pieces < 2) return;
     const int rows0 = min(s.ntok, p.tile_tok) * p.G;  // rows of the first tile
@@ -1148,8 +1188,17 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
     kern<<<grid, 512, SpanCfg<D>::kSmemAlloc, stream>>>(maps, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.rec) {
-        span_merge_kernel<D, PAGED><<<dim3((unsigned)grid, 8), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
+        // set up while the attention kernel still runs; it waits for its end itself
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)grid, (unsigned)p.merge_y);
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, span_merge_kernel<D, PAGED>, p);
     }
     return e;
 }
