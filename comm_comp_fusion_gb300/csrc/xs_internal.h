@@ -178,6 +178,7 @@ struct SpanParams {
     int left, right, sinks;     // at most 2^29 each
     float scale_log2;
     int tile_tok;               // tokens of a query tile: 128 / G
+    uint32_t g_magic;           // row / G = row * g_magic >> 16 for rows below 128: ceil(2^16 / G)
     int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
     int min_steps_log2;         // fewest steps that a CTA is started for
     int merge_y;                // blocks per item in the merge

@@ -358,6 +358,7 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
     p.max_pages = max_pages;
     p.scale_log2 = scale_log2(scale);
     p.tile_tok = 128 / p.G;
+    p.g_magic = (65536u + (uint32_t)p.G - 1u) / (uint32_t)p.G;
     p.heads = Hk;
     span_workspace_parts(workspace, D, sms, &p);
     SpanMaps maps;

@@ -56,18 +56,33 @@
 
 namespace xs {
 
-// Further barriers: the issuer asks warp 3 to clear a V tile's end, and its
-// answer; the ring of segments (kSegs full, kSegs empty).
-constexpr int kSegs = 6;
-enum : int { BFIX_ASK = 26, BFIX_DONE = 27, BSEG = 32 };
+constexpr int kSegs = 6;  // segments in the ring
+// mbarriers; per query tile (chain) 2 of each of the first eight, per ring slot 2, per segment 2.
+enum : int {
+    SPQ_FULL = 0, SPQ_EMPTY = 2, SPS_FULL = 4, SPP_FULL = 6, SPO_FINAL = 8, SPO_FREE = 10, SPL_FULL = 12, SPL_EMPTY = 14,
+    SP_DRAIN = 16, SPFIX_ASK = 17, SPFIX_DONE = 18,  // the issuer asks warp 3 to clear a V tile's end, and its answer
+    SPKV_FULL = 19, SPKV_EMPTY = 27, SPSEG_FULL = 35, SPSEG_EMPTY = 35 + kSegs, SP_BARS = 35 + 2 * kSegs
+};
 enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 
-template <int D> struct SpanCfg : Cfg<D> {
-    using C = Cfg<D>;
-    static constexpr uint32_t kOffSched = C::kSmemUsed;      // SpanSched
-    static constexpr uint32_t kOffSegBar = kOffSched + 64;   // the segment ring's barriers
-    static constexpr uint32_t kOffSeg = kOffSegBar + 128;    // the segments
-    static constexpr uint32_t kSmemAlloc = kOffSeg + 96 * kSegs + 1024;
+template <int D> struct SpanCfg {
+    static constexpr int kNDB = Cfg<D>::kNDB;
+    static constexpr uint32_t kBlk = Cfg<D>::kBlk, kTile = Cfg<D>::kTile;
+    // K/V ring: 128 KB in 16 KB (D = 64) or 32 KB slots. Single new tokens stream K/V at
+    // the rate of what is in flight: with four 16 KB slots D = 64 reached 3.9 TB/s.
+    static constexpr int kSlots = D == 64 ? 8 : 4;
+    static constexpr uint32_t kOffQ = 0;
+    static constexpr uint32_t kOffKV = 2 * kTile;
+    static constexpr uint32_t kOffStage = kOffKV + kSlots * kTile;
+    static constexpr uint32_t kStageWarp = Cfg<D>::kStageWarp;
+    static constexpr uint32_t kOffBar = kOffStage + 4 * kStageWarp;
+    static constexpr uint32_t kOffL = kOffBar + 8 * ((SP_BARS + 1) & ~1);  // float [tile][l, m][128]
+    static constexpr uint32_t kOffMisc = kOffL + 2 * 2 * 128 * 4;          // tmem base, abort flag
+    static constexpr uint32_t kOffSeg = kOffMisc + 16;                     // the ring of segments, then a SpanSched
+    static constexpr uint32_t kSmemAlloc = kOffSeg + 96 * kSegs + 64 + 1024;
+    __host__ __device__ static constexpr uint32_t colS(int t) { return 128u * (uint32_t)t; }
+    __host__ __device__ static constexpr uint32_t colO(int t) { return 256u + (uint32_t)D * (uint32_t)t; }
+    static constexpr uint32_t kTmemCols = 512;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
 };
 
@@ -248,21 +263,19 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, lon
     s.j = (int)(u - at);
 }
 
-// Every CTA: the call's steps, how many CTAs share them and where this CTA's part
-// starts, in *out. `sums` holds kSpanMaxChunks sums. Called by all threads and
-// followed by a barrier. One warp does it all while there are few groups.
-template <bool PAGED>
-__device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *out, long long *sums) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int groups = PAGED ? p.N : p.n_pairs, chunks = (groups + 31) / 32;
-    if (chunks > 1) {
-        for (int ch = warp; ch < chunks; ch += warps) {
-            const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
-            if (lane == 0) sums[ch] = s;
-        }
-        __syncthreads();
+// Sums of the steps of 32 groups each, when there are more; by all threads, and
+// followed by a barrier.
+template <bool PAGED> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int ch = warp; ch < chunks; ch += (int)(blockDim.x >> 5)) {
+        const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
+        if (lane == 0) sums[ch] = s;
     }
-    if (warp != 3) return;
+}
+
+// The call's steps, how many CTAs share them and where this CTA's part starts; by one warp.
+template <bool PAGED>
+__device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chunks, const long long *sums, int lane) {
     long long mine = 0, sum = 0;
     if (chunks > 1) {
         for (int ch = lane; ch < chunks; ch += 32) sum += sums[ch];
@@ -282,7 +295,7 @@ __device__ __forceinline__ void span_schedule(const SpanParams &p, SpanSched *ou
         else
             span_find<unsigned long long, PAGED>(p, s, sum, mine, chunks, sums, lane);
     }
-    if (lane == 0) *out = s;
+    return s;
 }
 
 // The CTA whose part holds step u.
@@ -309,7 +322,9 @@ struct SpanSeg {
     int slot;            // workspace record of a piece
     int fix;             // rows of the first V tile that hold keys, where the rest has to be cleared; -1: nothing to do
     int lo, last;        // first key of the window, last key that any token sees
-    int pad[4];
+    // a row of tile t misses a key of the K/V tile at c0 iff c0 > all_hi[t], or
+    // c0 < all_lo[t] and the tile's keys are not all sinks
+    int all_hi[2], all_lo[2];
 };
 static_assert(sizeof(SpanSeg) == 96, "segment ring");
 __device__ __forceinline__ int span_tile(const volatile SpanSeg &g, int y) {
@@ -385,10 +400,20 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, Span
         w.pair = (int)(item - (long long)w.head * p.n_pairs);
     }
     g.piece = g.n < it.n;
+    for (int t = 0; t < 2; ++t) {
+        const int tt = it.dual ? 0 : t * p.tile_tok, toks = min(it.ntok - tt, p.tile_tok);
+        g.all_hi[t] = min(it.pos0 + tt + p.right, w_keys - 1) - 127;
+        g.all_lo[t] = it.pos0 + tt + toks - 1 - p.left;
+    }
     // rows behind the last key, in a box that holds keys (boxes without are zeros)
     const int box = PAGED ? min(p.page, 128) : 128;
     g.fix = PAGED && g.j0 == 0 && it.hi == w_keys >> 7 && (w_keys & (box - 1)) ? w_keys & 127 : -1;
     return true;
+}
+
+// row / G of a query tile's row
+template <bool PAGED> __device__ __forceinline__ int span_row_tok(const SpanParams &p, int row) {
+    return PAGED ? (int)((uint32_t)row * p.g_magic >> 16) : row;
 }
 
 // Element offset of the output row of token `tok` (of the sequence's new tokens,
@@ -431,34 +456,33 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
     const uint32_t sQ = base + C::kOffQ, sKV = base + C::kOffKV, sStage = base + C::kOffStage;
-    const uint32_t sBar = base + C::kOffBar, sSegBar = base + C::kOffSegBar;
+    const uint32_t sBar = base + C::kOffBar;
     float *row_ml = reinterpret_cast<float *>(sm + C::kOffL);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + C::kOffMisc);
     volatile uint32_t *abort_flag = misc + 1;
-    SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSched);
     volatile SpanSeg *segs = reinterpret_cast<volatile SpanSeg *>(sm + C::kOffSeg);
 #define BAR(i) (sBar + 8u * (uint32_t)(i))
-#define SEG_FULL(i) (sSegBar + 8u * (uint32_t)(i))
-#define SEG_EMPTY(i) (sSegBar + 8u * (uint32_t)(kSegs + (i)))
+#define SEG_FULL(i) BAR(SPSEG_FULL + (i))
+#define SEG_EMPTY(i) BAR(SPSEG_EMPTY + (i))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(BAR(BQ_FULL + t), 1);
-            mbar_init(BAR(BQ_EMPTY + t), 1);
-            mbar_init(BAR(BS_FULL + t), 1);
-            mbar_init(BAR(BP_FULL + t), 4);
-            mbar_init(BAR(BO_FINAL + t), 1);
-            mbar_init(BAR(BO_FREE + t), 4);
-            mbar_init(BAR(BL_FULL + t), 4);
-            mbar_init(BAR(BL_EMPTY + t), 4);
+            mbar_init(BAR(SPQ_FULL + t), 1);
+            mbar_init(BAR(SPQ_EMPTY + t), 1);
+            mbar_init(BAR(SPS_FULL + t), 1);
+            mbar_init(BAR(SPP_FULL + t), 4);
+            mbar_init(BAR(SPO_FINAL + t), 1);
+            mbar_init(BAR(SPO_FREE + t), 4);
+            mbar_init(BAR(SPL_FULL + t), 4);
+            mbar_init(BAR(SPL_EMPTY + t), 4);
         }
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(BAR(BKV_FULL + s), 1);
-            mbar_init(BAR(BKV_EMPTY + s), 1);
+            mbar_init(BAR(SPKV_FULL + s), 1);
+            mbar_init(BAR(SPKV_EMPTY + s), 1);
         }
-        mbar_init(BAR(B_DRAIN), 1);
-        mbar_init(BAR(BFIX_ASK), 1);
-        mbar_init(BAR(BFIX_DONE), 1);
+        mbar_init(BAR(SP_DRAIN), 1);
+        mbar_init(BAR(SPFIX_ASK), 1);
+        mbar_init(BAR(SPFIX_DONE), 1);
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(SEG_FULL(s), 1);
             mbar_init(SEG_EMPTY(s), PAGED ? 15 : 14);  // producer, issuer, (V clearing,) 8 softmax warps, 4 epilogue warps
@@ -473,8 +497,19 @@ __global__ void __launch_bounds__(512, 1)
         tmem_alloc(smem_u32(misc), C::kTmemCols);
         tmem_relinquish();
     }
-    if (PAGED || p.rec)
-        span_schedule<PAGED>(p, sched, reinterpret_cast<long long *>(sm + C::kOffStage));
+    const int chunks = ((PAGED ? p.N : p.n_pairs) + 31) / 32;
+    long long *sums = reinterpret_cast<long long *>(sm + C::kOffStage);
+    SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSeg + 96 * kSegs);
+    if (PAGED || p.rec) {
+        if (chunks > 1) {
+            span_chunk_sums<PAGED>(p, chunks, sums);
+            __syncthreads();
+        }
+        if (warp == 3) {  // here, not by warp 2 in its role: with 48 registers it takes twice as long
+            const SpanSched s = span_schedule<PAGED>(p, chunks, sums, lane);
+            if (lane == 0) *sched = s;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -533,6 +568,10 @@ __global__ void __launch_bounds__(512, 1)
                     d.fix = g.fix;
                     d.lo = g.lo;
                     d.last = g.last;
+                    for (int t = 0; t < 2; ++t) {
+                        d.all_hi[t] = g.all_hi[t];
+                        d.all_lo[t] = g.all_lo[t];
+                    }
                     mbar_arrive(SEG_FULL(seg_it % kSegs));
                 }
             }
@@ -549,18 +588,18 @@ __global__ void __launch_bounds__(512, 1)
                 if (!ok || n == 0) break;
                 const bool dual = g.dual;
                 for (int t = 0; t < (dual ? 1 : 2) && ok; ++t) {
-                    ok = warp_bwait(BAR(BQ_EMPTY + t), ((t ? q_it1++ : q_it0++) & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+                    ok = warp_bwait(BAR(SPQ_EMPTY + t), ((t ? q_it1++ : q_it0++) & 1u) ^ 1u, abort_flag, kSiteLoadQ);
                     if (!ok) break;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(BAR(BQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
+                        mbar_arrive_expect_tx(BAR(SPQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
                         const int tok = g.q0 + g.tok0 + t * p.tile_tok;
 #pragma unroll
                         for (int db = 0; db < C::kNDB; ++db) {
                             const uint32_t dst = sQ + t * C::kTile + db * C::kBlk;
                             if (PAGED)
-                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, 0, head, tok);
+                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, 0, head, tok);
                             else
-                                tma_load_4d(dst, &tm.q, BAR(BQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
+                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
                         }
                     }
                 }
@@ -577,10 +616,10 @@ __global__ void __launch_bounds__(512, 1)
                 };
                 auto load_tile = [&](const CUtensorMap *m, int x, int page) {
                     const uint32_t slot = kv_it % C::kSlots, ph = (kv_it / C::kSlots) & 1u;
-                    ok = warp_bwait(BAR(BKV_EMPTY + slot), ph ^ 1u, abort_flag, kSiteLoadKV);
+                    ok = warp_bwait(BAR(SPKV_EMPTY + slot), ph ^ 1u, abort_flag, kSiteLoadKV);
                     if (!ok) return;
                     ++kv_it;
-                    if (lane == 0) mbar_arrive_expect_tx(BAR(BKV_FULL + slot), C::kTile);
+                    if (lane == 0) mbar_arrive_expect_tx(BAR(SPKV_FULL + slot), C::kTile);
                     __syncwarp();
                     const int tile = span_tile(g, j0 + x);
                     if (PAGED) {
@@ -589,10 +628,10 @@ __global__ void __launch_bounds__(512, 1)
                             const uint32_t dst = sKV + slot * C::kTile + (uint32_t)(lane * box) * 128u;
 #pragma unroll
                             for (int db = 0; db < C::kNDB; ++db)
-                                tma_load_4d(dst + db * C::kBlk, m, BAR(BKV_FULL + slot), db * 64, head, row, page);
+                                tma_load_4d(dst + db * C::kBlk, m, BAR(SPKV_FULL + slot), db * 64, head, row, page);
                         }
                     } else if (lane < C::kNDB) {
-                        tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(BKV_FULL + slot), lane * 64,
+                        tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(SPKV_FULL + slot), lane * 64,
                                     head % p.Hl, tile * 128, head / p.Hl);
                     }
                 };
@@ -626,7 +665,7 @@ __global__ void __launch_bounds__(512, 1)
                 const uint32_t slot = (kv_it + (SEG.dual && n > 1 ? 2u : 1u)) % C::kSlots;
                 kv_it += 2u * (uint32_t)n;
                 if (rows >= 0) {
-                    if (!warp_bwait(BAR(BFIX_ASK), fph, abort_flag, kSiteFix)) break;  // the tile is in
+                    if (!warp_bwait(BAR(SPFIX_ASK), fph, abort_flag, kSiteFix)) break;  // the tile is in
                     fph ^= 1u;
                     for (int r = rows * 8 + lane; r < ((rows + box - 1) / box * box) * 8; r += 32)
 #pragma unroll
@@ -634,7 +673,7 @@ __global__ void __launch_bounds__(512, 1)
                             st_shared_v4(sKV + slot * C::kTile + db * C::kBlk + (uint32_t)r * 16u, 0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(BFIX_DONE));
+                    if (lane == 0) mbar_arrive(BAR(SPFIX_DONE));
                 }
                 SEG_DONE();
             }
@@ -652,7 +691,7 @@ __global__ void __launch_bounds__(512, 1)
                     const uint32_t off = ((kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4;
                     tc_mma_ss(d, qa + off, ka + off, idS, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(BAR(BS_FULL + t));
+                tc_commit(BAR(SPS_FULL + t));
             };
             auto issue_PV = [&](int t, uint32_t slot, bool acc) {
                 const uint64_t va = dV + (opaque(sKV + slot * C::kTile) >> 4);
@@ -665,12 +704,12 @@ __global__ void __launch_bounds__(512, 1)
             bool ok = true;
             auto wait_kv = [&](uint32_t &slot) {
                 slot = kv_it % C::kSlots;
-                ok = ok && bwait(BAR(BKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
+                ok = ok && bwait(BAR(SPKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
                 ++kv_it;
             };
             auto wait_p = [&](int t, bool first) {  // P_t is in (and, at a tile's first step, O_t is free)
-                ok = bwait(BAR(BP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
-                if (ok && first) ok = bwait(BAR(BO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                ok = bwait(BAR(SPP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
+                if (ok && first) ok = bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
                 if (t)
                     pph1 ^= 1u;
                 else
@@ -680,14 +719,14 @@ __global__ void __launch_bounds__(512, 1)
             auto wait_v = [&](uint32_t &slot, bool fix) {
                 wait_kv(slot);
                 if (ok && fix) {
-                    mbar_arrive(BAR(BFIX_ASK));
-                    ok = bwait(BAR(BFIX_DONE), fph, abort_flag, kSiteFix);
+                    mbar_arrive(BAR(SPFIX_ASK));
+                    ok = bwait(BAR(SPFIX_DONE), fph, abort_flag, kSiteFix);
                     fph ^= 1u;
                 }
             };
             auto no_steps = [&](int t) {  // a tile or chain without a step in this segment
-                ok = bwait(BAR(BO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
-                if (ok) tc_commit(BAR(BO_FINAL + t));
+                ok = bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                if (ok) tc_commit(BAR(SPO_FINAL + t));
             };
             while (ok) {
                 ok = SEG_WAIT(bwait);
@@ -696,42 +735,42 @@ __global__ void __launch_bounds__(512, 1)
                 if (!ok || n == 0) break;
                 const bool fix = PAGED && g.fix >= 0;
                 uint32_t ks, vs;
-                ok = bwait(BAR(BQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
+                ok = bwait(BAR(SPQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
                 if (g.dual) {
                     // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
                     wait_kv(ks);
                     if (!ok) break;
                     tc_fence_after();
                     issue_S(0, 0, ks);
-                    tc_commit(BAR(BKV_EMPTY + ks));
+                    tc_commit(BAR(SPKV_EMPTY + ks));
                     if (n > 1) {
                         wait_kv(ks);
                         if (!ok) break;
                         tc_fence_after();
                         issue_S(1, 0, ks);
-                        tc_commit(BAR(BKV_EMPTY + ks));
+                        tc_commit(BAR(SPKV_EMPTY + ks));
                     }
-                    if (n <= 2) tc_commit(BAR(BQ_EMPTY + 0));
+                    if (n <= 2) tc_commit(BAR(SPQ_EMPTY + 0));
                     for (int x = 0; x < n; ++x) {
                         const int t = x & 1;
                         wait_v(vs, fix && x == 0);
                         if (ok) wait_p(t, x < 2);
                         if (!ok) break;
                         issue_PV(t, vs, x >= 2);
-                        tc_commit(BAR(BKV_EMPTY + vs));
-                        if (x + 2 >= n) tc_commit(BAR(BO_FINAL + t));
+                        tc_commit(BAR(SPKV_EMPTY + vs));
+                        if (x + 2 >= n) tc_commit(BAR(SPO_FINAL + t));
                         if (x + 2 < n) {
                             wait_kv(ks);
                             if (!ok) break;
                             tc_fence_after();
                             issue_S(t, 0, ks);
-                            tc_commit(BAR(BKV_EMPTY + ks));
-                            if (x + 3 == n) tc_commit(BAR(BQ_EMPTY + 0));
+                            tc_commit(BAR(SPKV_EMPTY + ks));
+                            if (x + 3 == n) tc_commit(BAR(SPQ_EMPTY + 0));
                         }
                     }
                     if (ok && n == 1) no_steps(1);
                 } else {
-                    if (ok) ok = bwait(BAR(BQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
+                    if (ok) ok = bwait(BAR(SPQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
                     // steps (of the segment) of tile 0: from f0 on; of tile 1: below l1 and from m1 on
                     const int f0 = max(g.s0 - g.j0, 0), l1 = min(g.e1 - g.j0, n), m1 = max(g.nw - g.j0, 0);
                     auto on1 = [&](int x) { return x < l1 || x >= m1; };
@@ -741,10 +780,10 @@ __global__ void __launch_bounds__(512, 1)
                     tc_fence_after();
                     if (f0 == 0) issue_S(0, 0, ks);
                     if (on1(0)) issue_S(1, 1, ks);
-                    tc_commit(BAR(BKV_EMPTY + ks));
+                    tc_commit(BAR(SPKV_EMPTY + ks));
                     if (n == 1) {
-                        tc_commit(BAR(BQ_EMPTY + 0));
-                        tc_commit(BAR(BQ_EMPTY + 1));
+                        tc_commit(BAR(SPQ_EMPTY + 0));
+                        tc_commit(BAR(SPQ_EMPTY + 1));
                     }
                     for (int x = 0; x < n; ++x) {
                         const bool more = x + 1 < n;
@@ -754,7 +793,7 @@ __global__ void __launch_bounds__(512, 1)
                             wait_p(0, x == f0);
                             if (!ok) break;
                             issue_PV(0, vs, x > f0);
-                            if (!more) tc_commit(BAR(BO_FINAL + 0));
+                            if (!more) tc_commit(BAR(SPO_FINAL + 0));
                         }
                         if (more) {
                             wait_kv(ks);
@@ -766,15 +805,15 @@ __global__ void __launch_bounds__(512, 1)
                             wait_p(1, x == first1);
                             if (!ok) break;
                             issue_PV(1, vs, x > first1);
-                            if (x == last1) tc_commit(BAR(BO_FINAL + 1));
+                            if (x == last1) tc_commit(BAR(SPO_FINAL + 1));
                         }
-                        tc_commit(BAR(BKV_EMPTY + vs));
+                        tc_commit(BAR(SPKV_EMPTY + vs));
                         if (more) {
                             if (on1(x + 1)) issue_S(1, 1, ks);
-                            tc_commit(BAR(BKV_EMPTY + ks));
+                            tc_commit(BAR(SPKV_EMPTY + ks));
                             if (x + 2 == n) {
-                                tc_commit(BAR(BQ_EMPTY + 0));
-                                tc_commit(BAR(BQ_EMPTY + 1));
+                                tc_commit(BAR(SPQ_EMPTY + 0));
+                                tc_commit(BAR(SPQ_EMPTY + 1));
                             }
                         }
                     }
@@ -784,10 +823,10 @@ __global__ void __launch_bounds__(512, 1)
                 if (ok) SEG_DONE();
             }
             if (!ok) {  // wait (bounded) for MMAs in flight before tensor memory is released
-                tc_commit(BAR(B_DRAIN));
+                tc_commit(BAR(SP_DRAIN));
                 uint32_t dummy = 0;
                 const unsigned long long t0 = globaltimer_ns();
-                while (!mbar_try_wait(BAR(B_DRAIN), 0) && globaltimer_ns() - t0 < 200000000ull) ++dummy;
+                while (!mbar_try_wait(BAR(SP_DRAIN), 0) && globaltimer_ns() - t0 < 200000000ull) ++dummy;
             }
         }
         __syncwarp();
@@ -806,20 +845,18 @@ __global__ void __launch_bounds__(512, 1)
             ok = SEG_WAIT(warp_bwait);
             volatile SpanSeg &g = SEG;
             if (!ok || g.n == 0) break;
-            const int tt = g.dual ? 0 : t * p.tile_tok;  // tokens before this tile
-            const int toks = min(g.ntok - tt, p.tile_tok);
-            // places of this row's token, and the first and last key it may see
-            const int pos = g.pos0 + tt + (PAGED ? row / p.G : row);
-            const bool row_ok = row < toks * p.G;
-            const int row_lo = max(0, pos - p.left), row_hi = min(pos + p.right, g.keys - 1);
-            const bool idle = (warp & 3) * 32 >= toks * p.G;  // no row of this warp exists
-            float m = -INFINITY, l = 0.f;
-            bool first = true;
+            // lim: the row sum that calls for the row max again: none for a row that does
+            // not exist, any for one that has not seen a key yet
+            float m = -INFINITY, l = 0.f, lim;
+            bool idle, first = true;
+            {
+                const int rows = min(g.ntok - (g.dual ? 0 : t * p.tile_tok), p.tile_tok) * p.G;
+                lim = row < rows ? -1.f : INFINITY;
+                idle = (warp & 3) * 32 >= rows;  // no row of this warp exists
+            }
             // This tile's (chain's) steps and K/V tiles: c, c - step, ... down to c_end, then
-            // the sinks' from ns - 1 on. Some row misses a key of tile c if its keys pass
-            // all_hi, or begin before all_lo without being sinks.
+            // the sinks' from ns - 1 on.
             int steps, c, c_end = g.hi - g.nw + 1;
-            const int step = g.dual ? 2 : 1;
             {
                 const int n = g.n, j0 = g.j0, nw = g.nw;
                 int y = j0;  // the first step's
@@ -838,21 +875,20 @@ __global__ void __launch_bounds__(512, 1)
                 c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
                 if (y >= nw) c_end = INT_MIN;
             }
-            const int all_hi = min(g.pos0 + tt + p.right, g.keys - 1) - 127, all_lo = g.pos0 + tt + toks - 1 - p.left;
 #pragma unroll 1
             for (; steps > 0; --steps) {
                 const int c0 = c * 128;
-                const bool masked = c0 > all_hi || (c0 < all_lo && c0 + 128 > p.sinks);
-                c -= step;
+                const bool masked = c0 > g.all_hi[t] || (c0 < g.all_lo[t] && c0 + 128 > p.sinks);
+                c -= 1 + g.dual;
                 if (c < c_end) {
                     c += g.ns - c_end;
                     c_end = INT_MIN;
                 }
-                ok = warp_bwait(BAR(BS_FULL + t), sph, abort_flag, kSiteSoftS);
+                ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                 if (!ok) break;
                 sph ^= 1u;
                 if (idle) {  // P keeps what S left there: only rows that do not exist read it
-                    if (lane == 0) mbar_arrive(BAR(BP_FULL + t));
+                    if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
                     continue;
                 }
                 tc_fence_after();
@@ -864,9 +900,13 @@ __global__ void __launch_bounds__(512, 1)
                     tmem_ld64x2(tS, sa, sb);
                     if (masked) {
                         const uint32_t ninf = f2u(-INFINITY);
+                        // places of this row's token and of the last key it may see
+                        const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
+                        const int row_hi = min(pos + p.right, g.keys - 1);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            const uint32_t bits = span_mask_word(row_lo - c0, row_hi - c0, p.sinks - c0, 32 * h);
+                            const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, 32 * h);
+                            if (__all_sync(0xffffffffu, bits == ~0u)) continue;  // a mask's edge crosses one or two of the four
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 uint32_t &s = h < 2 ? sa[(h & 1) * 32 + i] : sb[(h & 1) * 32 + i];
@@ -920,20 +960,24 @@ __global__ void __launch_bounds__(512, 1)
                     lstep = a0 + a1;
                 };
                 load_scores();
-                if (first) m = row_max();
+                if (first) {
+                    m = row_max();
+                    if (lim < 0.f && m > -INFINITY) lim = kSpanRise;
+                }
                 exps();
                 // The row max is taken at the first step and then kept while no row sum
                 // passes kSpanRise: p, l and O are floating point, so a maximum that lags by
                 // up to 2^14 costs no precision, and a first tile with only a few keys in it
                 // (a causal diagonal) seldom has to be put right. A row that has not seen a
                 // key before takes its max at the first step where it does.
-                if (!first && __any_sync(0xffffffffu, row_ok && (m == -INFINITY || !(lstep <= kSpanRise)))) {
+                if (!first && __any_sync(0xffffffffu, lstep > lim)) {
                     load_scores();
                     const float mnew = row_max();
                     float alpha = 1.f;
                     if (mnew > m) {
                         alpha = ex2_approx(m - mnew);
                         m = mnew;
+                        if (lim < 0.f) lim = kSpanRise;
                     }
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
                         // The commit that signalled S_t for this step also covers the
@@ -966,15 +1010,15 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(BP_FULL + t));
+                if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
             }
             if (!ok) break;
-            ok = warp_bwait(BAR(BL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
+            ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
             if (!ok) break;
             row_ml[t * 256 + row] = l;
             row_ml[t * 256 + 128 + row] = m;
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(BL_FULL + t));
+            if (lane == 0) mbar_arrive(BAR(SPL_FULL + t));
             SEG_DONE();
         }
     } else {
@@ -993,13 +1037,13 @@ __global__ void __launch_bounds__(512, 1)
             float *rec = p.rec + (size_t)g.slot * R::kFloats;
             auto row_dst = [&](int t, int rows) -> int64_t {
                 if (row >= rows) return -1;
-                const int r = PAGED ? row / p.G : row;
+                const int r = span_row_tok<PAGED>(p, row);
                 return span_out_offset<D, PAGED>(p, g.head, g.q0, g.tok0 + t * p.tile_tok + r, PAGED ? row - r * p.G : 0);
             };
             auto release_o = [&](int t) {  // O_t fully read: the next item may overwrite it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(BO_FREE + t));
+                if (lane == 0) mbar_arrive(BAR(SPO_FREE + t));
             };
             // one tile's 32 columns from c0 on (f: its factors) to the output or the record
             auto emit = [&](int t, int c0, const float (&f)[32], int64_t dst, bool any_row) {
@@ -1023,13 +1067,13 @@ __global__ void __launch_bounds__(512, 1)
                     flush_block<true, 4>(p.out, stage, lane, dst, c0 / 64);
             };
             auto take_ml = [&](int t, float &l, float &m) {
-                ok = warp_bwait(BAR(BO_FINAL + t), seg_it & 1u, abort_flag, kSiteEpiO) &&
-                     warp_bwait(BAR(BL_FULL + t), seg_it & 1u, abort_flag, kSiteEpiL);
+                ok = warp_bwait(BAR(SPO_FINAL + t), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     warp_bwait(BAR(SPL_FULL + t), seg_it & 1u, abort_flag, kSiteEpiL);
                 if (!ok) return;
                 l = row_ml[t * 256 + row];
                 m = row_ml[t * 256 + 128 + row];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(BL_EMPTY + t));
+                if (lane == 0) mbar_arrive(BAR(SPL_EMPTY + t));
                 tc_fence_after();
             };
             auto put_ml = [&](int t, float m, float l) {
@@ -1165,7 +1209,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
             }
         }
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int tk = PAGED ? row / p.G : row;
+        const int tk = span_row_tok<PAGED>(p, row);
         const int64_t dst = span_out_offset<D, PAGED>(p, s.head, s.q0, s.tok0 + t * p.tile_tok + tk, PAGED ? row - tk * p.G : 0);
         *reinterpret_cast<uint2 *>(p.out + dst + c4 * 4) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
