@@ -28,12 +28,16 @@
 //
 // Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
 // ordered by sequence, head and query rows, and each CTA takes an equal,
-// contiguous part. Lengths are read on the device: every CTA sums the steps per
-// sequence and finds its part by itself (span_schedule), so the call can be
-// captured and replayed with other lengths. An item that a part's border cuts
-// is computed in pieces; each piece writes its unnormalised O, row maxima and
-// sums to the workspace, and span_merge_kernel adds them up in piece order (no
-// atomics: the result is the same every time).
+// contiguous part. Of whole sequences with several items of about one length for
+// each CTA, whole items are dealt out round by round first, and only what is left is
+// shared out in steps: the CTAs then work on neighbouring query rows of a few
+// heads at a time, whose K/V stay in L2 (S = 16384, H = 24, a window of 4096: 2.85
+// GB of DRAM reads without the rounds, for 0.3 GB of inputs). Lengths are read on
+// the device: every CTA sums the steps per sequence and finds its part by itself
+// (span_schedule), so the call can be captured and replayed with other lengths.
+// An item that a part's border cuts is computed in pieces; each piece writes its
+// unnormalised O, row maxima and sums to the workspace, and span_merge_kernel
+// adds them up in piece order (no atomics: the result is the same every time).
 //
 // Roles of the 512 threads (registers 48 / 176 / 176 / 112 a thread):
 //   warp 0      TMA producer: Q tiles, then K and V tiles into a 4-slot ring. Pages
@@ -86,12 +90,15 @@ template <int D> struct SpanCfg {
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
 };
 
-// One CTA's part of the steps, found by span_schedule.
+// One CTA's share, found by span_schedule: first `rounds` whole items (blockIdx.x,
+// blockIdx.x + ctas, ... in the items' order), then `rem` steps of the shared rest
+// from (seq, head, pair, j) on.
 struct SpanSched {
-    long long total, rem;  // steps of the call, of this CTA
-    long long q;           // total / ctas, and the remainder
+    long long shared, rem;  // steps shared out, of the call and of this CTA
+    long long q;            // shared / ctas, and the remainder
     uint32_t r;
-    int ctas;              // CTAs that share the steps
+    int ctas;
+    int rounds;
     int seq, head, pair, j;
 };
 static_assert(sizeof(SpanSched) <= 64, "its place in shared memory");
@@ -184,8 +191,8 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
     return u;
 }
 
-// First step of CTA c's part: floor(c * total / ctas), with the quotient and
-// remainder of total / ctas (T is 32 bits wide unless the total is not).
+// First step of CTA c's part of the shared steps: floor(c * shared / ctas), with the
+// quotient and remainder of shared / ctas (T is 32 bits wide unless they are not).
 template <typename T> __device__ __forceinline__ T span_first(T q, uint32_t r, int ctas, int c) {
     return (T)c * q + (T)((uint32_t)c * r / (uint32_t)ctas);
 }
@@ -207,22 +214,25 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
     return l;
 }
 
-// Where CTA c's part begins, by one warp. `mine`: the steps of this lane's group
-// in the only chunk, when there is one; otherwise the chunks' sums are in `sums`.
+// Where this CTA's part of the shared steps begins, by one warp. The shared steps
+// are the call's from step `before` on. `sum`: the steps of one head (whole
+// sequences). `mine`: the steps of this lane's group in the only chunk, when there
+// is one; otherwise the chunks' sums are in `sums`.
 template <typename T, bool PAGED>
-__device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, long long sum, long long mine, int chunks,
-                                          const long long *sums, int lane) {
+__device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T before, long long sum, long long mine,
+                                          int chunks, const long long *sums, int lane) {
     const int c = (int)blockIdx.x;
-    const T total = (T)s.total, q = total / (T)s.ctas;
+    const T total = (T)s.shared, q = total / (T)s.ctas;
     const uint32_t r = (uint32_t)(total - q * (T)s.ctas);
     s.q = (long long)q;
     s.r = r;
     const T u0 = span_first<T>(q, r, s.ctas, c);
     s.rem = (long long)(span_first<T>(q, r, s.ctas, c + 1) - u0);
-    T u = u0, base = 0, at = 0;
+    if (s.rem == 0) return;
+    T u = before + u0, base = 0, at = 0;
     if (!PAGED) {
-        s.head = (int)(u0 / (T)sum);
-        u = u0 - (T)s.head * (T)sum;
+        s.head = (int)(u / (T)sum);
+        u -= (T)s.head * (T)sum;
     }
     int l = -1, ch = 0;
     if (chunks > 1) {
@@ -263,6 +273,28 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, lon
     s.j = (int)(u - at);
 }
 
+// Whole items dealt out round by round first, and the steps they hold (whole
+// sequences). None unless the items are of about one length (their mean at least
+// 4/5 of the longest: a CTA's rounds then end about when the others' do) and
+// there are two for each CTA. The last round is shared out in steps with the rest
+// when the rest alone would give each CTA less than 0.4 of an item: short pieces
+// cost more than they balance. `sum`: the steps of one head.
+__device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long long sum, int lane, long long &steps) {
+    steps = 0;
+    const long long items = (long long)p.heads * p.n_pairs;
+    int most = max(span_item(p, p.S, p.S, p.n_pairs >> 1).n, span_item(p, p.S, p.S, p.n_pairs - 1).n);
+    most = max(most, span_item(p, p.S, p.S, 0).n);
+    if (items < 2ll * grid || 5 * sum < 4ll * p.n_pairs * most) return 0;
+    int rounds = (int)(items / grid);
+    const int rest = (int)(items - (long long)rounds * grid);
+    if (rest && 5 * rest < 2 * grid) --rounds;
+    const long long first = (long long)rounds * grid, head = first / p.n_pairs;  // the first shared item
+    const int pairs = (int)(first - head * p.n_pairs);
+    for (int i = lane; i < pairs; i += 32) steps += span_item(p, p.S, p.S, i).n;
+    steps = warp_sum(steps) + head * sum;
+    return rounds;
+}
+
 // Sums of the steps of 32 groups each, when there are more; by all threads, and
 // followed by a barrier.
 template <bool PAGED> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
@@ -283,32 +315,36 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
         sum = mine = span_group_steps<PAGED>(p, 0, lane);
     }
     sum = warp_sum(sum);
+    const long long total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
-    s.total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
-    s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total >> p.min_steps_log2));
+    s.ctas = (int)max(1ll, min((long long)gridDim.x, total >> p.min_steps_log2));
     s.rem = s.q = 0;
     s.r = 0;
-    s.seq = s.head = s.pair = s.j = 0;
-    if ((int)blockIdx.x < s.ctas && s.total > 0) {
-        if (s.total < (1ll << 31))
-            span_find<uint32_t, PAGED>(p, s, sum, mine, chunks, sums, lane);
+    s.rounds = s.seq = s.head = s.pair = s.j = 0;
+    long long before = 0;
+    if (!PAGED && s.ctas == (int)gridDim.x) s.rounds = span_rounds(p, s.ctas, sum, lane, before);
+    s.shared = total - before;
+    if ((int)blockIdx.x < s.ctas && s.shared > 0) {
+        if (total < (1ll << 31))
+            span_find<uint32_t, PAGED>(p, s, (uint32_t)before, sum, mine, chunks, sums, lane);
         else
-            span_find<unsigned long long, PAGED>(p, s, sum, mine, chunks, sums, lane);
+            span_find<unsigned long long, PAGED>(p, s, (unsigned long long)before, sum, mine, chunks, sums, lane);
     }
     return s;
 }
 
-// The CTA whose part holds step u.
+// The CTA whose part holds shared step u.
 __device__ __forceinline__ int span_cta_of(const SpanSched &s, long long u) {
-    return (int)(((u + 1) * s.ctas - 1) / s.total);
+    return (int)(((u + 1) * s.ctas - 1) / s.shared);
 }
 
-// The walk through a CTA's part, one stretch (segment) of an item at a time.
+// The walk through a CTA's share, one stretch (segment) of an item at a time.
 struct SpanWalk {
-    long long rem;  // steps left (whole items: items left)
+    int rounds;      // whole items left
+    long long rem;   // shared steps left
     int seq, head, pair, j;
     int q0, q_len, keys;
-    bool first;
+    bool first;      // no shared segment yet
 };
 // What the roles need to know of a segment (96 bytes).
 struct SpanSeg {
@@ -331,27 +367,48 @@ __device__ __forceinline__ int span_tile(const volatile SpanSeg &g, int y) {
     const int nw = g.nw;
     return y < nw ? g.hi - y : g.ns - 1 - (y - nw);
 }
+// Moves the walk `by` items on in the items' order (whole sequences).
+__device__ __forceinline__ void span_skip(const SpanParams &p, SpanWalk &w, int by) {
+    const int at = w.pair + by, heads = at / p.n_pairs;
+    w.head += heads;
+    w.pair = at - heads * p.n_pairs;
+}
+// The walk's start in the shared steps.
 template <bool PAGED>
-__device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
-    w.first = true;
-    w.seq = w.j = 0;
-    if (PAGED || p.rec) {
-        w.seq = s.seq;
-        w.j = s.j;
-        w.rem = s.rem;
-        w.head = s.head;
-        w.pair = s.pair;
-    } else {  // whole items, dealt round
-        const long long items = (long long)p.heads * p.n_pairs;
-        w.rem = ((long long)items - blockIdx.x + gridDim.x - 1) / gridDim.x;
-        w.head = (int)(blockIdx.x / p.n_pairs);
-        w.pair = (int)(blockIdx.x % p.n_pairs);
-    }
+__device__ __forceinline__ void span_walk_shared(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
+    w.rem = s.rem;
+    w.seq = s.seq;
+    w.head = s.head;
+    w.pair = s.pair;
+    w.j = s.j;
     if (w.rem > 0) span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
 }
 template <bool PAGED>
-__device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, SpanSeg &g) {
-    if (w.rem <= 0) return false;
+__device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
+    w.first = true;
+    w.rounds = 0;
+    if (PAGED) {
+        span_walk_shared<PAGED>(p, s, w);
+        return;
+    }
+    if (p.rec) {
+        w.rounds = s.rounds;
+    } else {  // no workspace: whole items only
+        const long long items = (long long)p.heads * p.n_pairs;
+        w.rounds = (int)((items - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    }
+    if (w.rounds == 0) {
+        span_walk_shared<PAGED>(p, s, w);
+        return;
+    }
+    w.rem = 0;
+    w.seq = w.head = w.pair = w.j = 0;
+    span_lengths<PAGED>(p, 0, w.q0, w.q_len, w.keys);
+    span_skip(p, w, (int)blockIdx.x);
+}
+template <bool PAGED>
+__device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
+    if ((PAGED || w.rounds == 0) && w.rem <= 0) return false;
     if (PAGED)
         while (w.q_len == 0) {
             if (++w.seq >= p.N) return false;
@@ -375,8 +432,15 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, Span
     g.lo = max(0, it.pos0 - p.left);
     g.last = min(w.keys - 1, it.pos0 + it.ntok - 1 + p.right);
     g.slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
-    w.first = false;
-    if (PAGED || p.rec) {
+    if (!PAGED && w.rounds > 0) {
+        g.j0 = 0;
+        g.n = it.n;
+        if (--w.rounds > 0)
+            span_skip(p, w, (int)gridDim.x);
+        else if (p.rec)
+            span_walk_shared<PAGED>(p, sched, w);
+    } else {
+        w.first = false;
         g.j0 = w.j;
         g.n = (int)min((long long)(it.n - w.j), w.rem);
         w.rem -= g.n;
@@ -391,13 +455,6 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, SpanWalk &w, Span
                 }
             }
         }
-    } else {
-        g.j0 = 0;
-        g.n = it.n;
-        --w.rem;
-        const long long item = (long long)w.head * p.n_pairs + w.pair + gridDim.x;
-        w.head = (int)(item / p.n_pairs);
-        w.pair = (int)(item - (long long)w.head * p.n_pairs);
     }
     g.piece = g.n < it.n;
     for (int t = 0; t < 2; ++t) {
@@ -536,7 +593,7 @@ __global__ void __launch_bounds__(512, 1)
             span_walk_init<PAGED>(p, *sched, w);
             for (bool more = true; more; ++seg_it) {
                 SpanSeg g;
-                more = span_next<PAGED>(p, w, g);
+                more = span_next<PAGED>(p, *sched, w, g);
                 if (!more) g.n = 0;
                 if (more && g.piece && g.j0 == 0) {  // its first piece: this CTA's last segment
                     const int left = g.nw + g.ns - g.n;
@@ -774,17 +831,15 @@ __global__ void __launch_bounds__(512, 1)
                     // steps (of the segment) of tile 0: from f0 on; of tile 1: below l1 and from m1 on
                     const int f0 = max(g.s0 - g.j0, 0), l1 = min(g.e1 - g.j0, n), m1 = max(g.nw - g.j0, 0);
                     auto on1 = [&](int x) { return x < l1 || x >= m1; };
-                    const int first1 = l1 > 0 ? 0 : m1, last1 = m1 < n ? n - 1 : l1 - 1;
+                    const int first1 = l1 > 0 ? 0 : m1, last1 = m1 < n ? n - 1 : l1 - 1;  // last1 < 0: none
                     wait_kv(ks);
                     if (!ok) break;
                     tc_fence_after();
                     if (f0 == 0) issue_S(0, 0, ks);
+                    if (n == 1) tc_commit(BAR(SPQ_EMPTY + 0));  // after each tile's last S
                     if (on1(0)) issue_S(1, 1, ks);
+                    if (last1 <= 0) tc_commit(BAR(SPQ_EMPTY + 1));
                     tc_commit(BAR(SPKV_EMPTY + ks));
-                    if (n == 1) {
-                        tc_commit(BAR(SPQ_EMPTY + 0));
-                        tc_commit(BAR(SPQ_EMPTY + 1));
-                    }
                     for (int x = 0; x < n; ++x) {
                         const bool more = x + 1 < n;
                         wait_v(vs, fix && x == 0);
@@ -800,6 +855,7 @@ __global__ void __launch_bounds__(512, 1)
                             if (!ok) break;
                             tc_fence_after();
                             if (x + 1 >= f0) issue_S(0, 0, ks);
+                            if (x + 2 == n) tc_commit(BAR(SPQ_EMPTY + 0));
                         }
                         if (on1(x)) {
                             wait_p(1, x == first1);
@@ -810,11 +866,8 @@ __global__ void __launch_bounds__(512, 1)
                         tc_commit(BAR(SPKV_EMPTY + vs));
                         if (more) {
                             if (on1(x + 1)) issue_S(1, 1, ks);
+                            if (x + 1 == last1) tc_commit(BAR(SPQ_EMPTY + 1));
                             tc_commit(BAR(SPKV_EMPTY + ks));
-                            if (x + 2 == n) {
-                                tc_commit(BAR(SPQ_EMPTY + 0));
-                                tc_commit(BAR(SPQ_EMPTY + 1));
-                            }
                         }
                     }
                     if (ok && f0 >= n) no_steps(0);

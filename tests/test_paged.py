@@ -63,7 +63,7 @@ class Batch:
         for n, (ql, kl) in enumerate(zip(self.q_len, self.kv)):
             pos = np.arange(kl - ql, kl)
             seen = seen_mask(pos, kl, left, right, sinks)
-            for h in range(self.H):
+            for h in range(self.H) if self.H * ql < 9000 else sorted({0, 1, self.H // 3, self.H // 2, self.H - 1}):
                 ref, bound = attend(self.q[t:t + ql, h], self.k[n][:, h // G], self.v[n][:, h // G], seen, self.D ** -0.5)
                 check(got[t:t + ql, h], ref, bound, f"{what} sequence {n} head {h}")
                 assert (got[t:t + ql, h][~seen.any(-1)] == 0).all()
@@ -91,6 +91,9 @@ CASES = [  # q_len, kv_len, H, Hk, D, page, spare, (left, right, sinks)
     ([9], [0], 4, 2, 64, 16, 0, (-1, -1, 0)),
     ([3], [400], 128, 1, 64, 16, 0, (-1, 0, 0)),                           # 128 heads a key head
     ([600], [2500], 5, 1, 128, 32, 0, (700, 0, 140)),
+    ([700, 0, 900, 1, 640], [1500, 40, 1500, 1300, 1290], 32, 32, 64, 16, 3, (-1, 0, 0)),   # whole rounds, then a rest
+    ([500, 512], [1100, 1000], 76, 76, 64, 64, 0, (255, 0, 0)),            # two items a CTA, nothing left (152 SMs)
+    ([1500], [1500], 24, 24, 64, 128, 0, (-1, 0, 0)),                      # items of unlike lengths
 ]
 
 

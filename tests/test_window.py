@@ -25,6 +25,10 @@ CASES = [
     (1, 1500, 2, 128, 1, 200, 0, 3, 4.0),      # peaked scores
     (1, 2176, 8, 128, 8, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1.0),
     (1, 1280, 40, 64, 4, 400, 0, 64, 1.0),     # more items than SMs
+    (1, 2048, 48, 64, 2, 300, 0, 3, 1.0),      # several items a CTA: whole rounds, then half an item each
+    (1, 2560, 31, 64, 1, 200, 100, 0, 1.0),    # whole rounds, a little more than one item each left
+    (2, 1024, 76, 64, 4, 150, 0, 0, 1.0),      # whole rounds and nothing left (152 SMs)
+    (1, 2304, 40, 64, 1, -1, 0, 0, 1.0),       # items of unlike lengths: no rounds
 ]
 
 
@@ -61,7 +65,7 @@ def test_window_matches_64_bits(case):
     for ws, fill in ((True, None), (True, 0xFF), (False, None)):
         got = run(case, *dev, D ** -0.5, ws, fill)
         for b in range(B):
-            for h in range(H) if S * H < 9000 else (0, H - 1):
+            for h in range(H) if S * H < 9000 else sorted({0, 1, H // 3, H // 2, 2 * H // 3, H - 2, H - 1}):
                 ref, bound = attend(q[b, :, h], k[b, :, h], v[b, :, h], seen, D ** -0.5)
                 check(got[b, :, h], ref, bound, f"{case} b={b} h={h} ws={ws}")
     if left == right == sinks == 0:
