@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(512, 1)
             // lim: the row sum that calls for the row max again: none for a row that does
             // not exist, any for one that has not seen a key yet
             float m = -INFINITY, l = 0.f, lim;
-            bool idle, first = true;
+            bool idle;
             {
                 const int rows = min(g.ntok - (g.dual ? 0 : t * p.tile_tok), p.tile_tok) * p.G;
                 lim = row < rows ? -1.f : INFINITY;
@@ -928,6 +928,9 @@ __global__ void __launch_bounds__(512, 1)
                 c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
                 if (y >= nw) c_end = INT_MIN;
             }
+            // Rows whose keys end in an earlier tile than the first see none in it, so the
+            // maxima are taken over the first two steps.
+            const int settled = steps - 2;
 #pragma unroll 1
             for (; steps > 0; --steps) {
                 const int c0 = c * 128;
@@ -1013,17 +1016,20 @@ __global__ void __launch_bounds__(512, 1)
                     lstep = a0 + a1;
                 };
                 load_scores();
-                if (first) {
-                    m = row_max();
-                    if (lim < 0.f && m > -INFINITY) lim = kSpanRise;
+                if (steps > settled) {
+                    const float mx = row_max();
+                    if (lim < 0.f && mx > -INFINITY) {
+                        m = mx;
+                        lim = kSpanRise;
+                    }
                 }
                 exps();
-                // The row max is taken at the first step and then kept while no row sum
-                // passes kSpanRise: p, l and O are floating point, so a maximum that lags by
-                // up to 2^14 costs no precision, and a first tile with only a few keys in it
-                // (a causal diagonal) seldom has to be put right. A row that has not seen a
-                // key before takes its max at the first step where it does.
-                if (!first && __any_sync(0xffffffffu, lstep > lim)) {
+                // A row keeps its max while no row sum passes kSpanRise: p, l and O are floating
+                // point, so a maximum that lags by up to 2^14 costs no precision, and a first
+                // tile with only a few keys in it (a causal diagonal) seldom has to be put
+                // right. A row that sees its first key later yet (a piece that begins behind
+                // its window) gets its max here too. Until then its weights, sum and O are 0.
+                if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // not at the first step
                     load_scores();
                     const float mnew = row_max();
                     float alpha = 1.f;
@@ -1047,7 +1053,6 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     exps();
                 }
-                first = false;
                 l += lstep;
                 {
                     uint32_t h0[32], h1[32];
