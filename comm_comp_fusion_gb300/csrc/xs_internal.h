@@ -139,7 +139,7 @@ cudaError_t launch_permute(const void *in, void *out, const PermParams &p, bool 
                            cudaStream_t stream);
 
 // ------------------------------------------------------------ rotary positions
-constexpr int kRopeMaxPairs = 128, kRopeMaxUnits = 32, kRopeMaxAxes = 4;
+constexpr int kRopeMaxPairs = 128, kRopeMaxUnits = 16, kRopeMaxAxes = 4;
 struct RopeParams {
     const uint16_t *q, *k;  // k NULL: none (Hk = 0)
     uint16_t *q_out, *k_out;
@@ -147,13 +147,12 @@ struct RopeParams {
     int64_t pos_batch;      // S, or 0 when every batch shares the positions
     int B, S, H, Hk, Hl, Hkl, Sl, D;
     int n_axes, n_pairs;
-    int units;              // units of work per row (rope_kernel)
     int tile;               // tokens per block
     bool seq_in, seq_out, inverse;
-    uint32_t mU, sU, mH, sH, mSl, sSl;  // magic numbers: division by units, H + Hk, Sl
     uint64_t frac[kRopeMaxPairs];       // frequency in turns, a 64-bit binary fraction
     uint8_t axis[kRopeMaxPairs];
-    uint8_t unit_first[kRopeMaxUnits], unit_half[kRopeMaxUnits];  // pairs half an axis apart: see rope_kernel
+    uint8_t unit_first[kRopeMaxUnits], unit_half[kRopeMaxUnits];  // pairs half an axis apart: a unit's first
+                                                                  // chunk, and how far the second is (rope_kernel)
 };
 cudaError_t launch_rope(RopeParams &p, bool halves, int num_sms, cudaStream_t stream);
 

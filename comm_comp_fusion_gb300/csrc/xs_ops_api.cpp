@@ -198,10 +198,9 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
         p.frac[j] = turns_fraction(freqs[j]);
     }
     p.n_pairs = rot / 2;
-    p.units = D / 8;
-    if (halves) {
-        p.units = rot / 16;
-        for (int e = rot; e < D; e += 8) p.unit_first[p.units++] = (uint8_t)e;
+    for (int u = rot / 16; halves && u < D / 16; ++u) {  // copied
+        p.unit_first[u] = (uint8_t)(16 * u);
+        p.unit_half[u] = 8;
     }
     p.seq_in = flags & XS_ROPE_IN_SEQ;
     p.seq_out = flags & XS_ROPE_OUT_SEQ;

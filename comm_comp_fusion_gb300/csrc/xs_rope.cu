@@ -16,21 +16,22 @@
 // sincospif.
 //
 // Bound: HBM. Every element is read and written once (4 bytes of traffic for 3
-// flops); a block computes its tokens' sines and cosines once into shared
-// memory and uses them for every head of q and k.
+// flops). A block turns a few tokens of one batch: it computes their sines and
+// cosines once into shared memory, and each thread keeps those of its eight pairs
+// of one token in registers while it walks heads of q and then of k, four at a
+// time (eight 16-byte loads in flight). Measured on one GB300: B = 2, S = 16384, H = 40,
+// D = 128 199 us, 6.75 TB/s (with one unit of a random row per step instead of a
+// thread's own token, 251 us); S = 4096, H = 24 to the head partition 21 us, 4.8 TB/s.
 #include "xs_internal.h"
 #include "xs_ptx.cuh"
 
 namespace xs {
 
-constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;
 
-__device__ __forceinline__ uint32_t rope_div(uint32_t n, uint32_t m, uint32_t s) { return (__umulhi(n, m) + n) >> s; }
-
-__device__ __forceinline__ uint4 rope_load(const uint4 *ptr) {
+__device__ __forceinline__ uint4 rope_load(const uint16_t *ptr) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(ptr));
     return v;
@@ -60,28 +61,53 @@ __device__ __forceinline__ void turn_words(uint32_t &u, uint32_t &v, float2 c0, 
     v = pack_bf16x2(b0, b1);
 }
 
-// Element offset of (b, s, head h of nh) in the sequence or the head partition.
-__device__ __forceinline__ int64_t rope_row(const RopeParams &p, bool seq, int b, int s, int h, int nh, int nhl) {
+// The rows of one token in a tensor of nh heads: heads in order, `hop` elements
+// apart, with a jump of `jump` more after every nhl (head partition: the next rank's
+// slice; sequence partition: never).
+struct RopeRows {
+    int64_t at, jump;
+    int hop, left;  // left: heads before the next jump
+};
+__device__ __forceinline__ RopeRows rope_rows(const RopeParams &p, bool seq, int b, int s, int h, int nh, int nhl) {
+    RopeRows r;
+    r.hop = p.D;
     if (seq) {
-        const int r = (int)rope_div((uint32_t)s, p.mSl, p.sSl);
-        return ((((int64_t)r * p.B + b) * p.Sl + (s - r * p.Sl)) * nh + h) * p.D;
+        const int rk = s / p.Sl;
+        r.at = ((((int64_t)rk * p.B + b) * p.Sl + (s - rk * p.Sl)) * nh + h) * p.D;
+        r.jump = 0;
+        r.left = 1 << 30;
+    } else {
+        const int rk = h / nhl;
+        r.at = ((((int64_t)rk * p.B + b) * p.S + s) * nhl + (h - rk * nhl)) * p.D;
+        r.jump = ((int64_t)p.B * p.S - 1) * nhl * p.D;
+        r.left = nhl - (h - rk * nhl);
     }
-    const int r = h / nhl;
-    return ((((int64_t)r * p.B + b) * p.S + s) * nhl + (h - r * nhl)) * p.D;
+    return r;
+}
+// The row `by` heads on.
+__device__ __forceinline__ void rope_advance(RopeRows &r, int by, int nhl) {
+    r.at += (int64_t)by * r.hop;
+    r.left -= by;
+    while (r.left <= 0) {
+        r.at += r.jump;
+        r.left += nhl;
+    }
 }
 
-// A block turns `tile` tokens of one batch, all heads of q then of k. A unit is
-// 16 bytes of a row (neighbouring pairs), or two 16-byte chunks half an axis
-// apart (HALVES); chunks past the rotated elements are copied.
-template <bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    extern __shared__ float2 cs_tab[];  // [token][pair]
+// A thread's unit is two 16-byte chunks of a row, eight pairs: 16 elements in a row
+// (neighbouring pairs), or two chunks half an axis apart (HALVES); units past the
+// rotated elements are copied.
+template <int D, bool HALVES>
+__global__ void __launch_bounds__(D == 96 ? 192 : 256) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int U = D / 16, kThreads = D == 96 ? 192 : 256, kRows = kThreads / U;
+    extern __shared__ float2 cs_tab[];  // [token][pair], D / 2 pairs a token
     const int tiles = (p.S + p.tile - 1) / p.tile;
     const int b = (int)(blockIdx.x / (unsigned)tiles), s0 = ((int)blockIdx.x - b * tiles) * p.tile;
     const int nt = min(p.tile, p.S - s0);
     const int *pos = p.pos + ((int64_t)b * p.pos_batch + s0) * p.n_axes;
-    for (int i = threadIdx.x; i < nt * p.n_pairs; i += kRopeThreads) {
-        const int t = i / p.n_pairs, j = i - t * p.n_pairs;
+    for (int i = threadIdx.x; i < nt * (D / 2); i += kThreads) {
+        const int t = i / (D / 2), j = i - t * (D / 2);
+        if (j >= p.n_pairs) continue;
         const uint64_t phase = (uint64_t)(int64_t)pos[t * p.n_axes + p.axis[j]] * p.frac[j];
         const int turns = (int)(uint32_t)((phase + 0x80000000ull) >> 32);  // nearest multiple of 2^-32 turns
         float sn, cn;
@@ -89,77 +115,85 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         cs_tab[i] = make_float2(cn, p.inverse ? -sn : sn);
     }
     __syncthreads();
-    const uint32_t per_row = (uint32_t)p.units, heads = (uint32_t)(p.H + p.Hk);
-    const uint32_t total = (uint32_t)nt * heads * per_row;
-    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kRopeUnroll * kRopeThreads) {
-        uint4 x[kRopeUnroll], y[kRopeUnroll];
-        uint16_t *dst[kRopeUnroll];
-        int first[kRopeUnroll], half[kRopeUnroll], tok[kRopeUnroll];
+    const int unit = (int)threadIdx.x % U, rr = (int)threadIdx.x / U;
+    const int lanes = kRows / p.tile;  // threads of a token and unit: each takes every lanes-th head
+    const int t = rr / lanes, h0 = rr - t * lanes;
+    if (t >= nt) return;
+    const int pairs = min(8, p.n_pairs - unit * 8);  // pairs of this unit that turn
+    int c0 = unit * 16, c1 = c0 + 8;                 // its chunks' first elements
+    if (HALVES) {
+        c0 = p.unit_first[unit];
+        c1 = c0 + p.unit_half[unit];
+    }
+    float2 cs[8];
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            const uint32_t i = i0 + u * kRopeThreads;
-            if (i >= total) break;
-            const uint32_t row = rope_div(i, p.mU, p.sU), unit = i - row * per_row;
-            const int t = (int)rope_div(row, p.mH, p.sH);
-            int h = (int)(row - (uint32_t)t * heads);
-            const bool is_q = h < p.H;
-            if (!is_q) h -= p.H;
-            const int nh = is_q ? p.H : p.Hk, nhl = is_q ? p.Hl : p.Hkl;
-            const uint16_t *src = (is_q ? p.q : p.k) + rope_row(p, p.seq_in, b, s0 + t, h, nh, nhl);
-            dst[u] = (is_q ? p.q_out : p.k_out) + rope_row(p, p.seq_out, b, s0 + t, h, nh, nhl);
-            tok[u] = t;
-            if (HALVES) {
-                first[u] = p.unit_first[unit];
-                half[u] = p.unit_half[unit];  // elements between the two chunks; 0: a copied chunk
-                x[u] = rope_load(reinterpret_cast<const uint4 *>(src + first[u]));
-                if (half[u]) y[u] = rope_load(reinterpret_cast<const uint4 *>(src + first[u] + half[u]));
-            } else {
-                first[u] = (int)unit * 8;
-                half[u] = 0;
-                x[u] = rope_load(reinterpret_cast<const uint4 *>(src + first[u]));
-            }
-        }
+    for (int j = 0; j < 8; ++j) cs[j] = cs_tab[t * (D / 2) + unit * 8 + j];
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int nh = which ? p.Hk : p.H, nhl = which ? p.Hkl : p.Hl;
+        if (h0 >= nh) continue;
+        const uint16_t *src = which ? p.k : p.q;
+        uint16_t *dst = which ? p.k_out : p.q_out;
+        RopeRows in = rope_rows(p, p.seq_in, b, s0 + t, h0, nh, nhl), out = rope_rows(p, p.seq_out, b, s0 + t, h0, nh, nhl);
+        for (int h = h0; h < nh; h += kRopeUnroll * lanes) {
+            uint4 x[kRopeUnroll], y[kRopeUnroll];
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            const uint32_t i = i0 + u * kRopeThreads;
-            if (i >= total) break;
-            if (HALVES) {
-                if (half[u]) {
-                    const uint32_t unit = i - rope_div(i, p.mU, p.sU) * per_row;
-                    const float2 *cs = cs_tab + tok[u] * p.n_pairs + unit * 8;  // rotated units come first, 8 pairs each
-                    turn_words(x[u].x, y[u].x, cs[0], cs[1]);
-                    turn_words(x[u].y, y[u].y, cs[2], cs[3]);
-                    turn_words(x[u].z, y[u].z, cs[4], cs[5]);
-                    turn_words(x[u].w, y[u].w, cs[6], cs[7]);
-                    *reinterpret_cast<uint4 *>(dst[u] + first[u] + half[u]) = y[u];
+            for (int u = 0; u < kRopeUnroll; ++u)
+                if (h + u * lanes < nh) {
+                    x[u] = rope_load(src + in.at + c0);
+                    y[u] = rope_load(src + in.at + c1);
+                    rope_advance(in, lanes, nhl);
                 }
-            } else {
-                const int j = first[u] >> 1;  // the chunk's first pair
-                const float2 *cs = cs_tab + tok[u] * p.n_pairs + j;
-                if (j + 0 < p.n_pairs) x[u].x = turn_word(x[u].x, cs[0]);
-                if (j + 1 < p.n_pairs) x[u].y = turn_word(x[u].y, cs[1]);
-                if (j + 2 < p.n_pairs) x[u].z = turn_word(x[u].z, cs[2]);
-                if (j + 3 < p.n_pairs) x[u].w = turn_word(x[u].w, cs[3]);
-            }
-            *reinterpret_cast<uint4 *>(dst[u] + first[u]) = x[u];
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u)
+                if (h + u * lanes < nh) {
+                    if (HALVES) {
+                        if (pairs > 0) {
+                            turn_words(x[u].x, y[u].x, cs[0], cs[1]);
+                            turn_words(x[u].y, y[u].y, cs[2], cs[3]);
+                            turn_words(x[u].z, y[u].z, cs[4], cs[5]);
+                            turn_words(x[u].w, y[u].w, cs[6], cs[7]);
+                        }
+                    } else {
+                        if (pairs > 0) x[u].x = turn_word(x[u].x, cs[0]);
+                        if (pairs > 1) x[u].y = turn_word(x[u].y, cs[1]);
+                        if (pairs > 2) x[u].z = turn_word(x[u].z, cs[2]);
+                        if (pairs > 3) x[u].w = turn_word(x[u].w, cs[3]);
+                        if (pairs > 4) y[u].x = turn_word(y[u].x, cs[4]);
+                        if (pairs > 5) y[u].y = turn_word(y[u].y, cs[5]);
+                        if (pairs > 6) y[u].z = turn_word(y[u].z, cs[6]);
+                        if (pairs > 7) y[u].w = turn_word(y[u].w, cs[7]);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + out.at + c0) = x[u];
+                    *reinterpret_cast<uint4 *>(dst + out.at + c1) = y[u];
+                    rope_advance(out, lanes, nhl);
+                }
         }
     }
 }
 
 cudaError_t launch_rope(RopeParams &p, bool halves, int num_sms, cudaStream_t stream) {
-    // tokens per block: eight share a table when that still leaves several blocks
-    // for every SM, fewer for short calls
+    // tokens per block: eight share the table's set-up when that still leaves four
+    // blocks for every SM, fewer for short calls (S = 4096: 21 us with 4, 27 with 2)
     p.tile = 8;
     while (p.tile > 1 && (long long)p.B * ((p.S + p.tile - 1) / p.tile) < 4ll * num_sms) p.tile >>= 1;
-    fastdiv_magic((uint32_t)p.units, &p.mU, &p.sU);
-    fastdiv_magic((uint32_t)(p.H + p.Hk), &p.mH, &p.sH);
-    fastdiv_magic((uint32_t)p.Sl, &p.mSl, &p.sSl);
     const unsigned grid = (unsigned)((p.S + p.tile - 1) / p.tile) * (unsigned)p.B;
-    const size_t smem = (size_t)p.tile * p.n_pairs * sizeof(float2);
-    if (halves)
-        rope_kernel<true><<<grid, kRopeThreads, smem, stream>>>(p);
-    else
-        rope_kernel<false><<<grid, kRopeThreads, smem, stream>>>(p);
+    const size_t smem = (size_t)p.tile * (p.D / 2) * sizeof(float2);
+#define XS_ROPE_CASE(d)                                                        \
+    case d:                                                                    \
+        if (halves)                                                            \
+            rope_kernel<d, true><<<grid, d == 96 ? 192 : 256, smem, stream>>>(p);  \
+        else                                                                   \
+            rope_kernel<d, false><<<grid, d == 96 ? 192 : 256, smem, stream>>>(p); \
+        break;
+    switch (p.D) {
+        XS_ROPE_CASE(64)
+        XS_ROPE_CASE(96)
+        XS_ROPE_CASE(128)
+        XS_ROPE_CASE(256)
+        default: return cudaErrorInvalidValue;
+    }
+#undef XS_ROPE_CASE
     return cudaGetLastError();
 }
 
