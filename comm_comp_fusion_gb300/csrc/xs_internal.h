@@ -172,11 +172,13 @@ struct SpanParams {
     uint16_t *out;
     const int *table, *q_start, *kv_len;  // table NULL: whole sequences, head-partitioned
     int N, T, H, Hk, G;         // whole sequences: T = B * S rows of H heads
-    int page, n_pages, max_pages;
+    int page, page_log2, n_pages, max_pages;
     int B, S, P, Hl, Sl, head_out;  // whole sequences only
     int left, right, sinks;     // at most 2^29 each
     float scale_log2;
-    int tile_tok;               // tokens of a query tile: 128 / G
+    int few;                    // 0: query tiles of 128 rows; 16 or 32: the few-rows form
+    int tile_tok;               // tokens of a query tile: 128 / G, or few / G
+    int item_tok;               // tokens of an item: two tiles, or one with few rows
     uint32_t g_magic;           // row / G = row * g_magic >> 16 for rows below 128: ceil(2^16 / G)
     int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
     int min_steps_log2;         // fewest steps that a CTA is started for

@@ -115,6 +115,7 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     p.head_out = a2a ? 0 : 1;
     p.scale_log2 = scale_log2(scale);
     p.tile_tok = 128;
+    p.item_tok = 256;
     p.heads = B * H;
     p.n_pairs = (S + 255) / 256;
     if (ws) span_workspace_parts(ws, D, sms, &p);
@@ -356,7 +357,13 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
     p.n_pages = n_pages;
     p.max_pages = max_pages;
     p.scale_log2 = scale_log2(scale);
-    p.tile_tok = 128 / p.G;
+    // Few rows: batches of mostly single new tokens. The rows a sequence and key head
+    // have on average decide; longer sequences among them take several items.
+    const long long rows_avg = ((long long)T * p.G + N - 1) / N;
+    p.few = p.G <= 16 && rows_avg <= 16 ? 16 : p.G <= 32 && rows_avg <= 32 ? 32 : 0;
+    p.tile_tok = (p.few ? p.few : 128) / p.G;
+    p.item_tok = p.few ? p.tile_tok : 2 * p.tile_tok;
+    for (p.page_log2 = 4; 1 << p.page_log2 < page;) ++p.page_log2;
     p.g_magic = (65536u + (uint32_t)p.G - 1u) / (uint32_t)p.G;
     p.heads = Hk;
     span_workspace_parts(workspace, D, sms, &p);

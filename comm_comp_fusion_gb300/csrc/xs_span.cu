@@ -22,7 +22,7 @@ cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int nu
     SpanParams q = p;
     q.min_steps_log2 = p.table ? 1 : 2;
     // a merge thread adds up 4 columns of one row
-    const long long rows = (long long)std::min(p.T, 2 * p.tile_tok) * p.G;
+    const long long rows = (long long)std::min(p.T, p.item_tok) * p.G;
     q.merge_y = (int)std::max(1ll, (rows * (D / 4) + 255) / 256);
     const int grid = p.rec ? num_sms : (int)std::min((long long)num_sms, (long long)p.heads * p.n_pairs);
     if (D == 64) return launch_span_d64(maps, q, grid, stream);

@@ -21,10 +21,17 @@
 //   * Two tiles (pair): each K/V tile is used by both, one tile's softmax running
 //     under the other's MMAs. A K/V tile that only one of them sees (at the
 //     window's ends) costs the other nothing.
-//   * One tile (dual; single new tokens and the last rows of a chunk): the even
-//     and the odd K/V tiles form two chains with an O of their own each, which
-//     the epilogue adds up. A chain's step is a long dependent sequence (MMA,
-//     softmax, MMA), so two of them are what keeps K/V streaming.
+//   * One tile (dual; the last rows of a chunk): the even and the odd K/V tiles
+//     form two chains with an O of their own each, which the epilogue adds up. A
+//     chain's step is a long dependent sequence (MMA, softmax, MMA), so two of
+//     them are what keeps K/V streaming.
+//   * Few rows (FEW = 16 or 32; single new tokens): dual with the products
+//     turned round, S^T = K Q^T and O^T = V^T P^T, so that the 128 rows of an MMA
+//     are keys (or columns of V) and the query rows are its N. A softmax thread
+//     then holds one key's scores of all rows: 16 exponentials a step where the
+//     other form spends 128 on rows that mostly do not exist, and a step of a chain
+//     takes @FEWSTEP@ cycles instead of 3300, so that short calls end sooner and
+//     D = 64 and 96 are bound by HBM too.
 //
 // Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
 // ordered by sequence, head and query rows, and each CTA takes an equal,
@@ -65,29 +72,42 @@ constexpr int kSegs = 6;  // segments in the ring
 enum : int {
     SPQ_FULL = 0, SPQ_EMPTY = 2, SPS_FULL = 4, SPP_FULL = 6, SPO_FINAL = 8, SPO_FREE = 10, SPL_FULL = 12, SPL_EMPTY = 14,
     SP_DRAIN = 16, SPFIX_ASK = 17, SPFIX_DONE = 18,  // the issuer asks warp 3 to clear a V tile's end, and its answer
-    SPKV_FULL = 19, SPKV_EMPTY = 27, SPSEG_FULL = 35, SPSEG_EMPTY = 35 + kSegs, SP_BARS = 35 + 2 * kSegs
+    SPCHAIN = 19,                                    // few rows: the four softmax warps of a chain meet
+    SPKV_FULL = 21, SPKV_EMPTY = 31, SPSEG_FULL = 41, SPSEG_EMPTY = 41 + kSegs, SP_BARS = 41 + 2 * kSegs
 };
 enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 
-template <int D> struct SpanCfg {
+// FEW: query rows of a tile in the few-rows form; 0: tiles of 128 rows.
+template <int D, int FEW> struct SpanCfg {
     static constexpr int kNDB = Cfg<D>::kNDB;
     static constexpr uint32_t kBlk = Cfg<D>::kBlk, kTile = Cfg<D>::kTile;
-    // K/V ring: 128 KB in 16 KB (D = 64) or 32 KB slots. Single new tokens stream K/V at
-    // the rate of what is in flight: with four 16 KB slots D = 64 reached 3.9 TB/s.
-    static constexpr int kSlots = D == 64 ? 8 : 4;
-    static constexpr uint32_t kOffQ = 0;
-    static constexpr uint32_t kOffKV = 2 * kTile;
-    static constexpr uint32_t kOffStage = kOffKV + kSlots * kTile;
+    // K/V ring: single new tokens stream K/V at the rate of what is in flight, so it
+    // takes what shared memory the rest leaves (16 KB slots at D = 64, else 32 KB).
+    static constexpr int kSlots = D == 64 ? (FEW ? 10 : 8) : FEW == 16 ? 6 : FEW ? 5 : 4;
+    static constexpr uint32_t kOffKV = 0;
+    // Q: two tiles of the item, or with few rows two items' tiles
+    static constexpr uint32_t kQBlk = FEW ? FEW * 128u : kBlk, kQTile = kNDB * kQBlk;
+    static constexpr uint32_t kOffQ = kOffKV + kSlots * kTile;
     static constexpr uint32_t kStageWarp = Cfg<D>::kStageWarp;
-    static constexpr uint32_t kOffBar = kOffStage + 4 * kStageWarp;
+    static constexpr uint32_t kOffStage = kOffQ + 2 * kQTile;  // output rows; few rows: P of the two chains
+    static constexpr uint32_t kPTile = 2u * FEW * 128u;        // P: [64-key block][row][64 keys]
+    // few rows at D = 64: V^T is read as 128 rows, the last 64 from the next slot or,
+    // behind the ring, from here (they end in rows of O^T that nothing reads)
+    static constexpr uint32_t kBehind = FEW ? 2 * kPTile : 4 * kStageWarp;
+    static constexpr uint32_t kPad = 2 * kQTile + kBehind < kBlk ? kBlk - 2 * kQTile - kBehind : 0;
+    static constexpr uint32_t kOffRed = kOffStage + kBehind + kPad;    // few rows: float [chain][4 warps + m, exponent, alpha][FEW]
+    static constexpr uint32_t kOffBar = kOffRed + (FEW ? 2u * 8u * FEW * 4u : 0u);
     static constexpr uint32_t kOffL = kOffBar + 8 * ((SP_BARS + 1) & ~1);  // float [tile][l, m][128]
-    static constexpr uint32_t kOffMisc = kOffL + 2 * 2 * 128 * 4;          // tmem base, abort flag
+    static constexpr uint32_t kOffMisc = kOffL + 2 * 2 * 128 * 4;          // tmem base, abort flag, chain flags
     static constexpr uint32_t kOffSeg = kOffMisc + 16;                     // the ring of segments, then a SpanSched
     static constexpr uint32_t kSmemAlloc = kOffSeg + 96 * kSegs + 64 + 1024;
-    __host__ __device__ static constexpr uint32_t colS(int t) { return 128u * (uint32_t)t; }
-    __host__ __device__ static constexpr uint32_t colO(int t) { return 256u + (uint32_t)D * (uint32_t)t; }
-    static constexpr uint32_t kTmemCols = 512;
+    __host__ __device__ static constexpr uint32_t colS(int t) { return (FEW ? (uint32_t)FEW : 128u) * (uint32_t)t; }
+    __host__ __device__ static constexpr uint32_t colO(int t) {
+        return FEW ? (uint32_t)FEW * (uint32_t)(2 + t) : 256u + (uint32_t)D * (uint32_t)t;
+    }
+    static constexpr uint32_t kTmemCols = FEW ? 4 * FEW : 512;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
+    static_assert(kOffQ % 1024 == 0 && kOffStage % 1024 == 0, "swizzled tiles");
 };
 
 // One CTA's share, found by span_schedule: first `rounds` whole items (blockIdx.x,
@@ -121,8 +141,8 @@ struct SpanItem {
 
 __device__ __forceinline__ SpanItem span_item(const SpanParams &p, int q_len, int keys, int pair) {
     SpanItem it;
-    it.tok0 = pair * 2 * p.tile_tok;
-    it.ntok = min(2 * p.tile_tok, q_len - it.tok0);
+    it.tok0 = pair * p.item_tok;
+    it.ntok = min(p.item_tok, q_len - it.tok0);
     it.pos0 = keys - q_len + it.tok0;
     it.dual = it.ntok <= p.tile_tok;
     const int hi = min(keys - 1, it.pos0 + it.ntok - 1 + p.right);
@@ -157,7 +177,7 @@ __device__ __forceinline__ void span_lengths(const SpanParams &p, int seq, int &
 }
 
 __device__ __forceinline__ int span_pairs(const SpanParams &p, int q_len) {
-    const int t2 = 2 * p.tile_tok;
+    const int t2 = p.item_tok;
     return q_len <= t2 ? (q_len > 0) : (q_len + t2 - 1) / t2;
 }
 
@@ -447,7 +467,7 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
         w.j += g.n;
         if (w.j == it.n) {
             w.j = 0;
-            if (++w.pair * 2 * p.tile_tok >= w.q_len) {
+            if (++w.pair * p.item_tok >= w.q_len) {
                 w.pair = 0;
                 if (++w.head == p.heads) {
                     w.head = 0;
@@ -503,10 +523,10 @@ struct SpanPieces {
     int pieces, slot, seq, head, tok0, ntok, q0, unused;
 };
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int FEW>
 __global__ void __launch_bounds__(512, 1)
     span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
-    using C = SpanCfg<D>;
+    using C = SpanCfg<D, FEW>;
     using R = Rec<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -532,6 +552,7 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(BAR(SPO_FREE + t), 4);
             mbar_init(BAR(SPL_FULL + t), 4);
             mbar_init(BAR(SPL_EMPTY + t), 4);
+            mbar_init(BAR(SPCHAIN + t), 4);
         }
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(BAR(SPKV_FULL + s), 1);
@@ -644,15 +665,17 @@ __global__ void __launch_bounds__(512, 1)
                 const int n = g.n, j0 = g.j0, head = g.head;
                 if (!ok || n == 0) break;
                 const bool dual = g.dual;
-                for (int t = 0; t < (dual ? 1 : 2) && ok; ++t) {
-                    ok = warp_bwait(BAR(SPQ_EMPTY + t), ((t ? q_it1++ : q_it0++) & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+                for (int i = 0; i < (dual ? 1 : 2) && ok; ++i) {
+                    const int t = FEW ? (int)(seg_it & 1u) : i;  // few rows: items take the two tiles in turn
+                    const uint32_t use = FEW ? seg_it >> 1 : t ? q_it1++ : q_it0++;
+                    ok = warp_bwait(BAR(SPQ_EMPTY + t), (use & 1u) ^ 1u, abort_flag, kSiteLoadQ);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(BAR(SPQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
-                        const int tok = g.q0 + g.tok0 + t * p.tile_tok;
+                        const int tok = g.q0 + g.tok0 + i * p.tile_tok;
 #pragma unroll
                         for (int db = 0; db < C::kNDB; ++db) {
-                            const uint32_t dst = sQ + t * C::kTile + db * C::kBlk;
+                            const uint32_t dst = sQ + t * C::kQTile + db * C::kQBlk;
                             if (PAGED)
                                 tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, 0, head, tok);
                             else
@@ -668,7 +691,7 @@ __global__ void __launch_bounds__(512, 1)
                     if (!PAGED || lane * box >= 128 || x >= n) return 0;
                     const int k0 = span_tile(g, j0 + x) * 128 + lane * box;
                     if (k0 > g.last || (k0 + box <= g.lo && k0 >= p.sinks)) return p.n_pages;
-                    const int id = table[k0 / p.page];
+                    const int id = table[k0 >> p.page_log2];
                     return id < 0 || id >= p.n_pages ? p.n_pages : id;
                 };
                 auto load_tile = [&](const CUtensorMap *m, int x, int page) {
@@ -736,26 +759,38 @@ __global__ void __launch_bounds__(512, 1)
             }
         } else if (warp == 1 && lane == 0) {
             // -------------------------------------------------------- MMA issuer
-            constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0), idO = idesc_bf16_f32(128, D, 1);
+            // few rows: M = 128 keys (or columns of V, bit 15: A MN-major), N = the rows
+            constexpr uint32_t idS = idesc_bf16_f32(128, FEW ? FEW : 128, 0);
+            constexpr uint32_t idO = FEW ? idesc_bf16_f32(128, FEW, 0) | 1u << 15 : idesc_bf16_f32(128, D, 1);
             const uint64_t dK = sdesc_sw128(0, 16, 1024);       // K-major, 128-byte rows
             const uint64_t dV = sdesc_sw128(0, C::kBlk, 1024);  // MN-major V, 64-column blocks kBlk apart
             auto issue_S = [&](int t, int qt, uint32_t slot) {
-                const uint64_t qa = dK + (opaque(sQ + qt * C::kTile) >> 4);
+                const uint64_t qa = dK + (opaque(sQ + qt * C::kQTile) >> 4);
                 const uint64_t ka = dK + (opaque(sKV + slot * C::kTile) >> 4);
                 const uint32_t d = opaque(tmem + C::colS(t));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * C::kBlk + (kk & 3) * 32) >> 4;
-                    tc_mma_ss(d, qa + off, ka + off, idS, kk > 0 ? 1u : 0u);
+                    const uint32_t q_off = ((kk >> 2) * C::kQBlk + (kk & 3) * 32) >> 4;
+                    if (FEW)
+                        tc_mma_ss(d, ka + off, qa + q_off, idS, kk > 0 ? 1u : 0u);
+                    else
+                        tc_mma_ss(d, qa + q_off, ka + off, idS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(BAR(SPS_FULL + t));
             };
             auto issue_PV = [&](int t, uint32_t slot, bool acc) {
                 const uint64_t va = dV + (opaque(sKV + slot * C::kTile) >> 4);
                 const uint32_t d = opaque(tmem + C::colO(t)), a = opaque(tmem + C::colS(t));
+                const uint64_t pa = dK + (opaque(sStage + t * C::kPTile) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_ts(d, a + kk * 8, va + (kk * 2048 >> 4), idO, (acc || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 8; ++kk) {
+                    if (FEW)
+                        tc_mma_ss(d, va + (kk * 2048 >> 4), pa + (((kk >> 2) * C::kQBlk + (kk & 3) * 32) >> 4), idO,
+                                  (acc || kk > 0) ? 1u : 0u);
+                    else
+                        tc_mma_ts(d, a + kk * 8, va + (kk * 2048 >> 4), idO, (acc || kk > 0) ? 1u : 0u);
+                }
             };
             uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0, pph0 = 0, pph1 = 0, fph = 0;
             bool ok = true;
@@ -792,22 +827,23 @@ __global__ void __launch_bounds__(512, 1)
                 if (!ok || n == 0) break;
                 const bool fix = PAGED && g.fix >= 0;
                 uint32_t ks, vs;
-                ok = bwait(BAR(SPQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
-                if (g.dual) {
+                const int qb = FEW ? (int)(seg_it & 1u) : 0;  // the tile that holds Q (dual)
+                ok = bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
+                if (FEW || g.dual) {
                     // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
                     wait_kv(ks);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_S(0, 0, ks);
+                    issue_S(0, qb, ks);
                     tc_commit(BAR(SPKV_EMPTY + ks));
                     if (n > 1) {
                         wait_kv(ks);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_S(1, 0, ks);
+                        issue_S(1, qb, ks);
                         tc_commit(BAR(SPKV_EMPTY + ks));
                     }
-                    if (n <= 2) tc_commit(BAR(SPQ_EMPTY + 0));
+                    if (n <= 2) tc_commit(BAR(SPQ_EMPTY + qb));
                     for (int x = 0; x < n; ++x) {
                         const int t = x & 1;
                         wait_v(vs, fix && x == 0);
@@ -820,9 +856,9 @@ __global__ void __launch_bounds__(512, 1)
                             wait_kv(ks);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_S(t, 0, ks);
+                            issue_S(t, qb, ks);
                             tc_commit(BAR(SPKV_EMPTY + ks));
-                            if (x + 3 == n) tc_commit(BAR(SPQ_EMPTY + 0));
+                            if (x + 3 == n) tc_commit(BAR(SPQ_EMPTY + qb));
                         }
                     }
                     if (ok && n == 1) no_steps(1);
@@ -887,6 +923,181 @@ __global__ void __launch_bounds__(512, 1)
         // ------------------------------------------------------------- softmax
         setmaxnreg_inc<176>();
         const int t = wg - 1;
+        if constexpr (FEW > 0) {
+            // One thread per key of the tile, its scores of all rows in registers. The rows'
+            // maxima m (shared memory, common to the chain's 128 threads) follow the same
+            // rules as below; when some weight passes kSpanRise all four warps take the
+            // maxima anew. Sums are kept per thread and added up at the segment's end.
+            const int kl = (warp & 3) * 32 + lane;
+            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tS = tmem + lane_base + C::colS(t), tO = tmem + lane_base + C::colO(t);
+            // P goes to [64-key block][row][key], 128-byte rows, 16-byte chunks swizzled by row
+            const uint32_t p_at = sStage + t * C::kPTile + (uint32_t)(kl >> 6) * (FEW * 128u) + (uint32_t)(kl & 7) * 2u;
+            const uint32_t chunk = (uint32_t)(kl & 63) >> 3;
+            float *red = reinterpret_cast<float *>(sm + C::kOffRed) + t * 8 * FEW;  // [4][FEW], then m, its use, alpha
+            float *m_s = red + 4 * FEW, *me_s = red + 5 * FEW, *al_s = red + 6 * FEW;
+            volatile uint32_t *flags = misc + 2 + t;
+            const float sl2 = p.scale_log2;
+            uint32_t sph = 0;
+            bool ok = true;
+            volatile uint32_t *rise = reinterpret_cast<volatile uint32_t *>(red + 7 * FEW);  // by turns: the step that passed
+            uint32_t cph = 0, stamp = 0;
+            if (kl < 2) rise[kl] = 0u;
+            auto sync = [&]() {  // the chain's four warps meet (bounded, unlike a named barrier)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(SPCHAIN + t));
+                ok = ok && warp_bwait(BAR(SPCHAIN + t), cph, abort_flag, kSiteSoftS);
+                cph ^= 1u;
+            };
+            // v of all rows: the warps' results of `op` over their lanes to red, then a barrier
+            auto over_keys = [&](const float (&v)[FEW], auto op) {
+                float keep = 0.f;
+#pragma unroll
+                for (int r = 0; r < FEW; ++r) {
+                    float x = v[r];
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    keep = lane == r ? x : keep;
+                }
+                if (lane < FEW) red[(warp & 3) * FEW + lane] = keep;
+                sync();
+            };
+            while (ok) {
+                ok = SEG_WAIT(warp_bwait);
+                volatile SpanSeg &g = SEG;
+                if (!ok || g.n == 0) break;
+                const int rows = g.ntok * p.G;
+                if (kl < FEW) m_s[kl] = -INFINITY;
+                float l[FEW];
+#pragma unroll
+                for (int r = 0; r < FEW; ++r) l[r] = 0.f;
+                bool fresh = true;  // some row has not seen a key
+                int steps = (g.n + 1 - t) >> 1, c, c_end = g.hi - g.nw + 1;
+                {
+                    const int y = g.j0 + t, nw = g.nw;
+                    c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
+                    if (y >= nw) c_end = INT_MIN;
+                }
+#pragma unroll 1
+                for (; steps > 0; --steps) {
+                    const int c0 = c * 128;
+                    const bool masked = c0 > g.all_hi[0] || (c0 < g.all_lo[0] && c0 + 128 > p.sinks);
+                    c -= 2;
+                    if (c < c_end) {
+                        c += g.ns - c_end;
+                        c_end = INT_MIN;
+                    }
+                    ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
+                    if (!ok) break;
+                    sph ^= 1u;
+                    tc_fence_after();
+                    uint32_t s[FEW];
+                    float e[FEW];
+                    if constexpr (FEW == 16)
+                        tmem_ld16(tS, s);
+                    else
+                        tmem_ld32(tS, s);
+                    if (masked) {
+                        const int key = c0 + kl, keys = g.keys, pos0 = g.pos0;
+#pragma unroll
+                        for (int r = 0; r < FEW; ++r) {
+                            const int pos = pos0 + span_row_tok<PAGED>(p, r);
+                            const bool sees = key <= min(pos + p.right, keys - 1) && (key >= pos - p.left || key < p.sinks);
+                            s[r] = sees ? s[r] : f2u(-INFINITY);
+                        }
+                    }
+                    bool by_max = fresh;
+#pragma unroll 1
+                    for (;;) {
+                        if (by_max) {
+                            float v[FEW];
+#pragma unroll
+                            for (int r = 0; r < FEW; ++r) v[r] = u2f(s[r]);
+                            over_keys(v, [](float a, float b) { return fmaxf(a, b); });
+                            if (!ok) break;
+                            if ((warp & 3) == 0) {
+                                bool unseen = false, rise = false;
+                                if (lane < FEW) {
+                                    const float mx = fmaxf(fmaxf(red[lane], red[FEW + lane]),
+                                                           fmaxf(red[2 * FEW + lane], red[3 * FEW + lane])) * sl2;
+                                    const float old = m_s[lane];
+                                    const float now = old == -INFINITY || mx > old + 4.0f ? mx : old;
+                                    rise = old != -INFINITY && now != old && lane < rows;
+                                    unseen = now == -INFINITY && lane < rows;
+                                    m_s[lane] = now;
+                                    me_s[lane] = now == -INFINITY ? 0.f : now;
+                                    al_s[lane] = rise ? ex2_approx(old - now) : 1.f;
+                                }
+                                const uint32_t f = (__any_sync(0xffffffffu, unseen) ? 1u : 0u) |
+                                                   (__any_sync(0xffffffffu, rise) ? 2u : 0u);
+                                if (lane == 0) *flags = f;
+                            }
+                            sync();
+                            if (!ok) break;
+                            const uint32_t f = *flags;
+                            fresh = f & 1u;
+                            if (f & 2u) {
+                                // O^T is stable: the commit that signalled S_t covers the P V before
+                                uint32_t o[FEW];
+                                if constexpr (FEW == 16)
+                                    tmem_ld16(tO, o);
+                                else
+                                    tmem_ld32(tO, o);
+#pragma unroll
+                                for (int r = 0; r < FEW; ++r) {
+                                    l[r] *= al_s[r];
+                                    o[r] = f2u(u2f(o[r]) * al_s[r]);
+                                }
+                                if constexpr (FEW == 16)
+                                    tmem_st16(tO, o);
+                                else
+                                    tmem_st32(tO, o);
+                                tmem_st_wait();
+                            }
+                        }
+                        float top = 0.f;
+#pragma unroll
+                        for (int r = 0; r < FEW; ++r) {
+                            e[r] = ex2_approx(fmaf(u2f(s[r]), sl2, -me_s[r]));
+                            if (r < rows) top = fmaxf(top, e[r]);
+                        }
+                        if (by_max) break;
+                        if (__any_sync(0xffffffffu, top > kSpanRise) && lane == 0) rise[stamp & 1u] = stamp + 1u;
+                        sync();
+                        if (!ok) break;
+                        by_max = rise[stamp & 1u] == stamp + 1u;
+                        ++stamp;
+                        if (!by_max) break;
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int r = 0; r < FEW; r += 2) {
+                        l[r] += e[r];
+                        l[r + 1] += e[r + 1];
+                        const uint32_t two = pack_bf16x2(e[r], e[r + 1]);
+                        st_shared_u16(p_at + r * 128u + ((chunk ^ (r & 7)) << 4), two & 0xffffu);
+                        st_shared_u16(p_at + (r + 1) * 128u + ((chunk ^ ((r + 1) & 7)) << 4), two >> 16);
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
+                }
+                if (!ok) break;
+                over_keys(l, [](float a, float b) { return a + b; });
+                if (!ok) break;
+                ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
+                if (!ok) break;
+                if (kl < FEW) {
+                    row_ml[t * 256 + kl] = red[kl] + red[FEW + kl] + red[2 * FEW + kl] + red[3 * FEW + kl];
+                    row_ml[t * 256 + 128 + kl] = m_s[kl];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(SPL_FULL + t));
+                SEG_DONE();
+                sync();  // red and m are free for the next segment
+            }
+        } else {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::colS(t);
         const uint32_t tO = tmem + lane_base + C::colO(t);
@@ -1079,6 +1290,7 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) mbar_arrive(BAR(SPL_FULL + t));
             SEG_DONE();
         }
+        }
     } else {
         // ------------------------------------------------------------ epilogue
         setmaxnreg_dec<112>();
@@ -1138,7 +1350,53 @@ __global__ void __launch_bounds__(512, 1)
                 rec[R::kML + t * 256 + row] = m;
                 rec[R::kML + t * 256 + 128 + row] = l;
             };
-            if (g.dual) {
+            if constexpr (FEW > 0) {
+                // one thread per column of the output, all rows
+                ok = warp_bwait(BAR(SPO_FINAL + 0), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     warp_bwait(BAR(SPO_FINAL + 1), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     warp_bwait(BAR(SPL_FULL + 0), seg_it & 1u, abort_flag, kSiteEpiL) &&
+                     warp_bwait(BAR(SPL_FULL + 1), seg_it & 1u, abort_flag, kSiteEpiL);
+                if (!ok) break;
+                tc_fence_after();
+                const int rows = g.ntok * p.G, head = g.head, tok0 = g.tok0, q_row = g.q0;
+                uint32_t o0[FEW], o1[FEW];
+                if constexpr (FEW == 16) {
+                    tmem_ld16(tmem + lane_base + C::colO(0), o0);
+                    tmem_ld16(tmem + lane_base + C::colO(1), o1);
+                } else {
+                    tmem_ld32(tmem + lane_base + C::colO(0), o0);
+                    tmem_ld32(tmem + lane_base + C::colO(1), o1);
+                }
+                release_o(0);
+                release_o(1);
+#pragma unroll
+                for (int r = 0; r < FEW; ++r) {
+                    if (r >= rows) break;
+                    const float l0 = row_ml[r], m0 = row_ml[128 + r], l1 = row_ml[256 + r], m1 = row_ml[384 + r];
+                    const float m = fmaxf(m0, m1);
+                    const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+                    const float l = a0 * l0 + a1 * l1;
+                    float f = a0 > 0.f ? u2f(o0[r]) * a0 : 0.f;
+                    f = a1 > 0.f ? fmaf(u2f(o1[r]), a1, f) : f;
+                    if (row >= D) continue;
+                    if (piece) {
+                        rec[r * D + row] = f;
+                        if (row == 0) {
+                            rec[R::kML + r] = m;
+                            rec[R::kML + 128 + r] = l;
+                        }
+                    } else {
+                        const int tk = span_row_tok<PAGED>(p, r);
+                        p.out[span_out_offset<D, PAGED>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
+                            (uint16_t)pack_bf16x2(l > 0.f ? f * (1.0f / l) : 0.f, 0.f);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(BAR(SPL_EMPTY + 0));
+                    mbar_arrive(BAR(SPL_EMPTY + 1));
+                }
+            } else if (g.dual) {
                 float l0 = 0.f, m0 = 0.f, l1 = 0.f, m1 = 0.f;
                 take_ml(0, l0, m0);
                 if (ok) take_ml(1, l1, m1);
@@ -1221,7 +1479,7 @@ __global__ void __launch_bounds__(512, 1)
 // segment: piece 0 in the record named by the CTA, piece i > 0 in the first
 // record of CTA blockIdx.x + i. One thread per row and 4 columns; the pieces'
 // loads go out eight at a time, their latency being all that this costs.
-template <int D, bool PAGED>
+template <int D, bool PAGED, int FEW>
 __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__ SpanParams p) {
     using R = Rec<D>;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the attention kernel is done from here on
@@ -1231,10 +1489,12 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     const int rows = s.ntok * p.G;
     constexpr int U = 8;
     for (int i = (int)(blockIdx.y * 256 + threadIdx.x); i < rows * (D / 4); i += (int)gridDim.y * 256) {
-        // lanes hold neighbouring rows of one column group, as the records do
-        const int c4 = i / rows, r = i - c4 * rows;
+        // lanes hold neighbouring rows of one column group, or with few rows neighbouring
+        // column groups of one row, as the records do
+        const int c4 = FEW ? i % (D / 4) : i / rows, r = FEW ? i / (D / 4) : i - c4 * rows;
         const int t = r >= rows0 ? 1 : 0, row = t ? r - rows0 : r;
-        const size_t o_at = ((size_t)t * (D / 4) + c4) * 128 + row, ml_at = R::kML + t * 256 + row;
+        const size_t o_at = FEW ? (size_t)row * (D / 4) + c4 : ((size_t)t * (D / 4) + c4) * 128 + row;
+        const size_t ml_at = R::kML + t * 256 + row;
         float M = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = 0; k0 < s.pieces; k0 += U) {
@@ -1274,20 +1534,20 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     }
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int FEW>
 static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
-    auto kern = span_attn_kernel<D, PAGED>;
+    auto kern = span_attn_kernel<D, PAGED, FEW>;
     static std::atomic<uint64_t> configured{0};  // devices where the shared-memory limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D>::kSmemAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, FEW>::kSmemAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    kern<<<grid, 512, SpanCfg<D>::kSmemAlloc, stream>>>(maps, p);
+    kern<<<grid, 512, SpanCfg<D, FEW>::kSmemAlloc, stream>>>(maps, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.rec) {
         // set up while the attention kernel still runs; it waits for its end itself
@@ -1300,14 +1560,17 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, span_merge_kernel<D, PAGED>, p);
+        e = cudaLaunchKernelEx(&cfg, span_merge_kernel<D, PAGED, FEW>, p);
     }
     return e;
 }
 
 #define XS_DEFINE_SPAN_ENTRY(D)                                                                                       \
     cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
-        return p.table ? launch_span_one<D, true>(maps, p, grid, stream) : launch_span_one<D, false>(maps, p, grid, stream); \
+        if (!p.table) return launch_span_one<D, false, 0>(maps, p, grid, stream);                                     \
+        if (p.few == 16) return launch_span_one<D, true, 16>(maps, p, grid, stream);                                  \
+        if (p.few == 32) return launch_span_one<D, true, 32>(maps, p, grid, stream);                                  \
+        return launch_span_one<D, true, 0>(maps, p, grid, stream);                                                    \
     }                                                                                                                 \
     cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear) {                                          \
         cudaError_t e = cudaMemcpyFromSymbol(value, g_xs_error, sizeof(unsigned int));                                \

@@ -13,7 +13,7 @@ class Batch:
     """A cache with scattered pages. Whatever no sequence owns holds NaN; table entries past a sequence's pages hold
     numbers far outside the pool."""
 
-    def __init__(self, q_len, kv_len, H, Hk, D, page, spare=0, seed=0, sigma=1.0, evict=0):
+    def __init__(self, q_len, kv_len, H, Hk, D, page, spare=0, seed=0, sigma=1.0, evict=0, ramp=None):
         import torch
         rng = np.random.default_rng(seed)
         self.q_len, self.kv, self.H, self.Hk, self.D, self.page = q_len, kv_len, H, Hk, D, page
@@ -27,6 +27,11 @@ class Batch:
         self.k, self.v, at = [], [], 0
         for n in range(self.N):
             kb, k = bf16(rng, (kv_len[n], Hk, D), sigma)
+            if ramp:  # keys that point along the queries, longer from `ramp[1]` to `ramp[0]` times along the sequence
+                import torch
+                long = np.linspace(ramp[0], ramp[1], max(kv_len[n], 1)).reshape(-1, 1, 1)
+                kb = torch.from_numpy((np.abs(k) * long).astype(np.float32)).bfloat16().view(torch.int16).numpy().view(np.uint16)
+                k = values(kb)
             vb, v = bf16(rng, (kv_len[n], Hk, D))
             self.k.append(k)
             self.v.append(v)
@@ -39,6 +44,9 @@ class Batch:
             for j in range(evict):  # pages that a window has passed: their entries may hold anything
                 table[n, j] = (-7, 2 ** 31 - 1)[j % 2]
         self.qb, self.q = bf16(rng, (self.T, H, D), sigma)
+        if ramp:
+            self.qb = self.qb & 0x7FFF
+            self.q = np.abs(self.q)
         self.table = torch.from_numpy(table.astype(np.int32)).cuda()
         self.q_start = torch.tensor(np.concatenate(([0], np.cumsum(q_len))), dtype=torch.int32, device="cuda")
         self.kv_len = torch.tensor(kv_len, dtype=torch.int32, device="cuda")
@@ -124,6 +132,28 @@ def test_paged_peaked_scores():
     b = Batch([1, 40], [2000, 700], 8, 2, 128, 16, seed=3, sigma=4.0)
     b.call()
     b.verify()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_len,H,Hk", (([1, 1], 4, 2), ([2, 3], 16, 2), ([70, 1], 4, 2)))
+@pytest.mark.parametrize("ramp", ((8.0, 0.0), (0.0, 8.0)))
+def test_paged_rising_and_falling_keys(q_len, H, Hk, ramp):
+    """Scores that grow by hundreds along the sequence or against it: the running maxima move in every tile."""
+    b = Batch(q_len, [1900, 900], H, Hk, 128, 32, seed=4, ramp=ramp)
+    b.call()
+    b.verify()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", (64, 96, 128))
+@pytest.mark.parametrize("G,q_len", ((1, [1, 1, 1]), (5, [3, 1, 0]), (16, [1, 1, 1]), (11, [4, 1, 1]), (32, [1, 1, 1])))
+def test_paged_few_rows(D, G, q_len):
+    """Groups that do and do not fill the few-rows tiles, sequences of more tokens than one tile among them, and a
+    window whose pieces begin behind it."""
+    for page, span in ((16, (-1, 0, 0)), (256, (300, 0, 2)), (64, (40, 3, 200))):
+        b = Batch(q_len, [2500, 129, 700], 2 * G, 2, D, page, spare=2, seed=G + D)
+        b.call(*span)
+        b.verify(*span, what=f"{page} {span}")
 
 
 @pytest.mark.gpu
