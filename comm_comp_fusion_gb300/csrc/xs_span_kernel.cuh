@@ -81,9 +81,10 @@ enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 template <int D, int FEW> struct SpanCfg {
     static constexpr int kNDB = Cfg<D>::kNDB;
     static constexpr uint32_t kBlk = Cfg<D>::kBlk, kTile = Cfg<D>::kTile;
-    // K/V ring: single new tokens stream K/V at the rate of what is in flight, so it
-    // takes what shared memory the rest leaves (16 KB slots at D = 64, else 32 KB).
-    static constexpr int kSlots = D == 64 ? (FEW ? 10 : 8) : FEW == 16 ? 6 : FEW ? 5 : 4;
+    // K/V ring of 128 KB, in 16 KB (D = 64) or 32 KB slots. More in flight, where few
+    // rows leave the room, was slower: 32 single tokens over 16000 keys of 8 heads, D =
+    // 128, 320 us with 4 slots, 328 with 5, 339 with 6.
+    static constexpr int kSlots = D == 64 ? 8 : 4;
     static constexpr uint32_t kOffKV = 0;
     // Q: two tiles of the item, or with few rows two items' tiles
     static constexpr uint32_t kQBlk = FEW ? FEW * 128u : kBlk, kQTile = kNDB * kQBlk;
@@ -107,6 +108,7 @@ template <int D, int FEW> struct SpanCfg {
     }
     static constexpr uint32_t kTmemCols = FEW ? 4 * FEW : 512;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
+    static_assert(kSlots <= SPKV_EMPTY - SPKV_FULL, "barriers of the ring");
     static_assert(kOffQ % 1024 == 0 && kOffStage % 1024 == 0, "swizzled tiles");
 };
 
@@ -665,25 +667,6 @@ __global__ void __launch_bounds__(512, 1)
                 const int n = g.n, j0 = g.j0, head = g.head;
                 if (!ok || n == 0) break;
                 const bool dual = g.dual;
-                for (int i = 0; i < (dual ? 1 : 2) && ok; ++i) {
-                    const int t = FEW ? (int)(seg_it & 1u) : i;  // few rows: items take the two tiles in turn
-                    const uint32_t use = FEW ? seg_it >> 1 : t ? q_it1++ : q_it0++;
-                    ok = warp_bwait(BAR(SPQ_EMPTY + t), (use & 1u) ^ 1u, abort_flag, kSiteLoadQ);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(BAR(SPQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
-                        const int tok = g.q0 + g.tok0 + i * p.tile_tok;
-#pragma unroll
-                        for (int db = 0; db < C::kNDB; ++db) {
-                            const uint32_t dst = sQ + t * C::kQTile + db * C::kQBlk;
-                            if (PAGED)
-                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, 0, head, tok);
-                            else
-                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
-                        }
-                    }
-                }
-                if (!ok) break;
                 // page of this lane's box of step x's tile; n_pages (outside the pool)
                 // where no token of the item sees any of its keys
                 const int *table = PAGED ? p.table + (int64_t)g.seq * p.max_pages : nullptr;
@@ -716,6 +699,25 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 };
                 int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
+                for (int i = 0; i < (dual ? 1 : 2) && ok; ++i) {
+                    const int t = FEW ? (int)(seg_it & 1u) : i;  // few rows: items take the two tiles in turn
+                    const uint32_t use = FEW ? seg_it >> 1 : t ? q_it1++ : q_it0++;
+                    ok = warp_bwait(BAR(SPQ_EMPTY + t), (use & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(BAR(SPQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
+                        const int tok = g.q0 + g.tok0 + i * p.tile_tok;
+#pragma unroll
+                        for (int db = 0; db < C::kNDB; ++db) {
+                            const uint32_t dst = sQ + t * C::kQTile + db * C::kQBlk;
+                            if (PAGED)
+                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, 0, head, tok);
+                            else
+                                tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
+                        }
+                    }
+                }
+                if (!ok) break;
                 load_tile(&tm.k, 0, pg0);
                 if (ok && dual && n > 1) load_tile(&tm.k, 1, pg1);
                 for (int x = 0; ok && x < n; ++x) {
@@ -949,17 +951,20 @@ __global__ void __launch_bounds__(512, 1)
                 ok = ok && warp_bwait(BAR(SPCHAIN + t), cph, abort_flag, kSiteSoftS);
                 cph ^= 1u;
             };
-            // v of all rows: the warps' results of `op` over their lanes to red, then a barrier
-            auto over_keys = [&](const float (&v)[FEW], auto op) {
-                float keep = 0.f;
+            // v of all rows: the warps' results of `op` over their lanes to red, then a barrier.
+            // Each exchange halves the rows a lane holds; it ends with one row, lane / (32 / FEW).
+            auto over_keys = [&](float (&v)[FEW], auto op) {
 #pragma unroll
-                for (int r = 0; r < FEW; ++r) {
-                    float x = v[r];
+                for (int n = FEW / 2, d = 16; n; n >>= 1, d >>= 1) {
+                    const bool up = lane & d;
 #pragma unroll
-                    for (int d = 16; d; d >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    keep = lane == r ? x : keep;
+                    for (int i = 0; i < n; ++i) {
+                        const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, d));
+                    }
                 }
-                if (lane < FEW) red[(warp & 3) * FEW + lane] = keep;
+                if (FEW == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+                red[(warp & 3) * FEW + (FEW == 16 ? lane >> 1 : lane)] = v[0];
                 sync();
             };
             while (ok) {
