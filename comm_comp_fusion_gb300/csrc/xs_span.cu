@@ -21,9 +21,9 @@ void span_workspace_parts(void *ws, int D, int num_sms, SpanParams *p) {
 cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int num_sms, cudaStream_t stream) {
     SpanParams q = p;
     q.min_steps_log2 = p.table ? 1 : 2;
-    // a merge thread adds up 4 columns of one row
-    const long long rows = (long long)std::min(p.T, p.item_tok) * p.G;
-    q.merge_y = (int)std::max(1ll, (rows * (D / 4) + 255) / 256);
+    // a merge block adds up 32 rows of an item, or with few rows 256 groups of 4 columns
+    const int rows = std::min(p.T, p.item_tok) * p.G, tile = p.tile_tok * p.G;
+    q.merge_y = p.few ? (rows * (D / 4) + 255) / 256 : rows > tile ? 8 : (rows + 31) / 32;
     const int grid = p.rec ? num_sms : (int)std::min((long long)num_sms, (long long)p.heads * p.n_pairs);
     if (D == 64) return launch_span_d64(maps, q, grid, stream);
     if (D == 96) return launch_span_d96(maps, q, grid, stream);
