@@ -128,6 +128,61 @@ def test_paged_passed_pages_may_hold_anything(D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_len", ([1, 1], [90, 40]))
+def test_paged_sequences_share_pages(q_len):
+    """Two sequences with the same first pages (a common prefix), and one page named twice in a row of the table."""
+    b = Batch(q_len, [600, 500], 4, 2, 128, 64, seed=12)
+    b.table[1, :5] = b.table[0, :5]
+    b.table[0, 6] = b.table[0, 7]
+    b.k[1][:320], b.v[1][:320] = b.k[0][:320], b.v[0][:320]
+    b.k[0][384:448], b.v[0][384:448] = b.k[0][448:512], b.v[0][448:512]
+    b.call()
+    b.verify()
+
+
+@pytest.mark.gpu
+def test_paged_starts_behind_the_first_row():
+    """Packed rows before q_start[0] and behind q_start[N] belong to no sequence."""
+    b = Batch([3, 2], [200, 90], 4, 2, 64, 16, spare=6, seed=14)
+    b.q_start += 4
+    b.call()
+    whole = from_dev(b.out).reshape(b.T, 4, 64)
+    assert (whole[:4] == 0xFFFF).all() and (whole[9:] == 0xFFFF).all()
+    b.out = to_dev(np.concatenate((whole[4:9], whole[9:], whole[:4])))
+    b.q = np.concatenate((b.q[4:], b.q[:4]))
+    b.verify()
+
+
+@pytest.mark.gpu
+def test_paged_long_chunk_sampled():
+    """A chunk over a long cache: items of many K/V tiles in pieces, one row of every 60 against 64 bits."""
+    import torch
+    b = Batch([1000], [30000], 8, 2, 128, 128, seed=15)
+    b.call()
+    torch.cuda.synchronize()
+    got = from_dev(b.out).reshape(b.T, 8, 128)
+    rows = np.arange(0, 1000, 60)
+    for h in range(8):
+        ref, bound = attend(b.q[rows, h], b.k[0][:, h // 4], b.v[0][:, h // 4], seen_mask(29000 + rows, 30000, -1, 0, 0),
+                            128 ** -0.5)
+        check(got[rows, h], ref, bound, f"h={h}")
+
+
+@pytest.mark.gpu
+def test_paged_on_two_streams_at_once():
+    import torch
+    a, c = Batch([1] * 6, [900] * 6, 8, 2, 128, 16, seed=16), Batch([300, 20], [1500, 700], 4, 4, 64, 32, seed=17)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for x, s in zip((a, c), streams):
+            x.call(stream=s)
+    torch.cuda.synchronize()
+    a.verify()
+    c.verify()
+
+
+@pytest.mark.gpu
 def test_paged_peaked_scores():
     b = Batch([1, 40], [2000, 700], 8, 2, 128, 16, seed=3, sigma=4.0)
     b.call()

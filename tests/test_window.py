@@ -111,6 +111,20 @@ def test_window_falling_keys_after_far_first_tile():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("span", ((3000, 0, 70), (-1, 0, 0), (1500, 2500, 0)))
+def test_window_long_sampled(span):
+    """A long ragged sequence: items of many K/V tiles, one row of every query tile against 64 bits."""
+    B, S, H, D, P = 1, 12040, 6, 128, 2
+    rng = np.random.default_rng(77)
+    (qb, q), (kb, k), (vb, v) = (bf16(rng, (B, S, H, D)) for _ in range(3))
+    got = run((B, S, H, D, P, *span, 1.0), *[to_dev(tokens_to_head(x, P)) for x in (qb, kb, vb)], D ** -0.5)
+    for h in range(H):
+        rows = np.minimum(np.arange(0, S, 128) + rng.integers(0, 128, -(-S // 128)), S - 1)
+        ref, bound = attend(q[0, rows, h], k[0, :, h], v[0, :, h], seen_mask(rows, S, *span), D ** -0.5)
+        check(got[0, rows, h], ref, bound, f"{span} h={h}")
+
+
+@pytest.mark.gpu
 def test_window_unlimited_is_causal_and_full_attention():
     import torch
     import comm_comp_fusion_gb300 as xs
