@@ -270,15 +270,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
@@ -345,10 +336,6 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t in, uint32_t &lo, uint3
 
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x0), "r"(x1), "r"(x2), "r"(x3) : "memory");
-}
-
-__device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t x) {
-    asm volatile("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
 }
 
 // Orders this thread's generic-proxy shared-memory writes before later

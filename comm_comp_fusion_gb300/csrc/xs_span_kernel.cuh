@@ -67,6 +67,19 @@
 
 namespace xs {
 
+// 32 lanes x 32-bit, 16 consecutive columns per thread, to tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t x) {
+    asm volatile("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
+}
+
 constexpr int kSegs = 6;  // segments in the ring
 // mbarriers; per query tile (chain) 2 of each of the first eight, per ring slot 2, per segment 2.
 enum : int {
