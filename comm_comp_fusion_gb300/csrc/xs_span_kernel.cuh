@@ -29,9 +29,9 @@
 //     turned round, S^T = K Q^T and O^T = V^T P^T, so that the 128 rows of an MMA
 //     are keys (or columns of V) and the query rows are its N. A softmax thread
 //     then holds one key's scores of all rows: 16 exponentials a step where the
-//     other form spends 128 on rows that mostly do not exist, and a step of a chain
-//     takes @FEWSTEP@ cycles instead of 3300, so that short calls end sooner and
-//     D = 64 and 96 are bound by HBM too.
+//     other form spends 128 on rows that mostly do not exist (four sequences of 300
+//     to 1200 keys: 14.7 us against 16.7; 64 of 4000 to 8000 keys, D = 64: 156
+//     against 166).
 //
 // Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
 // ordered by sequence, head and query rows, and each CTA takes an equal,
@@ -46,9 +46,16 @@
 // unnormalised O, row maxima and sums to the workspace, and span_merge_kernel
 // adds them up in piece order (no atomics: the result is the same every time).
 //
+// Bounds. Single new tokens: HBM (32 sequences of 16000 keys, 8 key heads, D = 128: 320
+// us, 6.55 TB/s; rows of 128 bytes, D = 64, reach 5.05 TB/s). Long chunks and windows:
+// the chain S - softmax - P V of a step, about 2950 cycles for two tiles at D = 128
+// (chunks of 2048 over 16K keys, 32 heads: 655 us, 1.64 PFLOP/s). Short calls: about 10
+// us of set-up, first loads and first steps, whose instructions are fetched cold.
+//
 // Roles of the 512 threads (registers 48 / 176 / 176 / 112 a thread):
-//   warp 0      TMA producer: Q tiles, then K and V tiles into a 4-slot ring. Pages
-//               shorter than a tile take one box each, issued by as many lanes;
+//   warp 0      TMA producer: Q tiles, then K and V tiles into a 128 KB ring. Pages
+//               shorter than a tile take one box each, issued by as many lanes (by
+//               one lane in turn: 431 us instead of 371 for 32 long single tokens);
 //               page numbers are fetched three tiles ahead. Pages that no token
 //               sees are not read (their box lies outside the pool: zeros).
 //   warp 1      MMA issuer
@@ -122,6 +129,7 @@ template <int D, int FEW> struct SpanCfg {
     static constexpr uint32_t kTmemCols = FEW ? 4 * FEW : 512;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
     static_assert(kSlots <= SPKV_EMPTY - SPKV_FULL, "barriers of the ring");
+    static_assert(kSlots * kTile >= 8u * 2048u, "the schedule's sums (kSpanMaxChunks)");
     static_assert(kOffQ % 1024 == 0 && kOffStage % 1024 == 0, "swizzled tiles");
 };
 
@@ -592,7 +600,7 @@ __global__ void __launch_bounds__(512, 1)
         tmem_relinquish();
     }
     const int chunks = ((PAGED ? p.N : p.n_pairs) + 31) / 32;
-    long long *sums = reinterpret_cast<long long *>(sm + C::kOffStage);
+    long long *sums = reinterpret_cast<long long *>(sm + C::kOffKV);  // the ring is not in use yet
     SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSeg + 96 * kSegs);
     if (PAGED || p.rec) {
         if (chunks > 1) {
@@ -603,6 +611,7 @@ __global__ void __launch_bounds__(512, 1)
             const SpanSched s = span_schedule<PAGED>(p, chunks, sums, lane);
             if (lane == 0) *sched = s;
         }
+        if (chunks > 1) fence_proxy_async_smem();  // before TMA writes there
     }
     tc_fence_before();
     __syncthreads();
@@ -1148,198 +1157,198 @@ __global__ void __launch_bounds__(512, 1)
                 sync();  // red and m are free for the next segment
             }
         } else {
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + C::colS(t);
-        const uint32_t tO = tmem + lane_base + C::colO(t);
-        const int row = (warp & 3) * 32 + lane;
-        const float sl2 = p.scale_log2;
-        uint32_t sph = 0;
-        bool ok = true;
-        while (ok) {
-            ok = SEG_WAIT(warp_bwait);
-            volatile SpanSeg &g = SEG;
-            if (!ok || g.n == 0) break;
-            // lim: the row sum that calls for the row max again: none for a row that does
-            // not exist, any for one that has not seen a key yet
-            float m = -INFINITY, l = 0.f, lim;
-            bool idle;
-            {
-                const int rows = min(g.ntok - (g.dual ? 0 : t * p.tile_tok), p.tile_tok) * p.G;
-                lim = row < rows ? -1.f : INFINITY;
-                idle = (warp & 3) * 32 >= rows;  // no row of this warp exists
-            }
-            // This tile's (chain's) steps and K/V tiles: c, c - step, ... down to c_end, then
-            // the sinks' from ns - 1 on.
-            int steps, c, c_end = g.hi - g.nw + 1;
-            {
-                const int n = g.n, j0 = g.j0, nw = g.nw;
-                int y = j0;  // the first step's
-                if (g.dual) {
-                    steps = (n + 1 - t) >> 1;
-                    y += t;
-                } else if (t == 0) {
-                    y = max(j0, g.s0);
-                    steps = j0 + n - y;
-                } else {
-                    const int e1 = g.e1;
-                    steps = max(0, min(e1, j0 + n) - j0) + max(0, j0 + n - max(nw, j0));
-                    if (y >= e1) y = max(y, nw);
-                    c_end = g.hi - e1 + 1;
+            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tS = tmem + lane_base + C::colS(t);
+            const uint32_t tO = tmem + lane_base + C::colO(t);
+            const int row = (warp & 3) * 32 + lane;
+            const float sl2 = p.scale_log2;
+            uint32_t sph = 0;
+            bool ok = true;
+            while (ok) {
+                ok = SEG_WAIT(warp_bwait);
+                volatile SpanSeg &g = SEG;
+                if (!ok || g.n == 0) break;
+                // lim: the row sum that calls for the row max again: none for a row that does
+                // not exist, any for one that has not seen a key yet
+                float m = -INFINITY, l = 0.f, lim;
+                bool idle;
+                {
+                    const int rows = min(g.ntok - (g.dual ? 0 : t * p.tile_tok), p.tile_tok) * p.G;
+                    lim = row < rows ? -1.f : INFINITY;
+                    idle = (warp & 3) * 32 >= rows;  // no row of this warp exists
                 }
-                c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
-                if (y >= nw) c_end = INT_MIN;
-            }
-            // Rows whose keys end in an earlier tile than the first see none in it, so the
-            // maxima are taken over the first two steps.
-            const int settled = steps - 2;
+                // This tile's (chain's) steps and K/V tiles: c, c - step, ... down to c_end, then
+                // the sinks' from ns - 1 on.
+                int steps, c, c_end = g.hi - g.nw + 1;
+                {
+                    const int n = g.n, j0 = g.j0, nw = g.nw;
+                    int y = j0;  // the first step's
+                    if (g.dual) {
+                        steps = (n + 1 - t) >> 1;
+                        y += t;
+                    } else if (t == 0) {
+                        y = max(j0, g.s0);
+                        steps = j0 + n - y;
+                    } else {
+                        const int e1 = g.e1;
+                        steps = max(0, min(e1, j0 + n) - j0) + max(0, j0 + n - max(nw, j0));
+                        if (y >= e1) y = max(y, nw);
+                        c_end = g.hi - e1 + 1;
+                    }
+                    c = y < nw ? g.hi - y : g.ns - 1 - (y - nw);
+                    if (y >= nw) c_end = INT_MIN;
+                }
+                // Rows whose keys end in an earlier tile than the first see none in it, so the
+                // maxima are taken over the first two steps.
+                const int settled = steps - 2;
 #pragma unroll 1
-            for (; steps > 0; --steps) {
-                const int c0 = c * 128;
-                const bool masked = c0 > g.all_hi[t] || (c0 < g.all_lo[t] && c0 + 128 > p.sinks);
-                c -= 1 + g.dual;
-                if (c < c_end) {
-                    c += g.ns - c_end;
-                    c_end = INT_MIN;
-                }
-                ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
-                if (!ok) break;
-                sph ^= 1u;
-                if (idle) {  // P keeps what S left there: only rows that do not exist read it
-                    if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
-                    continue;
-                }
-                tc_fence_after();
-                uint32_t sa[64], sb[64];  // this thread's row of S: columns 0-63, 64-127
+                for (; steps > 0; --steps) {
+                    const int c0 = c * 128;
+                    const bool masked = c0 > g.all_hi[t] || (c0 < g.all_lo[t] && c0 + 128 > p.sinks);
+                    c -= 1 + g.dual;
+                    if (c < c_end) {
+                        c += g.ns - c_end;
+                        c_end = INT_MIN;
+                    }
+                    ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
+                    if (!ok) break;
+                    sph ^= 1u;
+                    if (idle) {  // P keeps what S left there: only rows that do not exist read it
+                        if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
+                        continue;
+                    }
+                    tc_fence_after();
+                    uint32_t sa[64], sb[64];  // this thread's row of S: columns 0-63, 64-127
 #define SV(i) u2f((i) < 64 ? sa[(i) & 63] : sb[(i) & 63])
-                uint32_t pk[64];
-                float lstep = 0.f;
-                auto load_scores = [&]() {
-                    tmem_ld64x2(tS, sa, sb);
-                    if (masked) {
-                        const uint32_t ninf = f2u(-INFINITY);
-                        // places of this row's token and of the last key it may see
-                        const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
-                        const int row_hi = min(pos + p.right, g.keys - 1);
+                    uint32_t pk[64];
+                    float lstep = 0.f;
+                    auto load_scores = [&]() {
+                        tmem_ld64x2(tS, sa, sb);
+                        if (masked) {
+                            const uint32_t ninf = f2u(-INFINITY);
+                            // places of this row's token and of the last key it may see
+                            const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
+                            const int row_hi = min(pos + p.right, g.keys - 1);
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, 32 * h);
-                            if (__all_sync(0xffffffffu, bits == ~0u)) continue;  // a mask's edge crosses one or two of the four
+                            for (int h = 0; h < 4; ++h) {
+                                const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, 32 * h);
+                                if (__all_sync(0xffffffffu, bits == ~0u)) continue;  // a mask's edge crosses one or two of the four
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                uint32_t &s = h < 2 ? sa[(h & 1) * 32 + i] : sb[(h & 1) * 32 + i];
-                                s = (bits >> i) & 1u ? s : ninf;
+                                for (int i = 0; i < 32; ++i) {
+                                    uint32_t &s = h < 2 ? sa[(h & 1) * 32 + i] : sb[(h & 1) * 32 + i];
+                                    s = (bits >> i) & 1u ? s : ninf;
+                                }
                             }
                         }
-                    }
-                };
-                auto row_max = [&]() {
-                    float mx0 = fmaxf(u2f(sa[0]), u2f(sa[1])), mx1 = fmaxf(u2f(sa[2]), u2f(sa[3]));
-                    float mx2 = fmaxf(u2f(sa[4]), u2f(sa[5])), mx3 = fmaxf(u2f(sa[6]), u2f(sa[7]));
+                    };
+                    auto row_max = [&]() {
+                        float mx0 = fmaxf(u2f(sa[0]), u2f(sa[1])), mx1 = fmaxf(u2f(sa[2]), u2f(sa[3]));
+                        float mx2 = fmaxf(u2f(sa[4]), u2f(sa[5])), mx3 = fmaxf(u2f(sa[6]), u2f(sa[7]));
 #pragma unroll
-                    for (int i = 8; i < 64; i += 8) {
-                        mx0 = fmax3(mx0, u2f(sa[i + 0]), u2f(sa[i + 1]));
-                        mx1 = fmax3(mx1, u2f(sa[i + 2]), u2f(sa[i + 3]));
-                        mx2 = fmax3(mx2, u2f(sa[i + 4]), u2f(sa[i + 5]));
-                        mx3 = fmax3(mx3, u2f(sa[i + 6]), u2f(sa[i + 7]));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 64; i += 8) {
-                        mx0 = fmax3(mx0, u2f(sb[i + 0]), u2f(sb[i + 1]));
-                        mx1 = fmax3(mx1, u2f(sb[i + 2]), u2f(sb[i + 3]));
-                        mx2 = fmax3(mx2, u2f(sb[i + 4]), u2f(sb[i + 5]));
-                        mx3 = fmax3(mx3, u2f(sb[i + 6]), u2f(sb[i + 7]));
-                    }
-                    return fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
-                };
-                // p = exp2(s * scale*log2e - m); a row that has seen no key yet takes m = 0,
-                // its scores being -inf
-                auto exps = [&]() {
-                    const float me = m == -INFINITY ? 0.f : m;
-                    const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-me, -me);
-                    uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const int e = 2 * i;
-                        float e0, e1, e2, e3;
-                        f2unpack(ffma2(f2pack(SV(e), SV(e + 1)), sc2, nm2), e0, e1);
-                        f2unpack(ffma2(f2pack(SV(e + 2), SV(e + 3)), sc2, nm2), e2, e3);
-                        e0 = ex2_approx(e0);
-                        e1 = ex2_approx(e1);
-                        e2 = ex2_approx(e2);
-                        e3 = ex2_approx(e3);
-                        acc0 = fadd2(acc0, f2pack(e0, e1));
-                        acc1 = fadd2(acc1, f2pack(e2, e3));
-                        pk[i] = pack_bf16x2(e0, e1);
-                        pk[i + 1] = pack_bf16x2(e2, e3);
-                    }
-                    float a0, a1;
-                    f2unpack(fadd2(acc0, acc1), a0, a1);
-                    lstep = a0 + a1;
-                };
-                load_scores();
-                if (steps > settled) {
-                    const float mx = row_max();
-                    if (lim < 0.f && mx > -INFINITY) {
-                        m = mx;
-                        lim = kSpanRise;
-                    }
-                }
-                exps();
-                // A row keeps its max while no row sum passes kSpanRise: p, l and O are floating
-                // point, so a maximum that lags by up to 2^14 costs no precision, and a first
-                // tile with only a few keys in it (a causal diagonal) seldom has to be put
-                // right. A row that sees its first key later yet (a piece that begins behind
-                // its window) gets its max here too. Until then its weights, sum and O are 0.
-                if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // not at the first step
-                    load_scores();
-                    const float mnew = row_max();
-                    float alpha = 1.f;
-                    if (mnew > m) {
-                        alpha = ex2_approx(m - mnew);
-                        m = mnew;
-                        if (lim < 0.f) lim = kSpanRise;
-                    }
-                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                        // The commit that signalled S_t for this step also covers the
-                        // previous O_t += P V, so O_t is stable here.
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + c, o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
-                            tmem_st32(tO + c, o);
+                        for (int i = 8; i < 64; i += 8) {
+                            mx0 = fmax3(mx0, u2f(sa[i + 0]), u2f(sa[i + 1]));
+                            mx1 = fmax3(mx1, u2f(sa[i + 2]), u2f(sa[i + 3]));
+                            mx2 = fmax3(mx2, u2f(sa[i + 4]), u2f(sa[i + 5]));
+                            mx3 = fmax3(mx3, u2f(sa[i + 6]), u2f(sa[i + 7]));
                         }
-                        l *= alpha;
+#pragma unroll
+                        for (int i = 0; i < 64; i += 8) {
+                            mx0 = fmax3(mx0, u2f(sb[i + 0]), u2f(sb[i + 1]));
+                            mx1 = fmax3(mx1, u2f(sb[i + 2]), u2f(sb[i + 3]));
+                            mx2 = fmax3(mx2, u2f(sb[i + 4]), u2f(sb[i + 5]));
+                            mx3 = fmax3(mx3, u2f(sb[i + 6]), u2f(sb[i + 7]));
+                        }
+                        return fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2;
+                    };
+                    // p = exp2(s * scale*log2e - m); a row that has seen no key yet takes m = 0,
+                    // its scores being -inf
+                    auto exps = [&]() {
+                        const float me = m == -INFINITY ? 0.f : m;
+                        const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-me, -me);
+                        uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) {
+                            const int e = 2 * i;
+                            float e0, e1, e2, e3;
+                            f2unpack(ffma2(f2pack(SV(e), SV(e + 1)), sc2, nm2), e0, e1);
+                            f2unpack(ffma2(f2pack(SV(e + 2), SV(e + 3)), sc2, nm2), e2, e3);
+                            e0 = ex2_approx(e0);
+                            e1 = ex2_approx(e1);
+                            e2 = ex2_approx(e2);
+                            e3 = ex2_approx(e3);
+                            acc0 = fadd2(acc0, f2pack(e0, e1));
+                            acc1 = fadd2(acc1, f2pack(e2, e3));
+                            pk[i] = pack_bf16x2(e0, e1);
+                            pk[i + 1] = pack_bf16x2(e2, e3);
+                        }
+                        float a0, a1;
+                        f2unpack(fadd2(acc0, acc1), a0, a1);
+                        lstep = a0 + a1;
+                    };
+                    load_scores();
+                    if (steps > settled) {
+                        const float mx = row_max();
+                        if (lim < 0.f && mx > -INFINITY) {
+                            m = mx;
+                            lim = kSpanRise;
+                        }
                     }
                     exps();
-                }
-                l += lstep;
-                {
-                    uint32_t h0[32], h1[32];
+                    // A row keeps its max while no row sum passes kSpanRise: p, l and O are floating
+                    // point, so a maximum that lags by up to 2^14 costs no precision, and a first
+                    // tile with only a few keys in it (a causal diagonal) seldom has to be put
+                    // right. A row that sees its first key later yet (a piece that begins behind
+                    // its window) gets its max here too. Until then its weights, sum and O are 0.
+                    if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // not at the first step
+                        load_scores();
+                        const float mnew = row_max();
+                        float alpha = 1.f;
+                        if (mnew > m) {
+                            alpha = ex2_approx(m - mnew);
+                            m = mnew;
+                            if (lim < 0.f) lim = kSpanRise;
+                        }
+                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                            // The commit that signalled S_t for this step also covers the
+                            // previous O_t += P V, so O_t is stable here.
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + c, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        h0[i] = pk[i];
-                        h1[i] = pk[32 + i];
+                                for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
+                                tmem_st32(tO + c, o);
+                            }
+                            l *= alpha;
+                        }
+                        exps();
                     }
-                    tmem_st32(tS, h0);
-                    tmem_st32(tS + 32, h1);
-                }
+                    l += lstep;
+                    {
+                        uint32_t h0[32], h1[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            h0[i] = pk[i];
+                            h1[i] = pk[32 + i];
+                        }
+                        tmem_st32(tS, h0);
+                        tmem_st32(tS + 32, h1);
+                    }
 #undef SV
-                tmem_st_wait();
-                tc_fence_before();
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
+                }
+                if (!ok) break;
+                ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
+                if (!ok) break;
+                row_ml[t * 256 + row] = l;
+                row_ml[t * 256 + 128 + row] = m;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
+                if (lane == 0) mbar_arrive(BAR(SPL_FULL + t));
+                SEG_DONE();
             }
-            if (!ok) break;
-            ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
-            if (!ok) break;
-            row_ml[t * 256 + row] = l;
-            row_ml[t * 256 + 128 + row] = m;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(SPL_FULL + t));
-            SEG_DONE();
-        }
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -1625,7 +1634,17 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
     kern<<<grid, 512, SpanCfg<D, FEW>::kSmemAlloc, stream>>>(maps, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = cudaGetLastError();
+    if (e == cudaErrorInvalidValue || e == cudaErrorLaunchOutOfResources) {
+        // the limit was lost (for instance by a device reset): set it again once
+        configured.fetch_and(~bit, std::memory_order_acq_rel);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, FEW>::kSmemAlloc);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+        kern<<<grid, 512, SpanCfg<D, FEW>::kSmemAlloc, stream>>>(maps, p);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
     if (p.rec) {
         // set up while the attention kernel still runs; it waits for its end itself
         cudaLaunchAttribute attr{};

@@ -324,8 +324,9 @@ xs_status xs_attn_trace_layout(int B, int S, int H, int D, int P, int *ctas, int
  * model keeps its keys and values in a paged cache. The common rules above hold
  * unless a call says otherwise. None of these calls synchronises, allocates or
  * keeps anything between calls, so each can be captured into a CUDA graph and
- * replayed; calls (or replays) that may run at the same time must not share a
- * workspace or write the same memory.
+ * replayed (make one call of each kind on a device before the first capture:
+ * it loads the kernels); calls or replays that may run at the same time must not
+ * share a workspace or write the same memory.
  */
 
 /*
@@ -378,6 +379,8 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
  *            xs_attn_window_workspace_size bytes; it needs no initialisation. With
  *            it the work is split evenly over the SMs, pieces of a query tile
  *            meeting in the workspace. NULL (with 0): whole query tiles only.
+ * k and v must be finite: a key that a token does not see has no weight, but 0
+ * times an infinity or NaN next to keys that it sees is NaN.
  * left, right >= -1, sinks >= 0, S <= 2^24. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
  */
 xs_status xs_attn_window(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,

@@ -128,6 +128,38 @@ def test_paged_passed_pages_may_hold_anything(D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,rows", ((1000, 1), (65536, 1), (40000, 3)))
+def test_paged_very_many_sequences(N, rows):
+    """Thousands of short sequences, many without new tokens: the schedule's sums over the whole batch."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    H, Hk, D, page, n_pages = 2 * rows, 2, 64, 16, 300
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    kp, vp = rand(n_pages, page, Hk, D), rand(n_pages, page, Hk, D)
+    q_len = torch.randint(0, 2, (N,), generator=gen, device="cuda")
+    kv = torch.randint(1, 2 * page + 1, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    table = torch.randint(0, n_pages, (N, 2), generator=gen, device="cuda", dtype=torch.int32)
+    q_start = torch.cat((torch.zeros(1, dtype=torch.long, device="cuda"), q_len.cumsum(0))).to(torch.int32)
+    T = int(q_start[-1])
+    q, out = rand(T, H, D), guarded(T * H * D)
+    ws = guarded(xs.attn_paged_workspace_size(N, T, H, Hk, D), torch.uint8)
+    xs.attn_paged(q, kp, vp, table, q_start, kv, out, N, T, H, Hk, D, page, n_pages, 2, 0.125, workspace=ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got = values(from_dev(out)).reshape(T, H, D)
+    seqs = q_len.nonzero().view(-1)
+    k = kp[table[seqs].long()].view(T, 2 * page, Hk, D).double().repeat_interleave(rows, 2)
+    v = vp[table[seqs].long()].view(T, 2 * page, Hk, D).double().repeat_interleave(rows, 2)
+    s = torch.einsum("thd,tkhd->thk", q.double(), k) * 0.125
+    s = s.masked_fill(torch.arange(2 * page, device="cuda") >= kv[seqs].view(T, 1, 1), -np.inf)
+    w = s.softmax(-1)
+    ref, a = (torch.einsum("thk,tkhd->thd", w, x).cpu().numpy() for x in (v, v.abs()))
+    # the bound of span_testlib.attend; here scale sum |q k| is below 2^5, so the scores' share 2 delta is below 2^-12
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * a + 1e-30).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("q_len", ([1, 1], [90, 40]))
 def test_paged_sequences_share_pages(q_len):
     """Two sequences with the same first pages (a common prefix), and one page named twice in a row of the table."""
