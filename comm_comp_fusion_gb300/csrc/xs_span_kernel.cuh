@@ -205,14 +205,14 @@ __device__ __forceinline__ int span_pairs(const SpanParams &p, int q_len) {
     return q_len <= t2 ? (q_len > 0) : (q_len + t2 - 1) / t2;
 }
 
-// Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
-// is a sequence (all its heads and query rows) or, for whole sequences, which
-// are all alike, a query tile pair of one head. T: see span_schedule.
 template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
+// Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
+// is a sequence (all its heads and query rows) or, for whole sequences, which
+// are all alike, a query tile pair of one head.
 template <bool PAGED>
 __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane) {
     const int g = ch * 32 + lane;
@@ -1299,7 +1299,7 @@ __global__ void __launch_bounds__(512, 1)
                     // tile with only a few keys in it (a causal diagonal) seldom has to be put
                     // right. A row that sees its first key later yet (a piece that begins behind
                     // its window) gets its max here too. Until then its weights, sum and O are 0.
-                    if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // not at the first step
+                    if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // (at the first step m is exact)
                         load_scores();
                         const float mnew = row_max();
                         float alpha = 1.f;
