@@ -52,7 +52,7 @@
 // (chunks of 2048 over 16K keys, 32 heads: 655 us, 1.64 PFLOP/s). Short calls: about 10
 // us of set-up, first loads and first steps, whose instructions are fetched cold.
 //
-// Roles of the 512 threads (registers 48 / 176 / 176 / 112 a thread):
+// Roles of the 512 threads (registers 48 / 184 / 184 / 96 a thread):
 //   warp 0      TMA producer: Q tiles, then K and V tiles into a 128 KB ring. Pages
 //               shorter than a tile take one box each, issued by as many lanes (by
 //               one lane in turn: 431 us instead of 371 for 32 long single tokens);
@@ -85,6 +85,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t x) {
     asm volatile("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
+}
+
+// Bounded waits in few instructions, a retry in a loop: there are some forty of them, and
+// what the kernel spends between two items is to a good part the fetch of code (with
+// each wait's retries unrolled, 300 KB of it instead of 190: two-sided window S = 4096 78 us
+// instead of 69, S = 16384 545 instead of 514, four short single tokens 14.7 instead of 13.4).
+__device__ __forceinline__ bool span_bwait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t site) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    int i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (++i & 63) continue;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1u;
+            atomicOr(&g_xs_error, 0x80000000u | (1u << site));
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool span_warp_bwait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t site) {
+    const bool ok = span_bwait(bar, parity, abort_flag, site);
+    return __all_sync(0xffffffffu, ok);
 }
 
 constexpr int kSegs = 6;  // segments in the ring
@@ -648,7 +673,7 @@ __global__ void __launch_bounds__(512, 1)
                     pieces = SpanPieces{span_cta_of(*sched, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, g.tok0,
                                         g.ntok, g.q0, 0};
                 }
-                if (!warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg)) break;
+                if (!span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg)) break;
                 if (lane == 0) {
                     volatile SpanSeg &d = SEG;
                     d.n = g.n;
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(512, 1)
             bool ok = true;
             const int box = PAGED ? min(p.page, 128) : 128;  // rows of a box
             while (ok) {
-                ok = SEG_WAIT(warp_bwait);
+                ok = SEG_WAIT(span_warp_bwait);
                 volatile SpanSeg &g = SEG;
                 const int n = g.n, j0 = g.j0, head = g.head;
                 if (!ok || n == 0) break;
@@ -702,7 +727,7 @@ __global__ void __launch_bounds__(512, 1)
                 };
                 auto load_tile = [&](const CUtensorMap *m, int x, int page) {
                     const uint32_t slot = kv_it % C::kSlots, ph = (kv_it / C::kSlots) & 1u;
-                    ok = warp_bwait(BAR(SPKV_EMPTY + slot), ph ^ 1u, abort_flag, kSiteLoadKV);
+                    ok = span_warp_bwait(BAR(SPKV_EMPTY + slot), ph ^ 1u, abort_flag, kSiteLoadKV);
                     if (!ok) return;
                     ++kv_it;
                     if (lane == 0) mbar_arrive_expect_tx(BAR(SPKV_FULL + slot), C::kTile);
@@ -725,7 +750,7 @@ __global__ void __launch_bounds__(512, 1)
                 for (int i = 0; i < (dual ? 1 : 2) && ok; ++i) {
                     const int t = FEW ? (int)(seg_it & 1u) : i;  // few rows: items take the two tiles in turn
                     const uint32_t use = FEW ? seg_it >> 1 : t ? q_it1++ : q_it0++;
-                    ok = warp_bwait(BAR(SPQ_EMPTY + t), (use & 1u) ^ 1u, abort_flag, kSiteLoadQ);
+                    ok = span_warp_bwait(BAR(SPQ_EMPTY + t), (use & 1u) ^ 1u, abort_flag, kSiteLoadQ);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(BAR(SPQ_FULL + t), (uint32_t)C::kNDB * 128u * (uint32_t)(p.tile_tok * p.G));
@@ -763,14 +788,14 @@ __global__ void __launch_bounds__(512, 1)
             // ------------------------------------ V rows behind the last key: zeros
             uint32_t kv_it = 0, fph = 0;
             const int box = min(p.page, 128);
-            while (SEG_WAIT(warp_bwait)) {
+            while (SEG_WAIT(span_warp_bwait)) {
                 const int n = SEG.n, rows = SEG.fix;
                 if (n == 0) break;
                 // the segment's first V tile follows its first one or two K tiles
                 const uint32_t slot = (kv_it + (SEG.dual && n > 1 ? 2u : 1u)) % C::kSlots;
                 kv_it += 2u * (uint32_t)n;
                 if (rows >= 0) {
-                    if (!warp_bwait(BAR(SPFIX_ASK), fph, abort_flag, kSiteFix)) break;  // the tile is in
+                    if (!span_warp_bwait(BAR(SPFIX_ASK), fph, abort_flag, kSiteFix)) break;  // the tile is in
                     fph ^= 1u;
                     for (int r = rows * 8 + lane; r < ((rows + box - 1) / box * box) * 8; r += 32)
 #pragma unroll
@@ -821,12 +846,12 @@ __global__ void __launch_bounds__(512, 1)
             bool ok = true;
             auto wait_kv = [&](uint32_t &slot) {
                 slot = kv_it % C::kSlots;
-                ok = ok && bwait(BAR(SPKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
+                ok = ok && span_bwait(BAR(SPKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
                 ++kv_it;
             };
             auto wait_p = [&](int t, bool first) {  // P_t is in (and, at a tile's first step, O_t is free)
-                ok = bwait(BAR(SPP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
-                if (ok && first) ok = bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                ok = span_bwait(BAR(SPP_FULL + t), t ? pph1 : pph0, abort_flag, kSiteMmaP);
+                if (ok && first) ok = span_bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
                 if (t)
                     pph1 ^= 1u;
                 else
@@ -837,23 +862,23 @@ __global__ void __launch_bounds__(512, 1)
                 wait_kv(slot);
                 if (ok && fix) {
                     mbar_arrive(BAR(SPFIX_ASK));
-                    ok = bwait(BAR(SPFIX_DONE), fph, abort_flag, kSiteFix);
+                    ok = span_bwait(BAR(SPFIX_DONE), fph, abort_flag, kSiteFix);
                     fph ^= 1u;
                 }
             };
             auto no_steps = [&](int t) {  // a tile or chain without a step in this segment
-                ok = bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
+                ok = span_bwait(BAR(SPO_FREE + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteMmaOFree);
                 if (ok) tc_commit(BAR(SPO_FINAL + t));
             };
             while (ok) {
-                ok = SEG_WAIT(bwait);
+                ok = SEG_WAIT(span_bwait);
                 volatile SpanSeg &g = SEG;
                 const int n = g.n;
                 if (!ok || n == 0) break;
                 const bool fix = PAGED && g.fix >= 0;
                 uint32_t ks, vs;
                 const int qb = FEW ? (int)(seg_it & 1u) : 0;  // the tile that holds Q (dual)
-                ok = bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
+                ok = span_bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
                 if (FEW || g.dual) {
                     // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
                     wait_kv(ks);
@@ -888,7 +913,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     if (ok && n == 1) no_steps(1);
                 } else {
-                    if (ok) ok = bwait(BAR(SPQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
+                    if (ok) ok = span_bwait(BAR(SPQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
                     // steps (of the segment) of tile 0: from f0 on; of tile 1: below l1 and from m1 on
                     const int f0 = max(g.s0 - g.j0, 0), l1 = min(g.e1 - g.j0, n), m1 = max(g.nw - g.j0, 0);
                     auto on1 = [&](int x) { return x < l1 || x >= m1; };
@@ -911,17 +936,17 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
                             for (; x < mid1; ++x) {
                                 vs = kv_it % C::kSlots;
-                                ok = bwait(BAR(SPKV_FULL + vs), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV) &&
-                                     bwait(BAR(SPP_FULL + 0), pph0, abort_flag, kSiteMmaP);
+                                ok = span_bwait(BAR(SPKV_FULL + vs), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV) &&
+                                     span_bwait(BAR(SPP_FULL + 0), pph0, abort_flag, kSiteMmaP);
                                 if (!ok) break;
                                 tc_fence_after();
                                 issue_PV(0, vs, true);
                                 ks = (kv_it + 1u) % C::kSlots;
-                                ok = bwait(BAR(SPKV_FULL + ks), ((kv_it + 1u) / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
+                                ok = span_bwait(BAR(SPKV_FULL + ks), ((kv_it + 1u) / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
                                 if (!ok) break;
                                 kv_it += 2u;
                                 issue_S(0, 0, ks);
-                                ok = bwait(BAR(SPP_FULL + 1), pph1, abort_flag, kSiteMmaP);
+                                ok = span_bwait(BAR(SPP_FULL + 1), pph1, abort_flag, kSiteMmaP);
                                 if (!ok) break;
                                 pph0 ^= 1u;
                                 pph1 ^= 1u;
@@ -977,7 +1002,7 @@ __global__ void __launch_bounds__(512, 1)
         __syncwarp();
     } else if (wg == 1 || wg == 2) {
         // ------------------------------------------------------------- softmax
-        setmaxnreg_inc<176>();
+        setmaxnreg_inc<184>();
         const int t = wg - 1;
         if constexpr (FEW > 0) {
             // One thread per key of the tile, its scores of all rows in registers. The rows'
@@ -1002,7 +1027,7 @@ __global__ void __launch_bounds__(512, 1)
             auto sync = [&]() {  // the chain's four warps meet (bounded, unlike a named barrier)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(SPCHAIN + t));
-                ok = ok && warp_bwait(BAR(SPCHAIN + t), cph, abort_flag, kSiteSoftS);
+                ok = ok && span_warp_bwait(BAR(SPCHAIN + t), cph, abort_flag, kSiteSoftS);
                 cph ^= 1u;
             };
             // v of all rows: the warps' results of `op` over their lanes to red, then a barrier.
@@ -1022,7 +1047,7 @@ __global__ void __launch_bounds__(512, 1)
                 sync();
             };
             while (ok) {
-                ok = SEG_WAIT(warp_bwait);
+                ok = SEG_WAIT(span_warp_bwait);
                 volatile SpanSeg &g = SEG;
                 if (!ok || g.n == 0) break;
                 const int rows = g.ntok * p.G;
@@ -1046,7 +1071,7 @@ __global__ void __launch_bounds__(512, 1)
                         c += g.ns - c_end;
                         c_end = INT_MIN;
                     }
-                    ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
+                    ok = span_warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                     if (!ok) break;
                     sph ^= 1u;
                     tc_fence_after();
@@ -1145,7 +1170,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (!ok) break;
                 over_keys(l, [](float a, float b) { return a + b; });
                 if (!ok) break;
-                ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
+                ok = span_warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
                 if (!ok) break;
                 if (kl < FEW) {
                     row_ml[t * 256 + kl] = red[kl] + red[FEW + kl] + red[2 * FEW + kl] + red[3 * FEW + kl];
@@ -1165,7 +1190,7 @@ __global__ void __launch_bounds__(512, 1)
             uint32_t sph = 0;
             bool ok = true;
             while (ok) {
-                ok = SEG_WAIT(warp_bwait);
+                ok = SEG_WAIT(span_warp_bwait);
                 volatile SpanSeg &g = SEG;
                 if (!ok || g.n == 0) break;
                 // lim: the row sum that calls for the row max again: none for a row that does
@@ -1210,7 +1235,7 @@ __global__ void __launch_bounds__(512, 1)
                         c += g.ns - c_end;
                         c_end = INT_MIN;
                     }
-                    ok = warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
+                    ok = span_warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                     if (!ok) break;
                     sph ^= 1u;
                     if (idle) {  // P keeps what S left there: only rows that do not exist read it
@@ -1341,7 +1366,7 @@ __global__ void __launch_bounds__(512, 1)
                     if (lane == 0) mbar_arrive(BAR(SPP_FULL + t));
                 }
                 if (!ok) break;
-                ok = warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
+                ok = span_warp_bwait(BAR(SPL_EMPTY + t), (seg_it & 1u) ^ 1u, abort_flag, kSiteSoftL);
                 if (!ok) break;
                 row_ml[t * 256 + row] = l;
                 row_ml[t * 256 + 128 + row] = m;
@@ -1352,14 +1377,14 @@ __global__ void __launch_bounds__(512, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        setmaxnreg_dec<112>();
+        setmaxnreg_dec<96>();
         const int wq = warp & 3;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const int row = wq * 32 + lane;
         const uint32_t stage = sStage + wq * C::kStageWarp;
         bool ok = true;
         while (ok) {
-            ok = SEG_WAIT(warp_bwait);
+            ok = SEG_WAIT(span_warp_bwait);
             volatile SpanSeg &g = SEG;
             if (!ok || g.n == 0) break;
             const bool piece = g.piece;
@@ -1396,8 +1421,8 @@ __global__ void __launch_bounds__(512, 1)
                     flush_block<true, 4>(p.out, stage, lane, dst, c0 / 64);
             };
             auto take_ml = [&](int t, float &l, float &m) {
-                ok = warp_bwait(BAR(SPO_FINAL + t), seg_it & 1u, abort_flag, kSiteEpiO) &&
-                     warp_bwait(BAR(SPL_FULL + t), seg_it & 1u, abort_flag, kSiteEpiL);
+                ok = span_warp_bwait(BAR(SPO_FINAL + t), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     span_warp_bwait(BAR(SPL_FULL + t), seg_it & 1u, abort_flag, kSiteEpiL);
                 if (!ok) return;
                 l = row_ml[t * 256 + row];
                 m = row_ml[t * 256 + 128 + row];
@@ -1411,10 +1436,10 @@ __global__ void __launch_bounds__(512, 1)
             };
             if constexpr (FEW > 0) {
                 // one thread per column of the output, all rows
-                ok = warp_bwait(BAR(SPO_FINAL + 0), seg_it & 1u, abort_flag, kSiteEpiO) &&
-                     warp_bwait(BAR(SPO_FINAL + 1), seg_it & 1u, abort_flag, kSiteEpiO) &&
-                     warp_bwait(BAR(SPL_FULL + 0), seg_it & 1u, abort_flag, kSiteEpiL) &&
-                     warp_bwait(BAR(SPL_FULL + 1), seg_it & 1u, abort_flag, kSiteEpiL);
+                ok = span_warp_bwait(BAR(SPO_FINAL + 0), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     span_warp_bwait(BAR(SPO_FINAL + 1), seg_it & 1u, abort_flag, kSiteEpiO) &&
+                     span_warp_bwait(BAR(SPL_FULL + 0), seg_it & 1u, abort_flag, kSiteEpiL) &&
+                     span_warp_bwait(BAR(SPL_FULL + 1), seg_it & 1u, abort_flag, kSiteEpiL);
                 if (!ok) break;
                 tc_fence_after();
                 const int rows = g.ntok * p.G, head = g.head, tok0 = g.tok0, q_row = g.q0;
