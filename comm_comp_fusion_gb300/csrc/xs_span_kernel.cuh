@@ -88,9 +88,10 @@ __device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t x) {
 }
 
 // Bounded waits in few instructions, a retry in a loop: there are some forty of them, and
-// what the kernel spends between two items is to a good part the fetch of code (with
-// each wait's retries unrolled, 300 KB of it instead of 190: two-sided window S = 4096 78 us
-// instead of 69, S = 16384 545 instead of 514, four short single tokens 14.7 instead of 13.4).
+// what the kernel spends between two items is to a good part the fetch of code. With
+// each wait's retries unrolled it held 300 KB of it instead of 175: two-sided window S =
+// 4096 78 us instead of 67, S = 16384 545 instead of 497, four short single tokens 14.7
+// instead of 12.8.
 __device__ __forceinline__ bool span_bwait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t site) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
@@ -100,8 +101,7 @@ __device__ __forceinline__ bool span_bwait(uint32_t bar, uint32_t parity, volati
         if (++i & 63) continue;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1u;
-            atomicOr(&g_xs_error, 0x80000000u | (1u << site));
+            *abort_flag = 0x80000000u | (1u << site);  // the kernel's end passes it on
             return false;
         }
     }
@@ -247,12 +247,14 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
     const int pairs = span_pairs(p, q_len);
     long long u = pairs == 1 ? (long long)span_item(p, q_len, keys, 0).n * p.heads : 0ll;
     uint32_t todo = __ballot_sync(0xffffffffu, pairs > 1);  // these the whole warp sums up, one after the other
+#pragma unroll 1
     while (todo) {
         const int src = __ffs((int)todo) - 1;
         todo &= todo - 1;
         const int ql = __shfl_sync(0xffffffffu, q_len, src), kl = __shfl_sync(0xffffffffu, keys, src);
         const int np = span_pairs(p, ql);
         long long s = 0;
+#pragma unroll 1
         for (int i = lane; i < np; i += 32) s += span_item(p, ql, kl, i).n;
         s = warp_sum(s);
         if (lane == src) u = s * p.heads;
@@ -283,6 +285,8 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
     return l;
 }
 
+// (The loops of the schedule stay rolled: they run once, and their code is fetched cold.)
+
 // Where this CTA's part of the shared steps begins, by one warp. The shared steps
 // are the call's from step `before` on. `sum`: the steps of one head (whole
 // sequences). `mine`: the steps of this lane's group in the only chunk, when there
@@ -305,6 +309,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     }
     int l = -1, ch = 0;
     if (chunks > 1) {
+#pragma unroll 1
         for (; l < 0 && ch < chunks; ch += 32)
             l = span_locate<T>(ch + lane < chunks ? (T)sums[ch + lane] : (T)0, u, base, at, lane);
         ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
@@ -329,6 +334,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
         return;
     }
     T per_head = 0;
+#pragma unroll 1
     for (int i = lane; i < np; i += 32) per_head += (T)span_item(p, q_len, keys, i).n;
     per_head = warp_sum(per_head);
     s.head = (int)(u / per_head);
@@ -336,6 +342,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     base = 0;
     l = -1;
     int i = 0;
+#pragma unroll 1
     for (; l < 0 && i < np; i += 32)
         l = span_locate<T>(i + lane < np ? (T)span_item(p, q_len, keys, i + lane).n : (T)0, u, base, at, lane);
     s.pair = i - 32 + l;
@@ -359,6 +366,7 @@ __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long l
     if (rest && 5 * rest < 2 * grid) --rounds;
     const long long first = (long long)rounds * grid, head = first / p.n_pairs;  // the first shared item
     const int pairs = (int)(first - head * p.n_pairs);
+#pragma unroll 1
     for (int i = lane; i < pairs; i += 32) steps += span_item(p, p.S, p.S, i).n;
     steps = warp_sum(steps) + head * sum;
     return rounds;
@@ -368,6 +376,7 @@ __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long l
 // followed by a barrier.
 template <bool PAGED> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int ch = warp; ch < chunks; ch += (int)(blockDim.x >> 5)) {
         const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
         if (lane == 0) sums[ch] = s;
@@ -379,6 +388,7 @@ template <bool PAGED>
 __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chunks, const long long *sums, int lane) {
     long long mine = 0, sum = 0;
     if (chunks > 1) {
+#pragma unroll 1
         for (int ch = lane; ch < chunks; ch += 32) sum += sums[ch];
     } else {
         sum = mine = span_group_steps<PAGED>(p, 0, lane);
@@ -1547,6 +1557,7 @@ __global__ void __launch_bounds__(512, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && misc[1]) atomicOr(&g_xs_error, misc[1]);  // a wait ran out
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
