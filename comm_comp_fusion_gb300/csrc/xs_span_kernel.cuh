@@ -52,7 +52,7 @@
 // (chunks of 2048 over 16K keys, 32 heads: 655 us, 1.64 PFLOP/s). Short calls: about 10
 // us of set-up, first loads and first steps, whose instructions are fetched cold.
 //
-// Roles of the 512 threads (registers 48 / 184 / 184 / 96 a thread):
+// Roles of the 512 threads:
 //   warp 0      TMA producer: Q tiles, then K and V tiles into a 128 KB ring. Pages
 //               shorter than a tile take one box each, issued by as many lanes (by
 //               one lane in turn: 431 us instead of 371 for 32 long single tokens);
@@ -123,7 +123,14 @@ enum : int {
 enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 
 // FEW: query rows of a tile in the few-rows form; 0: tiles of 128 rows.
-template <int D, int FEW> struct SpanCfg {
+template <int D, bool PAGED, int FEW> struct SpanCfg {
+    // Registers a thread of warps 0-3, of the softmax warps and of the epilogue's. One split for
+    // both calls with 128-row tiles costs 2-3% of one of them (56 / 176 / 104: two-sided window
+    // S = 4096 65.1 us, mixed paged batch 83.0; 48 / 184 / 96: 66.3 and 80.6); few rows have few scores.
+    static constexpr int kRegsOther = FEW ? 80 : PAGED ? 48 : 56;
+    static constexpr int kRegsSoftmax = FEW ? 160 : PAGED ? 184 : 176;
+    static constexpr int kRegsEpilogue = FEW ? 112 : PAGED ? 96 : 104;
+    static_assert(kRegsOther + 2 * kRegsSoftmax + kRegsEpilogue == 4 * 128, "the registers the block is launched with");
     static constexpr int kNDB = Cfg<D>::kNDB;
     static constexpr uint32_t kBlk = Cfg<D>::kBlk, kTile = Cfg<D>::kTile;
     // K/V ring of 128 KB, in 16 KB (D = 64) or 32 KB slots. More in flight, where few
@@ -585,7 +592,7 @@ struct SpanPieces {
 template <int D, bool PAGED, int FEW>
 __global__ void __launch_bounds__(512, 1)
     span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
-    using C = SpanCfg<D, FEW>;
+    using C = SpanCfg<D, PAGED, FEW>;
     using R = Rec<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(512, 1)
     } while (0)
 
     if (wg == 0) {
-        setmaxnreg_dec<48>();
+        setmaxnreg_dec<C::kRegsOther>();
         if (warp == 2) {
             // ---------------------------------------------------------- schedule
             SpanPieces pieces{};
@@ -757,6 +764,7 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 };
                 int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
+                load_tile(&tm.k, 0, pg0);  // before Q, whose place is free only after the last S of the item before
                 for (int i = 0; i < (dual ? 1 : 2) && ok; ++i) {
                     const int t = FEW ? (int)(seg_it & 1u) : i;  // few rows: items take the two tiles in turn
                     const uint32_t use = FEW ? seg_it >> 1 : t ? q_it1++ : q_it0++;
@@ -776,7 +784,6 @@ __global__ void __launch_bounds__(512, 1)
                     }
                 }
                 if (!ok) break;
-                load_tile(&tm.k, 0, pg0);
                 if (ok && dual && n > 1) load_tile(&tm.k, 1, pg1);
                 for (int x = 0; ok && x < n; ++x) {
                     const int pg3 = page_of(x + 3);
@@ -1012,7 +1019,7 @@ __global__ void __launch_bounds__(512, 1)
         __syncwarp();
     } else if (wg == 1 || wg == 2) {
         // ------------------------------------------------------------- softmax
-        setmaxnreg_inc<184>();
+        setmaxnreg_inc<C::kRegsSoftmax>();
         const int t = wg - 1;
         if constexpr (FEW > 0) {
             // One thread per key of the tile, its scores of all rows in registers. The rows'
@@ -1257,25 +1264,26 @@ __global__ void __launch_bounds__(512, 1)
 #define SV(i) u2f((i) < 64 ? sa[(i) & 63] : sb[(i) & 63])
                     uint32_t pk[64];
                     float lstep = 0.f;
-                    auto load_scores = [&]() {
-                        tmem_ld64x2(tS, sa, sb);
-                        if (masked) {
-                            const uint32_t ninf = f2u(-INFINITY);
-                            // places of this row's token and of the last key it may see
-                            const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
-                            const int row_hi = min(pos + p.right, g.keys - 1);
+                    if (masked) {
+                        // Masked scores become -inf in tensor memory, 32 columns at a time: a few
+                        // instructions in a loop, where masking them in the registers below is 500
+                        // that have to be fetched anew for the one or two tiles of an item with an
+                        // edge in them.
+                        // Places of this row's token and of the last key it may see:
+                        const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
+                        const int row_hi = min(pos + p.right, g.keys - 1);
+#pragma unroll 1
+                        for (int h = 0; h < 128; h += 32) {
+                            const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, h);
+                            if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+                            uint32_t s[32];
+                            tmem_ld32(tS + h, s);
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, 32 * h);
-                                if (__all_sync(0xffffffffu, bits == ~0u)) continue;  // a mask's edge crosses one or two of the four
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    uint32_t &s = h < 2 ? sa[(h & 1) * 32 + i] : sb[(h & 1) * 32 + i];
-                                    s = (bits >> i) & 1u ? s : ninf;
-                                }
-                            }
+                            for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : f2u(-INFINITY);
+                            tmem_st32(tS + h, s);
                         }
-                    };
+                        tmem_st_wait();
+                    }
                     auto row_max = [&]() {
                         float mx0 = fmaxf(u2f(sa[0]), u2f(sa[1])), mx1 = fmaxf(u2f(sa[2]), u2f(sa[3]));
                         float mx2 = fmaxf(u2f(sa[4]), u2f(sa[5])), mx3 = fmaxf(u2f(sa[6]), u2f(sa[7]));
@@ -1320,7 +1328,7 @@ __global__ void __launch_bounds__(512, 1)
                         f2unpack(fadd2(acc0, acc1), a0, a1);
                         lstep = a0 + a1;
                     };
-                    load_scores();
+                    tmem_ld64x2(tS, sa, sb);
                     if (steps > settled) {
                         const float mx = row_max();
                         if (lim < 0.f && mx > -INFINITY) {
@@ -1335,7 +1343,7 @@ __global__ void __launch_bounds__(512, 1)
                     // right. A row that sees its first key later yet (a piece that begins behind
                     // its window) gets its max here too. Until then its weights, sum and O are 0.
                     if (steps < settled + 2 && __any_sync(0xffffffffu, lstep > lim)) {  // (at the first step m is exact)
-                        load_scores();
+                        tmem_ld64x2(tS, sa, sb);
                         const float mnew = row_max();
                         float alpha = 1.f;
                         if (mnew > m) {
@@ -1387,7 +1395,7 @@ __global__ void __launch_bounds__(512, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        setmaxnreg_dec<96>();
+        setmaxnreg_dec<C::kRegsEpilogue>();
         const int wq = warp & 3;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const int row = wq * 32 + lane;
@@ -1665,19 +1673,19 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, FEW>::kSmemAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, PAGED, FEW>::kSmemAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    kern<<<grid, 512, SpanCfg<D, FEW>::kSmemAlloc, stream>>>(maps, p);
+    kern<<<grid, 512, SpanCfg<D, PAGED, FEW>::kSmemAlloc, stream>>>(maps, p);
     e = cudaGetLastError();
     if (e == cudaErrorInvalidValue || e == cudaErrorLaunchOutOfResources) {
         // the limit was lost (for instance by a device reset): set it again once
         configured.fetch_and(~bit, std::memory_order_acq_rel);
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, FEW>::kSmemAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, PAGED, FEW>::kSmemAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
-        kern<<<grid, 512, SpanCfg<D, FEW>::kSmemAlloc, stream>>>(maps, p);
+        kern<<<grid, 512, SpanCfg<D, PAGED, FEW>::kSmemAlloc, stream>>>(maps, p);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
