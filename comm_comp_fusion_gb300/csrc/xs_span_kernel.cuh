@@ -30,8 +30,8 @@
 //     are keys (or columns of V) and the query rows are its N. A softmax thread
 //     then holds one key's scores of all rows: 16 exponentials a step where the
 //     other form spends 128 on rows that mostly do not exist (four sequences of 300
-//     to 1200 keys: 14.7 us against 16.7; 64 of 4000 to 8000 keys, D = 64: 156
-//     against 166).
+//     to 1200 keys: 12.6 us against 15.9; 8 of 4000 to 9000 keys, D = 96: 58
+//     against 66; 32 of 4000 to 32768, D = 128: 345 against 352).
 //
 // Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
 // ordered by sequence, head and query rows, and each CTA takes an equal,
@@ -46,11 +46,14 @@
 // unnormalised O, row maxima and sums to the workspace, and span_merge_kernel
 // adds them up in piece order (no atomics: the result is the same every time).
 //
-// Bounds. Single new tokens: HBM (32 sequences of 16000 keys, 8 key heads, D = 128: 320
-// us, 6.55 TB/s; rows of 128 bytes, D = 64, reach 5.05 TB/s). Long chunks and windows:
-// the chain S - softmax - P V of a step, about 2950 cycles for two tiles at D = 128
-// (chunks of 2048 over 16K keys, 32 heads: 655 us, 1.64 PFLOP/s). Short calls: about 10
-// us of set-up, first loads and first steps, whose instructions are fetched cold.
+// Bounds. Single new tokens: HBM (32 sequences of 16000 keys, 8 key heads, D = 128, pages
+// of 32 tokens and more: 305 us, 6.9 TB/s; D = 64 and 96 reach 5.4; pages of 16 tokens
+// 5.9, their boxes' issue being the limit). Long chunks and windows: the chain S -
+// softmax - P V of a step, about 2850 cycles for two tiles at D = 128 (chunks of 2048
+// over 16K keys, 32 heads: 634 us, 1.69 PFLOP/s). Items of few steps (a two-sided window of
+// 512: 10): what lies between two items, about 6000 cycles of first loads, masked steps
+// and cold code, and steps that few rows need whole. Short calls: about 8 us of
+// set-up, first loads and first steps, whose instructions are fetched cold.
 //
 // Roles of the 512 threads:
 //   warp 0      TMA producer: Q tiles, then K and V tiles into a 128 KB ring. Pages
@@ -181,7 +184,7 @@ static_assert(sizeof(SpanSched) <= 64, "its place in shared memory");
 constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory
 
 constexpr float kSpanRise = 16384.0f;  // see the softmax
-constexpr int kMidSteps = 8;           // see the issuer
+constexpr int kMidSteps = 4;           // see the issuer
 
 // An item's K/V tiles by step y: hi, hi - 1, ... (nw of them, the window's), then
 // ns - 1, ..., 0 (those of the sinks that lie before it).
@@ -945,8 +948,8 @@ __global__ void __launch_bounds__(512, 1)
                     tc_commit(BAR(SPKV_EMPTY + ks));
                     // Steps in the middle, which both tiles take, as they do the next, have a loop
                     // without decisions: the issuer's own instructions are on the chain of every
-                    // step (chunks of 2048 over 16K keys: 757 -> 665 us). A few such steps do not
-                    // repay the fetch of its code (10-step items: 77 us without it, 83 with).
+                    // step (S = 16384, window of 4096: 497 us, 558 without; items of 10 steps, 5 of
+                    // them here: 63 us and 65).
                     const int mid0 = f0 + 1, mid1 = min(l1, n) - 2;  // short of the last S of either tile
                     for (int x = 0; x < n; ++x) {
                         if (x == mid0 && mid1 - x >= kMidSteps) {
