@@ -14,6 +14,15 @@ device pointers. Shapes follow the C ABI:
 
 ``ulysses_attn`` takes q, k, v and out all sequence-partitioned (both
 All-to-Alls fused); ``a2a_permute_inverse`` maps sequence- to head-partitioned.
+
+The operators around the attention: ``rope`` (rotary positions, ``RopeAxes``; either
+partition, or from the sequence to the head partition), ``attn_window`` and
+``attn_window_a2a`` (sliding window with sinks), and for a paged cache
+``cache_append`` and ``attn_paged``:
+
+    k_pages, v_pages : pools [n_pages][page][Hk][D] bf16
+    page_table       : [N][max_pages] int32; q_start [N + 1], kv_len [N] int32
+    q, out / k, v    : packed new tokens [T][H][D] / [T][Hk][D] bf16
 """
 from __future__ import annotations
 
