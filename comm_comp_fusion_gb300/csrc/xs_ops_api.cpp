@@ -77,6 +77,28 @@ int check_workspace(const void *ws, size_t bytes, const Buffer *others, int n) {
 }
 float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634073599246810019); }
 
+// K/V tiles that the two query tiles of pair i of a whole sequence walk.
+int pair_steps(const SpanParams &p, int i) {
+    const int tok = 256 * i, last = std::min(tok + 255, p.S - 1);
+    const int hi = std::min(p.S - 1, last + p.right), lo = std::max(0, tok - p.left) / 128;
+    return hi / 128 - lo + 1 + std::min((std::min(p.sinks, hi + 1) + 127) / 128, lo);
+}
+
+// Whether a CTA for each pair of query tiles, none cut, makes the longest CTA's part at
+// most three steps longer than an even split of all steps (in parts of four and more):
+// pieces, their schedule and merge cost as much.
+bool whole_pairs(const SpanParams &p, int sms) {
+    if ((long long)p.heads * p.n_pairs > sms) return false;
+    long long sum = 0;
+    int most = 0;
+    for (int i = 0; i < p.n_pairs; ++i) {
+        const int n = pair_steps(p, i);
+        sum += n;
+        most = std::max(most, n);
+    }
+    return most <= std::max(sum * p.heads / sms, 4ll) + 3;
+}
+
 int window_call(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P, float scale,
                 int left, int right, int sinks, void *ws, size_t ws_bytes, void *stream, bool a2a) {
     if (!q || !k || !v || !out) return api_fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
@@ -118,7 +140,7 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     p.item_tok = 256;
     p.heads = B * H;
     p.n_pairs = (S + 255) / 256;
-    if (ws) span_workspace_parts(ws, D, sms, &p);
+    if (ws && !whole_pairs(p, sms)) span_workspace_parts(ws, D, sms, &p);
     SpanMaps maps;
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.Hl, (uint64_t)S, (uint64_t)P * B};
     const uint64_t strides[3] = {(uint64_t)D * 2, (uint64_t)p.Hl * D * 2, (uint64_t)S * p.Hl * D * 2};

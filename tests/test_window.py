@@ -111,6 +111,28 @@ def test_window_falling_keys_after_far_first_tile():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", ((2, 4, 3, 96, 1, 726, 10, 4), (1, 68, 16, 128, 4, 35, 0, 200), (3, 257, 30, 64, 1, -1, 0, 0),
+                                  (1, 1000, 30, 128, 5, 300, 300, 4), (2, 900, 19, 96, 1, 200, 40, 0), (1, 1, 152, 64, 1, 0, 0, 0)))
+def test_window_small_calls_take_whole_items(case):
+    """No more items than SMs, none much longer than the others' share: no item is cut, so the bits are those without a
+    workspace, which are near 64 bits. (Three batches of 30 heads and two items are more than the SMs: some are cut.)"""
+    import torch
+    B, S, H, D, P, left, right, sinks = case
+    rng = np.random.default_rng(S + 3 * D)
+    (qb, q), (kb, k), (vb, v) = (bf16(rng, (B, S, H, D)) for _ in range(3))
+    dev = [to_dev(tokens_to_head(x, P)) for x in (qb, kb, vb)]
+    whole = run((*case, 1.0), *dev, D ** -0.5, False, None)
+    got = run((*case, 1.0), *dev, D ** -0.5, True, 0xFF)
+    if B * H * -(-S // 256) <= torch.cuda.get_device_properties(0).multi_processor_count:
+        np.testing.assert_array_equal(got, whole)
+    seen = seen_mask(np.arange(S), S, left, right, sinks)
+    for h in range(0, H, max(1, H // 4)):
+        ref, bound = attend(q[0, :, h], k[0, :, h], v[0, :, h], seen, D ** -0.5)
+        for bits in (got, whole):
+            check(bits[0, :, h], ref, bound, f"{case} h={h}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("span", ((3000, 0, 70), (-1, 0, 0), (1500, 2500, 0)))
 def test_window_long_sampled(span):
     """A long ragged sequence: items of many K/V tiles, one row of every query tile against 64 bits."""
