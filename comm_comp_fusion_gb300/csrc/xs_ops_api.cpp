@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -84,9 +85,13 @@ int pair_steps(const SpanParams &p, int i) {
     return hi / 128 - lo + 1 + std::min((std::min(p.sinks, hi + 1) + 127) / 128, lo);
 }
 
-// Whether a CTA for each pair of query tiles, none cut, makes the longest CTA's part at
-// most three steps longer than an even split of all steps (in parts of four and more):
-// pieces, their schedule and merge cost as much.
+// Whether to take a CTA for each pair of query tiles, none cut: if that makes the longest
+// part at most three steps longer than an even split of all steps (in parts of four and
+// more), since pieces, their schedule and merge cost as much, or seven where the split would
+// keep half the SMs and more busy with pieces, whose traffic then counts. 30 heads of S =
+// 1000, causal, D = 128 (8 steps against 4): 19.2 us whole, 22.7 split; 20 of S = 1500 (12
+// against 5) 24.3, 28.3; 4 of S = 1000, D = 64 (8 against 4, 32 parts) 17.2, 15.2; 8 of S =
+// 1500 (12 against 4) 24.0, 21.6.
 bool whole_pairs(const SpanParams &p, int sms) {
     if ((long long)p.heads * p.n_pairs > sms) return false;
     long long sum = 0;
@@ -96,7 +101,8 @@ bool whole_pairs(const SpanParams &p, int sms) {
         sum += n;
         most = std::max(most, n);
     }
-    return most <= std::max(sum * p.heads / sms, 4ll) + 3;
+    sum *= p.heads;
+    return most <= std::max(sum / sms, 4ll) + (sum >= 2ll * sms ? 7 : 3);
 }
 
 int window_call(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P, float scale,
