@@ -22,6 +22,8 @@
 // time (eight 16-byte loads in flight). Measured on one GB300: B = 2, S = 16384, H = 40,
 // D = 128 199 us, 6.75 TB/s (with one unit of a random row per step instead of a
 // thread's own token, 251 us); S = 4096, H = 24 to the head partition 21 us, 4.8 TB/s.
+#include <algorithm>
+
 #include "xs_internal.h"
 #include "xs_ptx.cuh"
 
@@ -105,14 +107,21 @@ __global__ void __launch_bounds__(D == 96 ? 192 : 256) rope_kernel(const __grid_
     const int b = (int)(blockIdx.x / (unsigned)tiles), s0 = ((int)blockIdx.x - b * tiles) * p.tile;
     const int nt = min(p.tile, p.S - s0);
     const int *pos = p.pos + ((int64_t)b * p.pos_batch + s0) * p.n_axes;
-    for (int i = threadIdx.x; i < nt * (D / 2); i += kThreads) {
+    auto sines = [&](int i) {
         const int t = i / (D / 2), j = i - t * (D / 2);
-        if (j >= p.n_pairs) continue;
+        if (j >= p.n_pairs) return;
         const uint64_t phase = (uint64_t)(int64_t)pos[t * p.n_axes + p.axis[j]] * p.frac[j];
         const int turns = (int)(uint32_t)((phase + 0x80000000ull) >> 32);  // nearest multiple of 2^-32 turns
         float sn, cn;
         sincospif((float)turns * 0x1p-31f, &sn, &cn);
         cs_tab[i] = make_float2(cn, p.inverse ? -sn : sn);
+    };
+    const int n = nt * (D / 2);
+    if (p.tile > 8) {  // several a thread: their places are fetched together
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kThreads) sines(i);
+    } else {
+        for (int i = threadIdx.x; i < n; i += kThreads) sines(i);
     }
     __syncthreads();
     const int unit = (int)threadIdx.x % U, rr = (int)threadIdx.x / U;
@@ -173,10 +182,15 @@ __global__ void __launch_bounds__(D == 96 ? 192 : 256) rope_kernel(const __grid_
 }
 
 cudaError_t launch_rope(RopeParams &p, bool halves, int num_sms, cudaStream_t stream) {
-    // tokens per block: eight share the table's set-up when that still leaves four
-    // blocks for every SM, fewer for short calls (S = 4096: 21 us with 4, 27 with 2)
-    p.tile = 8;
-    while (p.tile > 1 && (long long)p.B * ((p.S + p.tile - 1) / p.tile) < 4ll * num_sms) p.tile >>= 1;
+    // Tokens per block: eight share the table's set-up, or more while the threads of a
+    // token and unit would have fewer than four heads each; fewer for short calls, so that
+    // four blocks are left for every SM (S = 4096: 21 us with 4, 27 with 2; 2 + 1 heads of
+    // 111,900 tokens, D = 96: 39 us with 32 tokens a block, 98 with 8).
+    const int rows = (p.D == 96 ? 192 : 256) / (p.D / 16), heads = std::max(p.H, p.Hk);
+    p.tile = rows;
+    while (p.tile > 1 && ((p.tile > 8 && rows / p.tile * kRopeUnroll < heads) ||
+                          (long long)p.B * ((p.S + p.tile - 1) / p.tile) < 4ll * num_sms))
+        p.tile >>= 1;
     const unsigned grid = (unsigned)((p.S + p.tile - 1) / p.tile) * (unsigned)p.B;
     const size_t smem = (size_t)p.tile * (p.D / 2) * sizeof(float2);
 #define XS_ROPE_CASE(d)                                                        \

@@ -406,7 +406,9 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     sum = warp_sum(sum);
     const long long total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
-    s.ctas = (int)max(1ll, min((long long)gridDim.x, total >> p.min_steps_log2));
+    // parts of 2 steps or more (whole sequences: 4), or of an item of one key head each
+    const long long least = PAGED ? min(total, (long long)p.N * p.heads) : 0ll;
+    s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> p.min_steps_log2, least)));
     s.rem = s.q = 0;
     s.r = 0;
     s.rounds = s.seq = s.head = s.pair = s.j = 0;

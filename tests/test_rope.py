@@ -45,6 +45,11 @@ CASES = [  # B, S, H, Hk, D, P, axes, halves, inverse, seq_in, seq_out, farthest
     (1, 1304, 8, 8, 128, 8, (32, 48, 48), True, False, True, False, 2 ** 31 - 1),
     (5, 700, 3, 0, 128, 1, (126,), False, False, False, False, 2 ** 31 - 1),
     (2, 64, 40, 8, 128, 4, (16,), True, False, False, False, 5000),
+    # few heads, many tokens: more tokens share a block
+    (1, 39001, 1, 0, 64, 1, (64,), False, False, False, False, 100000),
+    (1, 19999, 2, 1, 96, 1, (32, 16), True, False, False, True, 1000),
+    (2, 10028, 4, 4, 128, 2, (44, 42, 42), False, True, True, False, 90),
+    (1, 9731, 1, 1, 256, 1, (256,), True, False, True, True, 2 ** 31 - 1),
 ]
 
 
