@@ -20,7 +20,10 @@ void span_workspace_parts(void *ws, int D, int num_sms, SpanParams *p) {
 
 cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int num_sms, cudaStream_t stream) {
     SpanParams q = p;
-    q.min_steps_log2 = p.table ? 1 : 2;
+    // The least part of a CTA: one step with few rows (4 sequences of 4 tokens over 1165 to 2941
+    // keys, one key head: 15.6 us, 17.1 with two), two for other chunks (5 of 267 to 669
+    // tokens over 996 keys: 20.9 us, 24.9 with four), four of whole sequences.
+    q.min_steps_log2 = p.few ? 0 : p.table ? 1 : 2;
     // a merge block adds up 32 rows of an item, or with few rows 256 groups of 4 columns
     const int rows = std::min(p.T, p.item_tok) * p.G, tile = p.tile_tok * p.G;
     q.merge_y = p.few ? (rows * (D / 4) + 255) / 256 : rows > tile ? 8 : (rows + 31) / 32;

@@ -86,6 +86,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// The same value to 32 columns.
+__device__ __forceinline__ void tmem_fill32(uint32_t taddr, uint32_t v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(taddr),
+        "r"(v)
+        : "memory");
+}
 __device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t x) {
     asm volatile("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(a), "r"(x) : "memory");
 }
@@ -406,7 +414,7 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     sum = warp_sum(sum);
     const long long total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
-    // parts of 2 steps or more (whole sequences: 4), or of an item of one key head each
+    // parts of a few steps or more, or a CTA for each key head of the sequences
     const long long least = PAGED ? min(total, (long long)p.N * p.heads) : 0ll;
     s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> p.min_steps_log2, least)));
     s.rem = s.q = 0;
@@ -1281,11 +1289,15 @@ __global__ void __launch_bounds__(512, 1)
                         for (int h = 0; h < 128; h += 32) {
                             const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, h);
                             if (__all_sync(0xffffffffu, bits == ~0u)) continue;
-                            uint32_t s[32];
-                            tmem_ld32(tS + h, s);
+                            if (__any_sync(0xffffffffu, bits)) {
+                                uint32_t s[32];
+                                tmem_ld32(tS + h, s);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : f2u(-INFINITY);
-                            tmem_st32(tS + h, s);
+                                for (int i = 0; i < 32; ++i) s[i] = (bits >> i) & 1u ? s[i] : f2u(-INFINITY);
+                                tmem_st32(tS + h, s);
+                            } else {
+                                tmem_fill32(tS + h, f2u(-INFINITY));
+                            }
                         }
                         tmem_st_wait();
                     }
