@@ -1112,13 +1112,13 @@ __global__ void __launch_bounds__(512, 1)
                     else
                         tmem_ld32(tS, s);
                     if (masked) {
-                        const int key = c0 + kl, keys = g.keys, pos0 = g.pos0;
+                        // the key is seen by tokens key - right .. key + left (a sink: by all from there
+                        // on), so by rows r0 <= r < r1 of the item
+                        const int key = c0 + kl, at = key - g.pos0;
+                        const int r0 = min(max(at - p.right, 0), FEW) * p.G;
+                        const int r1 = key >= g.keys ? 0 : key < p.sinks ? FEW : min(max(at + p.left + 1, 0), FEW) * p.G;
 #pragma unroll
-                        for (int r = 0; r < FEW; ++r) {
-                            const int pos = pos0 + span_row_tok<PAGED>(p, r);
-                            const bool sees = key <= min(pos + p.right, keys - 1) && (key >= pos - p.left || key < p.sinks);
-                            s[r] = sees ? s[r] : f2u(-INFINITY);
-                        }
+                        for (int r = 0; r < FEW; ++r) s[r] = r >= r0 && r < r1 ? s[r] : f2u(-INFINITY);
                     }
                     bool by_max = fresh;
 #pragma unroll 1
