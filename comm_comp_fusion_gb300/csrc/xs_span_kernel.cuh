@@ -911,34 +911,24 @@ __global__ void __launch_bounds__(512, 1)
                 ok = span_bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
                 if (FEW || g.dual) {
                     // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
-                    wait_kv(ks);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_S(0, qb, ks);
-                    tc_commit(BAR(SPKV_EMPTY + ks));
-                    if (n > 1) {
-                        wait_kv(ks);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_S(1, qb, ks);
-                        tc_commit(BAR(SPKV_EMPTY + ks));
-                    }
-                    if (n <= 2) tc_commit(BAR(SPQ_EMPTY + qb));
-                    for (int x = 0; x < n; ++x) {
-                        const int t = x & 1;
-                        wait_v(vs, fix && x == 0);
-                        if (ok) wait_p(t, x < 2);
-                        if (!ok) break;
-                        issue_PV(t, vs, x >= 2);
-                        tc_commit(BAR(SPKV_EMPTY + vs));
-                        if (x + 2 >= n) tc_commit(BAR(SPO_FINAL + t));
-                        if (x + 2 < n) {
+#pragma unroll 1
+                    for (int y = 0; y < n + 2; ++y) {  // S of step y, P V of step y - 2
+                        const int t = y & 1;
+                        if (y >= 2) {
+                            wait_v(vs, fix && y == 2);
+                            if (ok) wait_p(t, y < 4);
+                            if (!ok) break;
+                            issue_PV(t, vs, y >= 4);
+                            tc_commit(BAR(SPKV_EMPTY + vs));
+                            if (y >= n) tc_commit(BAR(SPO_FINAL + t));
+                        }
+                        if (y < n) {
                             wait_kv(ks);
                             if (!ok) break;
                             tc_fence_after();
                             issue_S(t, qb, ks);
                             tc_commit(BAR(SPKV_EMPTY + ks));
-                            if (x + 3 == n) tc_commit(BAR(SPQ_EMPTY + qb));
+                            if (y + 1 == n) tc_commit(BAR(SPQ_EMPTY + qb));
                         }
                     }
                     if (ok && n == 1) no_steps(1);
