@@ -381,6 +381,8 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
  *            meeting in the workspace. NULL (with 0): whole query tiles only.
  * k and v must be finite: a key that a token does not see has no weight, but 0
  * times an infinity or NaN next to keys that it sees is NaN.
+ * A row of q that is not finite gives an output row of no particular values, and
+ * changes no other.
  * left, right >= -1, sinks >= 0, S <= 2^24. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
  */
 xs_status xs_attn_window(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,

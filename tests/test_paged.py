@@ -173,6 +173,33 @@ def test_paged_sequences_share_pages(q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_len,kv_len,H,Hk,D", (([1] * 4, [700, 90, 1500, 64], 8, 2, 128), ([6, 3, 2], [400, 300, 5], 6, 2, 64),
+                                                 ([300, 1], [900, 700], 4, 2, 96), ([140], [3000], 2, 1, 128)))
+def test_paged_rows_that_are_not_finite_stay_alone(q_len, kv_len, H, Hk, D):
+    """A row of q with NaN or an infinity spoils its own output alone, whole and split, in every form."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    b = Batch(q_len, kv_len, H, Hk, D, 32, seed=D)
+    bad = {(0, 0): NAN, (b.T // 2, H - 1): 0x7F80, (b.T - 1, 1): 0xFF80}
+    bits = b.qb.copy()
+    for (t, h), x in bad.items():
+        bits[t, h, ::7] = x
+    b.dq = to_dev(bits)
+    b.call()
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got, t = from_dev(b.out).reshape(b.T, H, D), 0
+    for n, (ql, kl) in enumerate(zip(q_len, kv_len)):
+        for h in range(H):
+            ok = [i for i in range(ql) if (t + i, h) not in bad]
+            seen = seen_mask(np.arange(kl - ql, kl)[ok], kl, -1, 0, 0)
+            if ok:
+                ref, bound = attend(b.q[t:t + ql, h][ok], b.k[n][:, h // (H // Hk)], b.v[n][:, h // (H // Hk)], seen, D ** -0.5)
+                check(got[t:t + ql, h][ok], ref, bound, f"sequence {n} head {h}")
+        t += ql
+
+
+@pytest.mark.gpu
 def test_paged_starts_behind_the_first_row():
     """Packed rows before q_start[0] and behind q_start[N] belong to no sequence."""
     b = Batch([3, 2], [200, 90], 4, 2, 64, 16, spare=6, seed=14)

@@ -73,6 +73,24 @@ def test_window_matches_64_bits(case):
 
 
 @pytest.mark.gpu
+def test_window_rows_that_are_not_finite_stay_alone():
+    """A row of q with NaN or an infinity spoils its own output alone."""
+    B, S, H, D, P = 1, 1500, 3, 128, 1
+    case = (B, S, H, D, P, 400, 30, 4, 1.0)
+    rng = np.random.default_rng(8)
+    (qb, q), (kb, k), (vb, v) = (bf16(rng, (B, S, H, D)) for _ in range(3))
+    bad = {(0, 0): 0x7FC1, (700, 1): 0x7F80, (701, 2): 0xFF80, (1499, 2): 0x7FC1}
+    for (t, h), x in bad.items():
+        qb[0, t, h, 3::5] = x
+    for ws in (True, False):
+        got = run(case, *[to_dev(tokens_to_head(x, P)) for x in (qb, kb, vb)], D ** -0.5, ws)
+        for h in range(H):
+            ok = np.array([t for t in range(S) if (t, h) not in bad])
+            ref, bound = attend(q[0, ok, h], k[0, :, h], v[0, :, h], seen_mask(ok, S, 400, 30, 4), D ** -0.5)
+            check(got[0, ok, h], ref, bound, f"h={h} ws={ws}")
+
+
+@pytest.mark.gpu
 def test_window_rising_keys():
     """Scores that grow along the sequence: the running maximum moves in every tile, in the window and past the sinks."""
     B, S, H, D, P = 1, 1100, 2, 128, 1
