@@ -256,6 +256,9 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     long long before = 0;
     if (!PAGED && s.ctas == (int)gridDim.x) s.rounds = span_rounds(p, s.ctas, sum, lane, before);
     s.shared = total - before;
+    // Every CTA that shares them has a step: a part without one between two pieces of an item would
+    // have written no record for the merge.
+    if (s.shared > 0 && s.shared < s.ctas) s.ctas = (int)s.shared;
     if ((int)blockIdx.x < s.ctas && s.shared > 0) {
         if (total < (1ll << 31))
             span_find<uint32_t, PAGED>(p, s, (uint32_t)before, sum, mine, chunks, sums, lane);

@@ -234,6 +234,35 @@ def test_window_on_two_streams_at_once():
         assert np.array_equal(from_dev(o), from_dev(want))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", ((21, 256, 32, 64, 1, -1, 0, 0), (23, 200, 16, 96, 1, -1, 0, 0), (13, 256, 40, 64, 2, -1, -1, 0),
+                                  (1, 1280, 73, 64, 1, 0, 0, 0)))
+def test_window_rest_of_fewer_steps_than_sms(case):
+    """Whole rounds, then items of two or three steps whose steps are fewer than the CTAs (152 SMs): every head, with
+    a workspace that holds NaN or finite leftovers of another call, which no result may depend on."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    B, S, H, D, P, left, right, sinks = case
+    rng = np.random.default_rng(S + B)
+    (qb, q), (kb, k), (vb, v) = (bf16(rng, (B, S, H, D)) for _ in range(3))
+    dev = [to_dev(tokens_to_head(x, P)) for x in (qb, kb, vb)]
+    ws = guarded(xs.attn_window_workspace_size(B, S, H, D, P), torch.uint8)
+    outs = []
+    for fill in (0xFF, 0x3C):
+        ws.fill_(fill)
+        out = guarded(B * S * H * D)
+        xs.attn_window(*dev, out, B, S, H, D, P, D ** -0.5, left, right, sinks, ws)
+        torch.cuda.synchronize()
+        assert xs.device_status() == xs.XS_OK, xs.last_error()
+        outs.append(head_to_tokens(from_dev(out).reshape(P, B, S, H // P, D)))
+    seen = seen_mask(np.arange(S), S, left, right, sinks)
+    for b in range(B):
+        for h in range(H):
+            ref, bound = attend(q[b, :, h], k[b, :, h], v[b, :, h], seen, D ** -0.5)
+            check(outs[0][b, :, h], ref, bound, f"{case} b={b} h={h}")
+    assert np.array_equal(outs[0], outs[1])
+
+
 Q, K, V, O, W = 0x10000000, 0x20000000, 0x30000000, 0x40000000, 0x50000000
 
 
