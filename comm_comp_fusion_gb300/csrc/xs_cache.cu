@@ -2,7 +2,8 @@
 // paged cache.
 //
 // Token i of sequence n has place kv_len[n] - q_len[n] + i; its row goes to row
-// place % page of page page_table[n][place / page]. A pure copy, bound by HBM
+// place % page of page page_table[n][place / page], kv_len cut to the table's
+// max_pages * page keys first. A pure copy, bound by HBM
 // for prompts and by latency for single tokens: one warp copies one token's K
 // and V rows (Hk * D elements each) and looks its sequence up while the first
 // loads are on their way. Measured on one GB300: 19,181 prompt tokens of 8 heads, D = 128
@@ -31,9 +32,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) cache_append_kernel(const A
     const CacheRow at = find_sequence(p.q_start, p.N, p.T, t, lane);
     if (at.seq < 0) return;  // a row of no sequence
     const int64_t cap = (int64_t)p.max_pages * p.page;
-    const int64_t len = p.kv_len[at.seq];
+    const int64_t len = min(max((int64_t)p.kv_len[at.seq], (int64_t)0), cap);  // cut like the attention's (span_lengths)
     const int64_t place = len - at.q_len + at.i;
-    if (place < 0 || place >= cap) return;
+    if (place < 0) return;
     const int pg = (int)(place / p.page);
     const int id = p.table[(int64_t)at.seq * p.max_pages + pg];
     if (id < 0 || id >= p.n_pages) return;

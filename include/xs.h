@@ -406,11 +406,14 @@ xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_
  *            q_start[N] up to T belong to no sequence.
  *   kv_len : device [N] int32, keys of each sequence, its new tokens included:
  *            new token i stands at place kv_len[n] - (q_start[n + 1] - q_start[n]) + i.
+ *            A length of more than max_pages * page keys counts as that many, a
+ *            negative one as none, here and in the two calls below.
  * All three are read by the kernels, so a captured call follows them when they
  * change between replays. They are not checked on the host. What they name
  * outside the pool, the table or the packed rows is never accessed: keys in
  * pages outside 0 .. n_pages - 1 are undefined in attention and are not written by
- * the append, and lengths are cut to max_pages * page keys.
+ * the append. With a kv_len past the table's end the new tokens stand at the
+ * table's last places, are written there and attend from there.
  * page: a power of two from 16 to 1024; max_pages * page <= 2^29; N <= 65536;
  * T <= 2^29; D = 64, 96 or 128.
  *

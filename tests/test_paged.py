@@ -390,6 +390,40 @@ def test_append_and_attention_ignore_bad_metadata():
         assert not kp.any() and not vp.any()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_len,G", (([3, 2, 2], 2), ([40, 2, 60], 2)))
+def test_lengths_past_the_table_count_as_its_end(q_len, G):
+    """A kv_len of more keys than the table holds is cut to them, by the append and the attention alike: the new tokens
+    stand at the table's last places, are written there and seen there. A negative one counts as none."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    Hk, D, page = 2, 64, 16
+    for over in (1, 5, page, 2 ** 31 - 1 - 96):
+        b = Batch(q_len, [96, 90, 0], G * Hk, Hk, D, page, spare=2, seed=over % 1000)
+        b.max_pages = 6   # 96 keys
+        b.table = b.table[:, :6].contiguous()
+        b.kv_len = torch.tensor([96 + over, 90, -over], dtype=torch.int32, device="cuda")
+        (kb, k), (vb, v) = (bf16(np.random.default_rng(1), (b.T, Hk, D)) for _ in range(2))
+        old, table = [from_dev(x).reshape(b.n_pages, page, Hk, D) for x in (b.kp, b.vp)], b.table.cpu().numpy()
+        kp, vp = guarded(b.kp.numel()), guarded(b.vp.numel())
+        kp.copy_(b.kp.view(-1))
+        vp.copy_(b.vp.view(-1))
+        xs.cache_append(to_dev(kb), to_dev(vb), kp, vp, b.table, b.q_start, b.kv_len, b.N, b.T, Hk, D, page, b.n_pages, 6)
+        b.kp, b.vp = kp, vp
+        b.call()
+        torch.cuda.synchronize()
+        for got, want, new, own in ((kp, old[0], kb, b.k), (vp, old[1], vb, b.v)):
+            want, t = want.copy(), 0
+            for n in range(2):
+                for i in range(q_len[n]):
+                    place = b.kv[n] - q_len[n] + i
+                    want[table[n, place // page], place % page] = new[t + i]
+                    own[n][place] = values(new[t + i])
+                t += q_len[n]
+            assert (from_dev(got).reshape(want.shape) == want).all(), over
+        b.verify(what=f"over by {over}")
+
+
 # ------------------------------------------------------------------ in a row
 
 @pytest.mark.gpu
