@@ -27,6 +27,7 @@ partition, or from the sequence to the head partition), ``attn_window`` and
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from ._build import LIB as _LIB_PATH, build  # noqa: F401  (build is re-exported)
@@ -325,15 +326,30 @@ def attn_causal(q, k, v, out, B, S, H, D, P, scale, stream=None, check=True):
     return _check(st) if check else st
 
 
-def _dense(x, name, numel, itemsize):
-    """A tensor argument of the calls below must be contiguous, of `itemsize`-byte elements and at least `numel` of them
-    (raw addresses are taken as they are)."""
+@functools.cache
+def _accepted(kind):
+    import torch
+    # bf16 values may also come as their 16 bits
+    return {"bfloat16": (torch.bfloat16, torch.int16, torch.uint16), "int32": (torch.int32,)}[kind]
+
+
+def _dense(x, name, numel, kind):
+    """A tensor argument of the calls below must be contiguous, of its documented type and of at least `numel` elements (raw
+    addresses are taken as they are)."""
     if x is None or isinstance(x, int):
         return x
-    if not x.is_contiguous() or x.element_size() != itemsize or x.numel() < numel:
-        raise ValueError(f"{name}: {numel} contiguous elements of {itemsize} bytes are needed, got "
+    if not x.is_contiguous() or x.dtype not in _accepted(kind) or x.numel() < numel:
+        raise ValueError(f"{name}: {numel} contiguous {kind} elements are needed, got "
                          f"{tuple(x.shape)} {x.dtype}{'' if x.is_contiguous() else ' (not contiguous)'}")
     return x.data_ptr()
+
+
+def _bf16(x, name, numel):
+    return _dense(x, name, numel, "bfloat16")
+
+
+def _int32(x, name, numel):
+    return _dense(x, name, numel, "int32")
 
 
 class RopeAxes:
@@ -363,15 +379,15 @@ def rope(q, k, q_out, k_out, pos, B, S, H, Hk, D, P, axes, seq_in=False, seq_out
     flags = ((XS_ROPE_HALVES if axes.halves else 0) | (XS_ROPE_INVERSE if inverse else 0)
              | (XS_ROPE_IN_SEQ if seq_in else 0) | (XS_ROPE_OUT_SEQ if seq_out else 0))
     nq, nk = B * S * H * D, B * S * Hk * D
-    st = lib.xs_rope(_dense(q, "q", nq, 2), _dense(k, "k", nk, 2), _dense(q_out, "q_out", nq, 2),
-                     _dense(k_out, "k_out", nk, 2), _dense(pos, "pos", pos_batches * S * n, 4), pos_batches, B, S, H, Hk,
+    st = lib.xs_rope(_bf16(q, "q", nq), _bf16(k, "k", nk), _bf16(q_out, "q_out", nq),
+                     _bf16(k_out, "k_out", nk), _int32(pos, "pos", pos_batches * S * n), pos_batches, B, S, H, Hk,
                      D, P, n, axes._dims, axes._freqs, flags, _stream(stream, q, q_out))
     return _check(st) if check else st
 
 
 def _window(fn, q, k, v, out, B, S, H, D, P, scale, left, right, sinks, workspace, workspace_bytes, stream, check):
     n = B * S * H * D
-    st = fn(_dense(q, "q", n, 2), _dense(k, "k", n, 2), _dense(v, "v", n, 2), _dense(out, "out", n, 2), B, S, H, D, P,
+    st = fn(_bf16(q, "q", n), _bf16(k, "k", n), _bf16(v, "v", n), _bf16(out, "out", n), B, S, H, D, P,
             float(scale), left, right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes),
             _stream(stream, q, out))
     return _check(st) if check else st
@@ -403,9 +419,9 @@ def cache_append(k, v, k_pages, v_pages, page_table, q_start, kv_len, N, T, Hk, 
                  stream=None, check=True):
     """Writes the new tokens' keys and values into their pages (``xs_cache_append``)."""
     rows, pool = T * Hk * D, n_pages * page * Hk * D
-    st = lib.xs_cache_append(_dense(k, "k", rows, 2), _dense(v, "v", rows, 2), _dense(k_pages, "k_pages", pool, 2),
-                             _dense(v_pages, "v_pages", pool, 2), _dense(page_table, "page_table", N * max_pages, 4),
-                             _dense(q_start, "q_start", N + 1, 4), _dense(kv_len, "kv_len", N, 4), N, T, Hk, D, page,
+    st = lib.xs_cache_append(_bf16(k, "k", rows), _bf16(v, "v", rows), _bf16(k_pages, "k_pages", pool),
+                             _bf16(v_pages, "v_pages", pool), _int32(page_table, "page_table", N * max_pages),
+                             _int32(q_start, "q_start", N + 1), _int32(kv_len, "kv_len", N), N, T, Hk, D, page,
                              n_pages, max_pages, _stream(stream, k, k_pages))
     return _check(st) if check else st
 
@@ -414,10 +430,10 @@ def attn_paged(q, k_pages, v_pages, page_table, q_start, kv_len, out, N, T, H, H
                left=-1, right=0, sinks=0, workspace=None, workspace_bytes=None, stream=None, check=True):
     """Attention of the packed new tokens over a paged cache (``xs_attn_paged``); the workspace is required."""
     rows, pool = T * H * D, n_pages * page * Hk * D
-    st = lib.xs_attn_paged(_dense(q, "q", rows, 2), _dense(k_pages, "k_pages", pool, 2),
-                           _dense(v_pages, "v_pages", pool, 2), _dense(page_table, "page_table", N * max_pages, 4),
-                           _dense(q_start, "q_start", N + 1, 4), _dense(kv_len, "kv_len", N, 4),
-                           _dense(out, "out", rows, 2), N, T, H, Hk, D, page, n_pages, max_pages, float(scale), left,
+    st = lib.xs_attn_paged(_bf16(q, "q", rows), _bf16(k_pages, "k_pages", pool),
+                           _bf16(v_pages, "v_pages", pool), _int32(page_table, "page_table", N * max_pages),
+                           _int32(q_start, "q_start", N + 1), _int32(kv_len, "kv_len", N),
+                           _bf16(out, "out", rows), N, T, H, Hk, D, page, n_pages, max_pages, float(scale), left,
                            right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
     return _check(st) if check else st
 

@@ -543,3 +543,32 @@ def test_paged_small_workspace_and_host_memory_are_refused():
     assert b.call(check=False) == xs.XS_ERR_UNSUPPORTED
     torch.cuda.synchronize()
     assert (from_dev(b.out) == 0xFFFF).all()
+
+
+def test_types_are_checked():
+    """float16 values are not taken as bf16, nor floats as places, numbers of pages or lengths; bf16 bits are."""
+    import __graft_entry__
+    __graft_entry__.build()
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    x, i = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int32)
+    ax = xs.RopeAxes.powers((64,))
+
+    def calls(x, o, i):
+        return [lambda: xs.rope(x, x, o, o, i, 1, 4, 2, 2, 64, 1, ax, check=False),
+                lambda: xs.attn_window(x, x, x, o, 1, 4, 2, 64, 1, 0.1, check=False),
+                lambda: xs.attn_window_a2a(x, x, x, o, 1, 4, 2, 64, 1, 0.1, check=False),
+                lambda: xs.cache_append(x, x, o, o, i, i, i, 1, 4, 2, 64, 2, 1, 1, check=False),
+                lambda: xs.attn_paged(x, x, x, i, i, i, o, 1, 4, 2, 2, 64, 2, 1, 1, 0.1, check=False)]
+
+    for bad in (calls(x.half(), x, i), calls(x, x.half(), i)):
+        for call in bad:
+            with pytest.raises(ValueError, match="bfloat16"):
+                call()
+    for k in (0, 3, 4):
+        for wrong in (i.float(), i.view(torch.float32)):
+            with pytest.raises(ValueError, match="int32"):
+                calls(x, x, wrong)[k]()
+    for bits in (torch.int16, torch.uint16):
+        for call in calls(x.view(bits), x.view(bits), i):
+            assert call() != xs.XS_OK  # these are host tensors, or one buffer twice: refused behind the types
