@@ -105,15 +105,20 @@ bool whole_pairs(const SpanParams &p, int sms) {
     return most <= std::max(sum / sms, 4ll) + (sum >= 2ll * sms ? 7 : 3);
 }
 
+// Shape rules of the windowed calls; the size of one tensor in bytes.
+int check_window(int B, int S, int H, int D, int P, size_t *bytes) {
+    if (const int st = api_shape(B, S, H, D, P, bytes)) return st;
+    if (D == 256) return api_fail(XS_ERR_UNSUPPORTED, "windowed attention takes D = 64, 96 or 128 (got D=256)");
+    if (S > (1 << 24)) return api_fail(XS_ERR_SHAPE, "S=%d exceeds 2^24", S);
+    return 0;
+}
+
 int window_call(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P, float scale,
                 int left, int right, int sinks, void *ws, size_t ws_bytes, void *stream, bool a2a) {
     if (!q || !k || !v || !out) return api_fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
     size_t bytes = 0;
-    int st = api_shape(B, S, H, D, P, &bytes);
-    if (st) return st;
-    if (D == 256) return api_fail(XS_ERR_UNSUPPORTED, "windowed attention takes D = 64, 96 or 128 (got D=256)");
-    if (S > (1 << 24)) return api_fail(XS_ERR_SHAPE, "S=%d exceeds 2^24", S);
-    if ((st = check_scale(scale))) return st;
+    int st = check_window(B, S, H, D, P, &bytes);
+    if (st || (st = check_scale(scale))) return st;
     SpanParams p{};
     if ((st = span_limits(left, right, sinks, &p))) return st;
     if (misaligned16(q) || misaligned16(k) || misaligned16(v) || misaligned16(out))
@@ -177,6 +182,13 @@ int check_cache(int N, int T, int Hk, int D, int page, int n_pages, int max_page
     if (N > (1 << 16)) return api_fail(XS_ERR_SHAPE, "N=%d exceeds 65536 sequences", N);
     *pool = (size_t)rows * Hk * D * 2;
     *table = (size_t)N * max_pages * sizeof(int);
+    return 0;
+}
+// The query heads of the attention over it.
+int check_heads(int T, int H, int Hk) {
+    if (H < 1 || H % Hk) return api_fail(XS_ERR_SHAPE, "H=%d is not a positive multiple of Hk=%d", H, Hk);
+    if (H / Hk > 128) return api_fail(XS_ERR_UNSUPPORTED, "H/Hk=%d query heads a key head exceed 128", H / Hk);
+    if ((long long)T * H >= (1ll << 31)) return api_fail(XS_ERR_SHAPE, "T * H exceeds 2^31-1 rows");
     return 0;
 }
 
@@ -285,9 +297,8 @@ xs_status xs_attn_window_a2a(const void *q, const void *k, const void *v, void *
 xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_t *bytes) {
     if (!bytes) return (xs_status)api_fail(XS_ERR_NULL, "bytes must be non-NULL");
     size_t tb = 0;
-    int st = api_shape(B, S, H, D, P, &tb);
+    int st = check_window(B, S, H, D, P, &tb);
     if (st) return (xs_status)st;
-    if (D == 256) return (xs_status)api_fail(XS_ERR_UNSUPPORTED, "windowed attention takes D = 64, 96 or 128 (got D=256)");
     *bytes = 0;
     if (tb == 0) return XS_OK;
     int dev, sms;
@@ -345,10 +356,7 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
     size_t pool, table;
     int st = check_cache(N, T, Hk, D, page, n_pages, max_pages, &pool, &table);
     if (st) return (xs_status)st;
-    if (H < 1 || H % Hk) return (xs_status)api_fail(XS_ERR_SHAPE, "H=%d is not a positive multiple of Hk=%d", H, Hk);
-    if (H / Hk > 128) return (xs_status)api_fail(XS_ERR_UNSUPPORTED, "H/Hk=%d query heads a key head exceed 128", H / Hk);
-    if ((long long)T * H >= (1ll << 31)) return (xs_status)api_fail(XS_ERR_SHAPE, "T * H exceeds 2^31-1 rows");
-    if ((st = check_scale(scale))) return (xs_status)st;
+    if ((st = check_heads(T, H, Hk)) || (st = check_scale(scale))) return (xs_status)st;
     SpanParams p{};
     if ((st = span_limits(left, right, sinks, &p))) return (xs_status)st;
     if (misaligned16(q) || misaligned16(k_pages) || misaligned16(v_pages) || misaligned16(out))
@@ -416,7 +424,7 @@ xs_status xs_attn_paged_workspace_size(int N, int T, int H, int Hk, int D, size_
     size_t pool, table;
     int st = check_cache(N, T, Hk, D, 16, 1, 1, &pool, &table);
     if (st) return (xs_status)st;
-    if (H < 1 || H % Hk) return (xs_status)api_fail(XS_ERR_SHAPE, "H=%d is not a positive multiple of Hk=%d", H, Hk);
+    if ((st = check_heads(T, H, Hk))) return (xs_status)st;
     *bytes = 0;
     if (N == 0 || T == 0) return XS_OK;
     int dev, sms;

@@ -572,3 +572,21 @@ def test_types_are_checked():
     for bits in (torch.int16, torch.uint16):
         for call in calls(x.view(bits), x.view(bits), i):
             assert call() != xs.XS_OK  # these are host tensors, or one buffer twice: refused behind the types
+
+
+def test_workspace_sizes_refuse_what_the_calls_refuse():
+    import __graft_entry__
+    __graft_entry__.build()
+    import ctypes
+    import comm_comp_fusion_gb300 as xs
+    n = ctypes.c_size_t(7)
+    for T, H, Hk in ((4, 258, 2), (4, 7, 2), (4, 0, 2), (1 << 27, 16, 16)):
+        want = xs.attn_paged(Q, KP, VP, TAB, QS, KL, O, 2, T, H, Hk, 64, 16, 50, 20, 0.1, workspace=W, workspace_bytes=1 << 27,
+                             check=False)
+        assert want in (xs.XS_ERR_SHAPE, xs.XS_ERR_UNSUPPORTED)
+        assert xs.lib.xs_attn_paged_workspace_size(2, T, H, Hk, 64, ctypes.byref(n)) == want
+    for B, S, H, D, P in ((1, (1 << 24) + 128, 1, 64, 1), (1, 128, 1, 256, 1), (1, 129, 2, 64, 2)):
+        want = xs.attn_window(Q, KP, VP, O, B, S, H, D, P, 0.1, check=False)
+        assert want in (xs.XS_ERR_SHAPE, xs.XS_ERR_UNSUPPORTED)
+        assert xs.lib.xs_attn_window_workspace_size(B, S, H, D, P, ctypes.byref(n)) == want
+    assert n.value == 7
