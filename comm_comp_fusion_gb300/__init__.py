@@ -352,6 +352,15 @@ def _int32(x, name, numel):
     return _dense(x, name, numel, "int32")
 
 
+def _workspace(x):
+    """A workspace tensor: numel() elements have to lie behind its address, as they do not in an expanded one."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor is needed, got {tuple(x.shape)} with strides {x.stride()}")
+    return x.data_ptr()
+
+
 class RopeAxes:
     """How a head's elements turn with the token's place (``axis_dims``, ``freqs`` of ``xs_rope``): elements per axis
     and one frequency in radians per pair; ``halves`` pairs elements half an axis apart instead of neighbours."""
@@ -388,7 +397,7 @@ def rope(q, k, q_out, k_out, pos, B, S, H, Hk, D, P, axes, seq_in=False, seq_out
 def _window(fn, q, k, v, out, B, S, H, D, P, scale, left, right, sinks, workspace, workspace_bytes, stream, check):
     n = B * S * H * D
     st = fn(_bf16(q, "q", n), _bf16(k, "k", n), _bf16(v, "v", n), _bf16(out, "out", n), B, S, H, D, P,
-            float(scale), left, right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+            float(scale), left, right, sinks, _workspace(workspace), _nbytes(workspace, workspace_bytes),
             _stream(stream, q, out))
     return _check(st) if check else st
 
@@ -434,7 +443,7 @@ def attn_paged(q, k_pages, v_pages, page_table, q_start, kv_len, out, N, T, H, H
                            _bf16(v_pages, "v_pages", pool), _int32(page_table, "page_table", N * max_pages),
                            _int32(q_start, "q_start", N + 1), _int32(kv_len, "kv_len", N),
                            _bf16(out, "out", rows), N, T, H, Hk, D, page, n_pages, max_pages, float(scale), left,
-                           right, sinks, _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
+                           right, sinks, _workspace(workspace), _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
     return _check(st) if check else st
 
 

@@ -590,3 +590,15 @@ def test_workspace_sizes_refuse_what_the_calls_refuse():
         assert want in (xs.XS_ERR_SHAPE, xs.XS_ERR_UNSUPPORTED)
         assert xs.lib.xs_attn_window_workspace_size(B, S, H, D, P, ctypes.byref(n)) == want
     assert n.value == 7
+
+
+def test_workspace_tensors_are_contiguous():
+    import __graft_entry__
+    __graft_entry__.build()
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 27), torch.zeros(64, 2, dtype=torch.float32).t()):
+        with pytest.raises(ValueError, match="workspace"):
+            xs.attn_window(Q, KP, VP, O, 1, 128, 1, 64, 1, 0.1, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            xs.attn_paged(Q, KP, VP, TAB, QS, KL, O, 2, 4, 4, 2, 64, 16, 50, 20, 0.1, workspace=ws)
