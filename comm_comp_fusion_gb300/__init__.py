@@ -27,7 +27,6 @@ partition, or from the sequence to the head partition), ``attn_window`` and
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 from ._build import LIB as _LIB_PATH, build  # noqa: F401  (build is re-exported)
@@ -326,30 +325,37 @@ def attn_causal(q, k, v, out, B, S, H, D, P, scale, stream=None, check=True):
     return _check(st) if check else st
 
 
-@functools.cache
-def _accepted(kind):
-    import torch
-    # bf16 values may also come as their 16 bits
-    return {"bfloat16": (torch.bfloat16, torch.int16, torch.uint16), "int32": (torch.int32,)}[kind]
+_BF16, _INT32 = [], []   # the types that count as such, once torch has been imported (_dense)
 
 
-def _dense(x, name, numel, kind):
-    """A tensor argument of the calls below must be contiguous, of its documented type and of at least `numel` elements (raw
-    addresses are taken as they are)."""
-    if x is None or isinstance(x, int):
-        return x
-    if not x.is_contiguous() or x.dtype not in _accepted(kind) or x.numel() < numel:
+def _dense(x, name, numel, kind, types):
+    """The address of a tensor argument of the calls below: it must be contiguous, of its documented type and of at least
+    `numel` elements."""
+    if not types:
+        import torch
+        # bf16 values may also come as their 16 bits
+        types += [torch.bfloat16, torch.int16, torch.uint16] if kind == "bfloat16" else [torch.int32]
+    if x.dtype not in types or not x.is_contiguous() or x.numel() < numel:
         raise ValueError(f"{name}: {numel} contiguous {kind} elements are needed, got "
                          f"{tuple(x.shape)} {x.dtype}{'' if x.is_contiguous() else ' (not contiguous)'}")
     return x.data_ptr()
 
 
 def _bf16(x, name, numel):
-    return _dense(x, name, numel, "bfloat16")
+    """(Raw addresses are taken as they are.)"""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype in _BF16 and x.is_contiguous() and x.numel() >= numel:
+        return x.data_ptr()
+    return _dense(x, name, numel, "bfloat16", _BF16)
 
 
 def _int32(x, name, numel):
-    return _dense(x, name, numel, "int32")
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype in _INT32 and x.is_contiguous() and x.numel() >= numel:
+        return x.data_ptr()
+    return _dense(x, name, numel, "int32", _INT32)
 
 
 def _workspace(x):
