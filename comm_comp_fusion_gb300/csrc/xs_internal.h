@@ -182,8 +182,10 @@ struct SpanParams {
     uint32_t g_magic;           // row / G = row * g_magic >> 16 for rows below 128: ceil(2^16 / G)
     int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
     int min_steps_log2;         // fewest steps that a CTA is started for
+    int stretch;                // most steps that one sum in tensor memory takes; 0: no item has more (LONG = false)
     int merge_y;                // blocks per item in the merge
-    float *rec;                 // workspace: 2 records a CTA (Rec<D>), then a SpanPieces a CTA; NULL: whole items
+    float *rec;                 // workspace: 2 records a CTA (Rec<D>), one more a CTA for the segment at hand of a part in
+                                // several, then a SpanPieces a CTA; NULL: whole items, each one segment
     SpanPieces *pieces;
 };
 // TMA maps: q by query tile, k and v by 128-key tile or page (see xs_ops_api.cpp).

@@ -78,6 +78,11 @@ int check_workspace(const void *ws, size_t bytes, const Buffer *others, int n) {
 }
 float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634073599246810019); }
 
+// Most K/V tiles of a query tile pair without a workspace: 2^20 keys, after which a sum in
+// tensor memory, whose additions truncate, has lost about half a bf16 step. (With a workspace it is
+// taken in stretches.)
+constexpr int kStepsWithoutWorkspace = 1 << 13;
+
 // K/V tiles that the two query tiles of pair i of a whole sequence walk.
 int pair_steps(const SpanParams &p, int i) {
     const int tok = 256 * i, last = std::min(tok + 255, p.S - 1);
@@ -128,6 +133,11 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     const Buffer all[4] = {in[0], in[1], in[2], o};
     if ((st = check_workspace(ws, ws_bytes, all, 4))) return st;
     if (bytes == 0) return XS_OK;
+    p.S = S;
+    p.n_pairs = (S + 255) / 256;
+    for (int i = 0; !ws && S > 128 * kStepsWithoutWorkspace && i < p.n_pairs; ++i)
+        if (pair_steps(p, i) > kStepsWithoutWorkspace)
+            return api_fail(XS_ERR_WORKSPACE, "query tiles that walk over more than 2^20 keys need a workspace");
     int dev, sms;
     if ((st = api_device(&dev, &sms)) || (st = check_device(all, 4, dev))) return st;
     if (ws) {
@@ -141,7 +151,6 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     p.H = H;
     p.G = 1;
     p.B = B;
-    p.S = S;
     p.P = P;
     p.Hl = H / P;
     p.Sl = S / P;
@@ -150,7 +159,6 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     p.tile_tok = 128;
     p.item_tok = 256;
     p.heads = B * H;
-    p.n_pairs = (S + 255) / 256;
     if (ws && !whole_pairs(p, sms)) span_workspace_parts(ws, D, sms, &p);
     SpanMaps maps;
     const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.Hl, (uint64_t)S, (uint64_t)P * B};

@@ -46,6 +46,15 @@
 // unnormalised O, row maxima and sums to the workspace, and span_merge_kernel
 // adds them up in piece order (no atomics: the result is the same every time).
 //
+// Long items (LONG). The tensor cores' additions to O truncate: with values of 1, one sum over
+// 2^18 keys still rounds to 1, after 2^20 0.4% are missing, after 2^22 2.3%. Where a
+// sequence can hold more than 2^18 keys, what a CTA has of an item is therefore taken in
+// segments of 2048 tiles, each with a sum, maxima and row sums of its own. A segment's O goes
+// to the CTA's third record and is added to its part's record, in fp32 and rounded to
+// nearest, by the thread that has the row (or, with few rows, the column). These are instances
+// apart: their code costs short items 1 to 3% (mixed paged batch 82.9 us instead of 80.4).
+// They also keep every wait far below its limit, however long the sequence.
+//
 // Bounds. Single new tokens: HBM (32 sequences of 16000 keys, 8 key heads, D = 128, pages
 // of 32 tokens and more: 305 us, 6.9 TB/s; D = 64 and 96 reach 5.4; pages of 16 tokens
 // 5.9, their boxes' issue being the limit). Long chunks and windows: the chain S -
@@ -163,7 +172,7 @@ template <int D, bool PAGED, int FEW> struct SpanCfg {
     static constexpr uint32_t kOffL = kOffBar + 8 * ((SP_BARS + 1) & ~1);  // float [tile][l, m][128]
     static constexpr uint32_t kOffMisc = kOffL + 2 * 2 * 128 * 4;          // tmem base, abort flag, chain flags
     static constexpr uint32_t kOffSeg = kOffMisc + 16;                     // the ring of segments, then a SpanSched
-    static constexpr uint32_t kSmemAlloc = kOffSeg + 96 * kSegs + 64 + 1024;
+    static constexpr uint32_t kSmemAlloc = kOffSeg + (uint32_t)sizeof(SpanSeg) * kSegs + 64 + 1024;
     __host__ __device__ static constexpr uint32_t colS(int t) { return (FEW ? (uint32_t)FEW : 128u) * (uint32_t)t; }
     __host__ __device__ static constexpr uint32_t colO(int t) {
         return FEW ? (uint32_t)FEW * (uint32_t)(2 + t) : 256u + (uint32_t)D * (uint32_t)t;
@@ -172,6 +181,7 @@ template <int D, bool PAGED, int FEW> struct SpanCfg {
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
     static_assert(kSlots <= SPKV_EMPTY - SPKV_FULL, "barriers of the ring");
     static_assert(kSlots * kTile >= 8u * 2048u, "the schedule's sums (kSpanMaxChunks)");
+    static_assert((kOffSeg + sizeof(SpanSeg) * kSegs) % 8 == 0, "the SpanSched's place");
     static_assert(kOffQ % 1024 == 0 && kOffStage % 1024 == 0, "swizzled tiles");
 };
 
@@ -207,7 +217,7 @@ __device__ __forceinline__ uint32_t span_mask_word(int a, int b, int s, int col0
     return le & (ge | lt);
 }
 
-template <int D, bool PAGED, int FEW>
+template <int D, bool PAGED, int FEW, bool LONG>
 __global__ void __launch_bounds__(512, 1)
     span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
     using C = SpanCfg<D, PAGED, FEW>;
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     const int chunks = ((PAGED ? p.N : p.n_pairs) + 31) / 32;
     long long *sums = reinterpret_cast<long long *>(sm + C::kOffKV);  // the ring is not in use yet
-    SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSeg + 96 * kSegs);
+    SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSeg + (uint32_t)sizeof(SpanSeg) * kSegs);
     if (PAGED || p.rec) {
         if (chunks > 1) {
             span_chunk_sums<PAGED>(p, chunks, sums);
@@ -297,18 +307,21 @@ __global__ void __launch_bounds__(512, 1)
             SpanPieces pieces{};
             SpanWalk w;
             span_walk_init<PAGED>(p, *sched, w);
-            for (bool more = true; more; ++seg_it) {
+            for (bool more = true; more;) {
                 SpanSeg g;
                 more = span_next<PAGED>(p, *sched, w, g);
-                if (!more) g.n = 0;
-                if (more && g.piece && g.j0 == 0) pieces = span_pieces_of(*sched, g);  // its first piece: this CTA's last segment
-                if (!span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg)) break;
+                if (!more) g.n = 0;  // (and no rest)
+                if (more && g.flags && g.j0 == 0) pieces = span_pieces_of(*sched, g);  // its first piece: this CTA's last part
+                if (LONG) span_cut(g, p.stretch);
+                bool ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
+                if (!ok) break;
                 if (lane == 0) {
                     volatile SpanSeg &d = SEG;
                     d.n = g.n;
                     d.j0 = g.j0;
                     d.dual = g.dual;
-                    d.piece = g.piece;
+                    d.flags = g.flags;
+                    if (LONG) d.rest = g.rest;
                     d.hi = g.hi;
                     d.nw = g.nw;
                     d.ns = g.ns;
@@ -331,6 +344,20 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     mbar_arrive(SEG_FULL(seg_it % kSegs));
                 }
+                if (LONG) __syncwarp();
+                ++seg_it;
+#pragma unroll 1
+                while (LONG && segs[(seg_it - 1) % kSegs].rest) {  // the segments behind it
+                    ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        span_continue(SEG, segs[(seg_it - 1) % kSegs], p.stretch);
+                        mbar_arrive(SEG_FULL(seg_it % kSegs));
+                    }
+                    __syncwarp();
+                    ++seg_it;
+                }
+                if (!ok) break;
             }
             if ((PAGED || p.rec) && lane == 0) p.pieces[blockIdx.x] = pieces;
         } else if (warp == 0) {
@@ -1011,8 +1038,10 @@ __global__ void __launch_bounds__(512, 1)
             ok = SEG_WAIT(span_warp_bwait);
             volatile SpanSeg &g = SEG;
             if (!ok || g.n == 0) break;
-            const bool piece = g.piece;
-            float *rec = p.rec + (size_t)g.slot * R::kFloats;
+            // a segment among several of a part goes to the CTA's third record, and from there to its part's
+            auto several = [&]() -> bool { return LONG && g.flags & (SPAN_ADD | SPAN_MORE); };
+            const bool piece = g.flags;
+            float *rec = p.rec + (size_t)(several() ? 2 * gridDim.x + blockIdx.x : g.slot) * R::kFloats;
             auto row_dst = [&](int t, int rows) -> int64_t {
                 if (row >= rows) return -1;
                 const int r = span_row_tok<PAGED>(p, row);
@@ -1058,6 +1087,15 @@ __global__ void __launch_bounds__(512, 1)
                 rec[R::kML + t * 256 + row] = m;
                 rec[R::kML + t * 256 + 128 + row] = l;
             };
+            // m and l of a row's segment with what its part's record holds (written by this thread): their
+            // common maximum and sum, and the factors of either O
+            auto join = [&](float m_part, float l_part, float &m, float &l, float &a, float &a_part) {
+                const float top = fmaxf(m, m_part);
+                a = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                a_part = m_part == -INFINITY ? 0.f : ex2_approx(m_part - top);
+                l = a * l + a_part * l_part;
+                m = top;
+            };
             if constexpr (FEW > 0) {
                 // one thread per column of the output, all rows
                 ok = span_warp_bwait(BAR(SPO_FINAL + 0), seg_it & 1u, abort_flag, kSiteEpiO) &&
@@ -1097,6 +1135,34 @@ __global__ void __launch_bounds__(512, 1)
                         const int tk = span_row_tok<PAGED>(p, r);
                         p.out[span_out_offset<D, PAGED>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
                             (uint16_t)pack_bf16x2(l > 0.f ? f * (1.0f / l) : 0.f, 0.f);
+                    }
+                }
+                if (several() && row < D) {
+                    const int flags = g.flags;
+                    // as below for tiles; each thread keeps maxima and sums of its own, behind O in the third record
+                    float *part = p.rec + (size_t)g.slot * R::kFloats, *own = rec + FEW * D + row;
+                    static_assert(FEW * D + 256 * FEW <= R::kML, "their place in the record");
+#pragma unroll 1
+                    for (int r = 0; r < rows; ++r, own += 256) {
+                        const float l0 = row_ml[r], m0 = row_ml[128 + r], l1 = row_ml[256 + r], m1 = row_ml[384 + r];
+                        float m = fmaxf(m0, m1), a = 1.f, a_part = 0.f;
+                        float l = (m0 == -INFINITY ? 0.f : ex2_approx(m0 - m) * l0) + (m1 == -INFINITY ? 0.f : ex2_approx(m1 - m) * l1);
+                        if (flags & SPAN_ADD) join(own[0], own[128], m, l, a, a_part);
+                        float f = rec[r * D + row] * a;  // zero where no key has been seen
+                        if (a_part > 0.f) f = fmaf(part[r * D + row], a_part, f);
+                        own[0] = m;
+                        own[128] = l;
+                        if (flags & (SPAN_PIECE | SPAN_MORE)) {
+                            part[r * D + row] = f;
+                            if (row == 0) {
+                                part[R::kML + r] = m;
+                                part[R::kML + 128 + r] = l;
+                            }
+                        } else {
+                            const int tk = span_row_tok<PAGED>(p, r);
+                            p.out[span_out_offset<D, PAGED>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
+                                (uint16_t)pack_bf16x2(l > 0.f ? f * (1.0f / l) : 0.f, 0.f);
+                        }
                     }
                 }
                 __syncwarp();
@@ -1163,6 +1229,43 @@ __global__ void __launch_bounds__(512, 1)
                         for (int i = 0; i < 32; ++i) f[i] = u2f(o[i]) * inv;
                         emit(t, c0, f, dst, any_row);
                     }
+                }
+            }
+            if constexpr (LONG && FEW == 0) {
+                if (ok && several()) {
+                    // the rows' segment from the third record to their part's record or, the part being all
+                    // of the item and this its last segment, to the output
+#pragma unroll 1
+                    for (int t = 0; t < (g.dual ? 1 : 2); ++t) {
+                        const int64_t dst = row_dst(t, min(g.ntok - t * p.tile_tok, p.tile_tok) * p.G);
+                        if (dst < 0) continue;
+                        float *part = p.rec + (size_t)g.slot * R::kFloats;
+                        const size_t ml = R::kML + t * 256 + row, at = (size_t)t * (D / 4) * 128 + row;
+                        const int flags = g.flags;
+                        float m = rec[ml], l = rec[ml + 128], a = 1.f, a_part = 0.f;
+                        if (flags & SPAN_ADD) join(part[ml], part[ml + 128], m, l, a, a_part);
+                        const bool out = !(flags & (SPAN_PIECE | SPAN_MORE));
+                        const float inv = !out ? 1.f : l > 0.f ? 1.0f / l : 0.f;
+                        part[ml] = m;
+                        part[ml + 128] = l;
+#pragma unroll 1
+                        for (int c = 0; c < D / 4; ++c) {
+                            const float4 x = reinterpret_cast<const float4 *>(rec)[at + c * 128];
+                            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (a > 0.f) f = make_float4(x.x * a, x.y * a, x.z * a, x.w * a);  // (else there is no O)
+                            float4 *o4 = reinterpret_cast<float4 *>(part) + at + c * 128;
+                            if (a_part > 0.f) {
+                                const float4 y = *o4;
+                                f = make_float4(fmaf(y.x, a_part, f.x), fmaf(y.y, a_part, f.y), fmaf(y.z, a_part, f.z), fmaf(y.w, a_part, f.w));
+                            }
+                            if (!out)
+                                *o4 = f;
+                            else
+                                *reinterpret_cast<uint2 *>(p.out + dst + 4 * c) =
+                                    make_uint2(pack_bf16x2(f.x * inv, f.y * inv), pack_bf16x2(f.z * inv, f.w * inv));
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (ok) SEG_DONE();
@@ -1270,9 +1373,9 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     }
 }
 
-template <int D, bool PAGED, int FEW>
+template <int D, bool PAGED, int FEW, bool LONG>
 static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
-    auto kern = span_attn_kernel<D, PAGED, FEW>;
+    auto kern = span_attn_kernel<D, PAGED, FEW, LONG>;
     static std::atomic<uint64_t> configured{0};  // devices where the shared-memory limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1311,12 +1414,18 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
     return e;
 }
 
+template <int D, bool PAGED, int FEW>
+static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
+    return p.stretch ? launch_span_one<D, PAGED, FEW, true>(maps, p, grid, stream)
+                     : launch_span_one<D, PAGED, FEW, false>(maps, p, grid, stream);
+}
+
 #define XS_DEFINE_SPAN_ENTRY(D)                                                                                       \
     cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
-        if (!p.table) return launch_span_one<D, false, 0>(maps, p, grid, stream);                                     \
-        if (p.few == 16) return launch_span_one<D, true, 16>(maps, p, grid, stream);                                  \
-        if (p.few == 32) return launch_span_one<D, true, 32>(maps, p, grid, stream);                                  \
-        return launch_span_one<D, true, 0>(maps, p, grid, stream);                                                    \
+        if (!p.table) return launch_span_form<D, false, 0>(maps, p, grid, stream);                                    \
+        if (p.few == 16) return launch_span_form<D, true, 16>(maps, p, grid, stream);                                 \
+        if (p.few == 32) return launch_span_form<D, true, 32>(maps, p, grid, stream);                                 \
+        return launch_span_form<D, true, 0>(maps, p, grid, stream);                                                   \
     }                                                                                                                 \
     cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear) {                                          \
         cudaError_t e = cudaMemcpyFromSymbol(value, g_xs_error, sizeof(unsigned int));                                \

@@ -281,23 +281,33 @@ struct SpanWalk {
     int q0, q_len, keys;
     bool first;      // no shared segment yet
 };
-// What the roles need to know of a segment (96 bytes).
+// What a CTA has of an item, its part, is one segment, or several of p.stretch steps: O of a
+// segment is one sum in tensor memory, whose additions truncate (values of 1: 0.4% are missing
+// after 2^20 keys, 2.3% after 2^22; in two chains 1.2% after 2^22, 5% after 2^24). Segments
+// of a part are added up in a workspace record (the epilogue).
+enum : int {
+    SPAN_PIECE = 1,  // the part is not the whole item
+    SPAN_ADD = 2,    // not the part's first segment
+    SPAN_MORE = 4    // nor its last
+};
+// What the roles need to know of a segment.
 struct SpanSeg {
     int n;            // steps; 0: no segment, the roles are done
     int j0;           // the item's step that it starts with
-    int dual, piece;  // piece: not the whole item
+    int dual, flags;
+    int rest;         // the part's steps behind it
     int hi, nw, ns, s0, e1;
     int seq, head;
     int q0, tok0, ntok;  // the sequence's first packed row; the item's first token, their number
     int pos0, keys;      // the first token's place; the sequence's keys
-    int slot;            // workspace record of a piece
+    int slot;            // the part's workspace record
     int fix;             // rows of the first V tile that hold keys, where the rest has to be cleared; -1: nothing to do
     int lo, last;        // first key of the window, last key that any token sees
     // a row of tile t misses a key of the K/V tile at c0 iff c0 > all_hi[t], or
     // c0 < all_lo[t] and the tile's keys are not all sinks
     int all_hi[2], all_lo[2];
 };
-static_assert(sizeof(SpanSeg) == 96, "segment ring");
+static_assert(sizeof(SpanSeg) == 100, "segment ring");
 __device__ __forceinline__ int span_tile(const volatile SpanSeg &g, int y) {
     const int nw = g.nw;
     return y < nw ? g.hi - y : g.ns - 1 - (y - nw);
@@ -341,6 +351,7 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
     span_lengths<PAGED>(p, 0, w.q0, w.q_len, w.keys);
     span_skip(p, w, (int)blockIdx.x);
 }
+// The next part, as one segment.
 template <bool PAGED>
 __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
     if ((PAGED || w.rounds == 0) && w.rem <= 0) return false;
@@ -391,7 +402,7 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
             }
         }
     }
-    g.piece = g.n < it.n;
+    g.flags = g.n < it.n ? SPAN_PIECE : 0;
     for (int t = 0; t < 2; ++t) {
         const int tt = it.dual ? 0 : t * p.tile_tok, toks = min(it.ntok - tt, p.tile_tok);
         g.all_hi[t] = min(it.pos0 + tt + p.right, w_keys - 1) - 127;
@@ -403,12 +414,31 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
     return true;
 }
 
+// Cuts what follows the first `stretch` steps off a part.
+__device__ __forceinline__ void span_cut(SpanSeg &g, int stretch) {
+    g.rest = max(g.n - stretch, 0);
+    g.n -= g.rest;
+    if (g.rest) g.flags |= SPAN_MORE;
+}
+// The segment d that follows segment o in its part.
+__device__ __forceinline__ void span_continue(volatile SpanSeg &d, const volatile SpanSeg &o, int stretch) {
+#pragma unroll 1
+    for (int i = 0; i < (int)(sizeof(SpanSeg) / sizeof(int)); ++i)
+        reinterpret_cast<volatile int *>(&d)[i] = reinterpret_cast<const volatile int *>(&o)[i];
+    const int rest = o.rest;
+    d.j0 = o.j0 + o.n;
+    d.n = min(rest, stretch);
+    d.rest = max(rest - stretch, 0);
+    d.fix = -1;
+    d.flags = (o.flags & SPAN_PIECE) | SPAN_ADD | (rest > stretch ? SPAN_MORE : 0);
+}
+
 // Written by each CTA for span_merge_kernel: the item whose first piece is the
-// CTA's last segment (pieces 0: none).
+// CTA's last part (pieces 0: none).
 struct SpanPieces {
     int pieces, slot, seq, head, tok0, ntok, q0, unused;
 };
-// Of a segment that is an item's first piece: its pieces lie in this CTA and the next ones.
+// Of a part that is an item's first piece: its pieces lie in this CTA and the next ones.
 __device__ __forceinline__ SpanPieces span_pieces_of(const SpanSched &s, const SpanSeg &g) {
     const int left = g.nw + g.ns - g.n;
     const long long end = span_first<unsigned long long>(s.q, s.r, s.ctas, (int)blockIdx.x + 1) + left;  // behind the item's last step

@@ -378,7 +378,9 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
  *   workspace, workspace_bytes : device memory, 256-byte aligned, of at least
  *            xs_attn_window_workspace_size bytes; it needs no initialisation. With
  *            it the work is split evenly over the SMs, pieces of a query tile
- *            meeting in the workspace. NULL (with 0): whole query tiles only.
+ *            meeting in the workspace. NULL (with 0): whole query tiles only, and
+ *            XS_ERR_WORKSPACE where those walk over more than 2^20 keys: sums in
+ *            tensor memory truncate, and longer ones are added up in a workspace.
  * k and v must be finite: a key that a token does not see has no weight, but 0
  * times an infinity or NaN next to keys that it sees is NaN.
  * A row of q that is not finite gives an output row of no particular values, and

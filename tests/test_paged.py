@@ -321,6 +321,43 @@ def test_paged_pool_past_32_bits():
     assert torch.equal(rows.reshape(-1), k.reshape(-1))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,Hk,D,keys", ((1, 152, 152, 64, 2 ** 23 - 77), (1, 190, 190, 128, 2 ** 21 + 5),
+                                           (3, 304, 38, 64, 2 ** 22 + 1), (100, 170, 170, 64, 2 ** 21 - 9),
+                                           (256, 160, 160, 64, 2 ** 22 - 300), (200, 152, 152, 128, 2 ** 20 + 900)))
+def test_paged_very_many_keys(T, H, Hk, D, keys):
+    """Millions of keys a sequence in every form, whole items and pieces: sums in tensor memory truncate, so they are taken
+    in stretches. Values around 1, where that shows. Four pages stand for all, so a key's weight counts as often as it
+    comes. The bound: that of span_testlib.attend, and 2^14 additions of a stretch that truncate by 2^-23 at most."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    page, n_pages = 1024, 4
+    max_pages, own = -(-keys // page), n_pages * page
+    gen = torch.Generator(device="cuda").manual_seed(keys)
+    rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda")  # noqa: E731
+    q, kp, vp = rand(T, H, D).bfloat16(), rand(n_pages, page, Hk, D).bfloat16(), (1 + 0.25 * rand(n_pages, page, Hk, D)).bfloat16()
+    table = (torch.arange(max_pages, device="cuda") % n_pages).to(torch.int32)
+    q_start, kv_len = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, T], [keys]))
+    out = guarded(T * H * D)
+    ws = guarded(xs.attn_paged_workspace_size(1, T, H, Hk, D), torch.uint8, 0xFF)
+    xs.attn_paged(q, kp, vp, table, q_start, kv_len, out, 1, T, H, Hk, D, page, n_pages, max_pages, D ** -0.5, workspace=ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got = from_dev(out).reshape(T, H, D)
+    j, pos = torch.arange(own, device="cuda"), torch.arange(keys - T, keys, device="cuda")
+    often = ((pos.view(-1, 1) - j) // own + 1).double()
+    for h in sorted({0, 1, H // 5, H // 3, H // 2, 2 * H // 3, 4 * H // 5, H - 2, H - 1}):
+        k, v = kp[:, :, h * Hk // H].reshape(own, D).double(), vp[:, :, h * Hk // H].reshape(own, D).double()
+        qd = q[:, h].double()
+        s = qd @ k.T * D ** -0.5
+        w = often * (s - s.amax(-1, keepdim=True)).exp()
+        w = w / w.sum(-1, keepdim=True)
+        ref, a = w @ v, w @ v.abs()
+        delta = 2.0 ** -18 * (qd.abs() @ k.abs().T * D ** -0.5).amax(-1, keepdim=True)
+        bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * delta + 2.0 ** -9) * a
+        check(got[:, h], ref.cpu().numpy(), bound.cpu().numpy(), f"head {h}")
+
+
 # ------------------------------------------------------------------ append
 
 APPEND = [  # q_len, kv_len, Hk, D, page, spare

@@ -126,17 +126,22 @@ template <bool PAGED> static void call(SpanParams &p) {
         span_walk_init<PAGED>(p, s[0], w);
         SpanSeg g;
         while (span_next<PAGED>(p, s[0], w, g)) {
-            std::printf("s %u %d %d %d %d %d %d %d\n", c, g.seq, g.head, g.tok0, g.j0, g.n, g.nw + g.ns, g.piece ? g.slot : -1);
-            if (g.piece && g.j0 == 0) pieces = span_pieces_of(s[0], g);
+            if (g.flags && g.j0 == 0) pieces = span_pieces_of(s[0], g);
+            span_cut(g, p.stretch);
+            for (bool more = true; more;) {
+                std::printf("s %u %d %d %d %d %d %d %d %d\n", c, g.seq, g.head, g.tok0, g.j0, g.n, g.nw + g.ns, g.flags, g.slot);
+                const SpanSeg o = g;
+                if ((more = o.rest > 0)) span_continue(g, o, p.stretch);
+            }
         }
         if (pieces.pieces) std::printf("p %u %d %d %d %d %d\n", c, pieces.seq, pieces.head, pieces.tok0, pieces.pieces, pieces.slot);
     }
 }
 
 int main() {
-    int paged, grid, heads, item_tok, tile_tok, left, right, sinks, log2, S, N;
+    int paged, grid, heads, item_tok, tile_tok, left, right, sinks, log2, stretch, S, N;
     static float rec[1];
-    while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d", &paged, &grid, &heads, &item_tok, &tile_tok, &left, &right, &sinks, &log2, &S, &N) == 11) {
+    while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d %d", &paged, &grid, &heads, &item_tok, &tile_tok, &left, &right, &sinks, &log2, &stretch, &S, &N) == 12) {
         SpanParams p{};
         p.heads = heads;
         p.item_tok = item_tok;
@@ -145,6 +150,7 @@ int main() {
         p.right = right < 0 ? 1 << 29 : right;
         p.sinks = sinks;
         p.min_steps_log2 = log2;
+        p.stretch = stretch;
         p.rec = rec;
         grid_.x = grid;
         std::vector<int> starts(1, 0), kv;
@@ -208,23 +214,46 @@ def steps_of(pos0, ntok, keys, left, right, sinks):
     return len(tiles)
 
 
-def verify(lines, items, grid):
+PIECE, ADD, MORE = 1, 2, 4
+WHOLE = 1 << 30
+
+
+def verify(lines, items, grid, stretch=WHOLE):
     """items: {(seq, head, tok0): steps}."""
-    parts, merges, at = {}, {}, 0
+    parts, merges, open_, kept = {}, {}, {}, {}
     for line in lines:
         kind, *x = line.split()
         assert kind in "sp", line
         x = [int(v) for v in x]
         if kind == "s":
-            cta, seq, head, tok0, j0, n, total, slot = x
-            assert items[seq, head, tok0] == total and n >= 1
-            assert (slot < 0) == (n == total), line
-            parts.setdefault((seq, head, tok0), []).append((cta, j0, n, slot))
+            cta, seq, head, tok0, j0, n, total, flags, slot = x
+            item = seq, head, tok0
+            assert items[item] == total and 1 <= n <= stretch
+            assert 2 * cta <= slot <= 2 * cta + 1
+            # the segments of a part follow one another and use one record, which no kept one has
+            if flags & ADD:
+                assert open_[cta][:3] == (item, j0, slot), line
+            else:
+                assert open_.get(cta) is None, line
+                open_[cta] = (item, j0, slot, j0)
+            begin = open_[cta][3]
+            if flags != 0:
+                assert slot not in kept, (line, kept[slot])
+            if flags & MORE:
+                assert n == stretch
+                open_[cta] = (item, j0 + n, slot, begin)
+                continue
+            open_[cta] = None
+            whole = begin == 0 and j0 + n == total
+            assert bool(flags & PIECE) != whole, line
+            parts.setdefault(item, []).append((cta, begin, j0 + n - begin, None if whole else slot))
+            if not whole:
+                kept[slot] = line
         else:
             cta, seq, head, tok0, pieces, slot = x
             merges[seq, head, tok0] = [slot] + [2 * (cta + i) for i in range(1, pieces)]
             assert cta + pieces <= grid
-    assert set(parts) == set(items)
+    assert set(parts) == set(items) and not any(open_.values())
     for item, segs in parts.items():
         segs.sort(key=lambda s: s[1])
         at = 0
@@ -233,23 +262,22 @@ def verify(lines, items, grid):
             at += n
         assert at == items[item]
         if len(segs) == 1:
-            assert item not in merges
+            assert item not in merges and segs[0][3] is None
             continue
         # the records the merge adds up are those that the pieces write, in order
         assert merges[item] == [s[3] for s in segs], (item, segs, merges[item])
-    slots = [s for m in merges.values() for s in m]
-    assert len(slots) == len(set(slots)) and all(0 <= s < 2 * grid for s in slots)
 
 
 def window_items(S, heads, left, right, sinks):
     return {(0, h, t): steps_of(t, min(256, S - t), S, left, right, sinks) for h in range(heads) for t in range(0, S, 256)}
 
 
-def window(walk, cases):
-    text = "".join(f"0 {grid} {heads} 256 128 {left} {right} {sinks} 2 {S} 0\n" for grid, heads, S, left, right, sinks in cases)
+def window(walk, cases, stretch=WHOLE):
+    text = "".join(f"0 {grid} {heads} 256 128 {left} {right} {sinks} 2 {stretch} {S} 0\n"
+                   for grid, heads, S, left, right, sinks in cases)
     for case, lines in zip(cases, walk(text)):
         grid, heads, S, left, right, sinks = case
-        verify(lines, window_items(S, heads, left, right, sinks), grid)
+        verify(lines, window_items(S, heads, left, right, sinks), grid, stretch)
 
 
 def test_window_rests_smaller_than_the_grid(walk):
@@ -277,7 +305,8 @@ def test_window_any_shape(walk):
         left = rng.choice((-1, 0, rng.randint(0, 300), rng.randint(0, 4000)))
         right = rng.choice((-1, 0, 0, left, rng.randint(0, 1000)))
         cases.append((grid, heads, S, left, right, rng.choice((0, 0, 4, 128, 300))))
-    window(walk, cases)
+    for stretch in (WHOLE, 1, 3, 16):
+        window(walk, cases, stretch)
 
 
 def test_paged_any_batch(walk):
@@ -292,12 +321,12 @@ def test_paged_any_batch(walk):
         left = rng.choice((-1, -1, 0, rng.randint(0, 700)))
         right, sinks = rng.choice((0, 0, -1, rng.randint(0, 300))), rng.choice((0, 4, 200))
         log2 = 0 if few else 1
-        lens = []
+        lens, stretch = [], rng.choice((WHOLE, WHOLE, 1, 2, 7, 30))
         for _ in range(N):
             q = rng.choice((0, 1, 1, rng.randint(1, 5), rng.randint(1, 3 * item)))
             lens.append((q, rng.choice((0, q, q + rng.randint(0, 300), q + rng.randint(0, 5000), rng.randint(0, q)))))
-        text += f"1 {grid} {heads} {item} {tile} {left} {right} {sinks} {log2} 0 {N} " + " ".join(f"{a} {b}" for a, b in lens) + "\n"
-        wants.append((grid, {(n, h, t): steps_of(k - q + t, min(item, q - t), k, left, right, sinks)
-                             for n, (q, k) in enumerate(lens) for h in range(heads) for t in range(0, q, item)}))
-    for (grid, items), lines in zip(wants, walk(text)):
-        verify(lines, items, grid)
+        text += f"1 {grid} {heads} {item} {tile} {left} {right} {sinks} {log2} {stretch} 0 {N} " + " ".join(f"{a} {b}" for a, b in lens) + "\n"
+        wants.append((grid, stretch, {(n, h, t): steps_of(k - q + t, min(item, q - t), k, left, right, sinks)
+                                       for n, (q, k) in enumerate(lens) for h in range(heads) for t in range(0, q, item)}))
+    for (grid, stretch, items), lines in zip(wants, walk(text)):
+        verify(lines, items, grid, stretch)

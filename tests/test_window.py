@@ -263,6 +263,56 @@ def test_window_rest_of_fewer_steps_than_sms(case):
     assert np.array_equal(outs[0], outs[1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,H,span", ((2 ** 20 + 77, 1, (-1, 0, 0)), (1300001, 1, (290000, 0, 500)), (530000, 2, (-1, -1, 0))))
+def test_window_of_very_many_keys(S, H, span):
+    """Items of thousands of K/V tiles, whose sums are taken in stretches: values around 1, of which a single sum in tensor
+    memory loses what its additions truncate (2^-23 at most each, 2^14 of them in a stretch: 2^-9 more than the bound of
+    span_testlib.attend)."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    D = 64
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    q, k, v = (torch.randn(1, 1, S, H, D, generator=gen, device="cuda") for _ in range(3))
+    q, k, v = q.bfloat16(), k.bfloat16(), (1 + 0.25 * v).bfloat16()
+    out = guarded(q.numel())
+    ws = guarded(xs.attn_window_workspace_size(1, S, H, D, 1), torch.uint8, 0xFF)
+    xs.attn_window(q, k, v, out, 1, S, H, D, 1, D ** -0.5, *span, ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got = from_dev(out).reshape(S, H, D)
+    for i in (0, 255, S // 3, S // 2 + 1, S - 300, S - 1):
+        lo = 0 if span[0] < 0 else max(0, i - span[0])
+        hi = S if span[1] < 0 else i + 1
+        at = torch.cat((torch.arange(min(span[2], lo)), torch.arange(lo, hi))).cuda()
+        for h in range(H):
+            qd, kd, vd = (x.double().cpu().numpy() for x in (q[0, 0, i:i + 1, h], k[0, 0, at, h], v[0, 0, at, h]))
+            ref, bound = attend(qd, kd, vd, np.ones((1, len(at)), bool), D ** -0.5)
+            check(got[i:i + 1, h], ref, bound + 2.0 ** -9 * np.abs(ref), f"row {i} head {h}")
+
+
+def test_window_without_workspace_takes_no_more_keys_than_it_can_add_up():
+    import __graft_entry__
+    __graft_entry__.build()
+    import comm_comp_fusion_gb300 as xs
+
+    def f(S, left, right, sinks, ws=None, nb=None):
+        return xs.attn_window(Q, Q + (1 << 33), Q + (2 << 33), Q + (3 << 33), 1, S, 1, 64, 1, 0.1, left, right, sinks, ws, nb,
+                              check=False)
+
+    M = 1 << 20
+    for S, *span in ((M + 1, -1, 0, 0), (1 << 24, -1, -1, 0), (2 * M, M, 0, 0), (3 * M, 100, 0, M), (1 << 24, 0, M, 0)):
+        assert f(S, *span) == xs.XS_ERR_WORKSPACE and "2^20" in xs.last_error()
+        assert f(S, *span, Q + (4 << 33), 1 << 28) != xs.XS_ERR_WORKSPACE or _gpu()
+    for S, *span in ((M, -1, -1, 0), (1 << 24, 1000, 1000, 100000), (2 * M, M - 512, 0, 0)):
+        assert f(S, *span) in (xs.XS_ERR_CUDA, xs.XS_ERR_UNSUPPORTED)   # no device, or addresses of nothing
+
+
+def _gpu():
+    import torch
+    return torch.cuda.is_available()
+
+
 Q, K, V, O, W = 0x10000000, 0x20000000, 0x30000000, 0x40000000, 0x50000000
 
 
