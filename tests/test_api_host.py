@@ -200,3 +200,13 @@ def test_host_buffer_argument_checks(xs):
     g = lambda hv=HV: xs.attn_host(HQ, HK, hv, HO, Q, K, V, O, 1, 256, 8, 64, 4, 0.125, check=False)
     assert g(hv=0) == xs.XS_ERR_NULL
     assert g(hv=O) == xs.XS_ERR_ALIAS
+
+
+def test_current_stream_without_the_shortcut(xs, monkeypatch):
+    """Where torch lacks the raw lookup, its public one gives the current stream."""
+    import types
+    import torch
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=77 + device))
+    on_gpu = types.SimpleNamespace(is_cuda=True, device=1, get_device=lambda: 1)
+    assert xs._stream(None, None, on_gpu) == 78 and xs._stream(5, on_gpu) == 5
