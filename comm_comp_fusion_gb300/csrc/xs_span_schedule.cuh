@@ -203,9 +203,15 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
 // Whole items dealt out round by round first, and the steps they hold (whole
 // sequences). None unless the items are of about one length (their mean at least
 // 4/5 of the longest: a CTA's rounds then end about when the others' do) and
-// there are two for each CTA. The last round is shared out in steps with the rest
-// when the rest alone would give each CTA less than 0.4 of an item: short pieces
-// cost more than they balance. `sum`: the steps of one head.
+// there are two for each CTA. S = 4096, H = 48, D = 128, windows to the left: mean 0.62 of the
+// longest, 182 us in rounds and 164 without; 0.75 154 and 144; 0.81 131 and 128; 0.88 106 and
+// 122; 0.94 83 and 89. All full rounds are dealt out, however little is left: sharing the
+// last of them too costs 2 to 20% (two-sided window of 512, S = 4096: 60.7 us, 64.9 with 23 heads,
+// 0.42 items a CTA left; 57.3, 62.2 with 22; 52.3, 56.4 with 20; 104.1, 107.8 with 48, 5
+// rounds). Of many rounds of long items it gains 1%: S = 16384, H = 24, 10 rounds of up to 35
+// steps and 0.1 items left 501 us, 496 shared; S = 8192, 5 rounds of up to 18, 0.05 left
+// 160.1, 158.6; 0.26 164.3, 163.1; 0.47 168.7, 173.5; but 2 rounds 75.1, 82.2. `sum`: the
+// steps of one head.
 __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long long sum, int lane, long long &steps) {
     steps = 0;
     const long long items = (long long)p.heads * p.n_pairs;
@@ -214,7 +220,7 @@ __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long l
     if (items < 2ll * grid || 5 * sum < 4ll * p.n_pairs * most) return 0;
     int rounds = (int)(items / grid);
     const int rest = (int)(items - (long long)rounds * grid);
-    if (rest && 5 * rest < 2 * grid) --rounds;
+    if (rest && rounds >= 5 && most >= 16 && 5 * rest < 2 * grid) --rounds;
     const long long first = (long long)rounds * grid, head = first / p.n_pairs;  // the first shared item
     const int pairs = (int)(first - head * p.n_pairs);
 #pragma unroll 1

@@ -236,7 +236,7 @@ def test_window_on_two_streams_at_once():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("case", ((21, 256, 32, 64, 1, -1, 0, 0), (23, 200, 16, 96, 1, -1, 0, 0), (13, 256, 40, 64, 2, -1, -1, 0),
-                                  (1, 1280, 73, 64, 1, 0, 0, 0)))
+                                  (1, 1280, 73, 64, 1, 0, 0, 0), (2, 256, 160, 64, 1, -1, -1, 0), (5, 300, 31, 128, 1, 70, 0, 0)))
 def test_window_rest_of_fewer_steps_than_sms(case):
     """Whole rounds, then items of two or three steps whose steps are fewer than the CTAs (152 SMs): every head, with
     a workspace that holds NaN or finite leftovers of another call, which no result may depend on."""
