@@ -401,10 +401,21 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
     p.n_pages = n_pages;
     p.max_pages = max_pages;
     p.scale_log2 = scale_log2(scale);
-    // Few rows: batches of mostly single new tokens. The rows a sequence and key head
-    // have on average decide; longer sequences among them take several items.
+    // Few rows: batches of mostly single new tokens. The rows that a sequence and key head
+    // have on average decide (the lengths are on the device); a longer sequence among them takes
+    // an item for each tile of 16 or 32 rows, each of which walks all its keys. Tiles of 16, 32
+    // and 128 rows, us, 8 key heads:
+    //   rows  16 x 4000 keys D = 128  16 x 4000 D = 64   16 x 1000 D = 128  4 x 1000 D = 64
+    //     8     48.6   49.2   52.9     33.0  34.9  36.0
+    //    16     49.7   50.9   53.5     34.2  36.5  36.2   19.2  22.6  20.1   12.9  14.0  12.3
+    //    20            52.8   55.7           37.8  36.5         23.5  20.3         14.7  12.4
+    //    24            53.9   55.2           38.9  36.4         24.8  20.4         15.3  12.5
+    //    32            57.8   55.8           42.5  36.3         27.7  21.0         17.8  12.7
+    // and with more parts an item 32 gains more: 3 x 20000, 2 heads, 20 rows, D = 128 21.4 us, 25.7 with
+    // tiles of 128. A chunk among single tokens costs: 64 of them over 1000 keys with 400 tokens over 8000
+    // (G = 4, so 29 rows) took 244 us in tiles of 32 and 92 in tiles of 128, apart 50 and 52.
     const long long rows_avg = ((long long)T * p.G + N - 1) / N;
-    p.few = p.G <= 16 && rows_avg <= 16 ? 16 : p.G <= 32 && rows_avg <= 32 ? 32 : 0;
+    p.few = p.G <= 16 && rows_avg <= 16 ? 16 : D > 64 && p.G <= 32 && rows_avg <= 24 ? 32 : 0;
     p.tile_tok = (p.few ? p.few : 128) / p.G;
     p.item_tok = p.few ? p.tile_tok : 2 * p.tile_tok;
     for (p.page_log2 = 4; 1 << p.page_log2 < page;) ++p.page_log2;

@@ -1424,7 +1424,8 @@ static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, i
     cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
         if (!p.table) return launch_span_form<D, false, 0>(maps, p, grid, stream);                                    \
         if (p.few == 16) return launch_span_form<D, true, 16>(maps, p, grid, stream);                                 \
-        if (p.few == 32) return launch_span_form<D, true, 32>(maps, p, grid, stream);                                 \
+        if constexpr (D > 64)                                                                                         \
+            if (p.few == 32) return launch_span_form<D, true, 32>(maps, p, grid, stream);                             \
         return launch_span_form<D, true, 0>(maps, p, grid, stream);                                                   \
     }                                                                                                                 \
     cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear) {                                          \

@@ -441,6 +441,13 @@ xs_status xs_cache_append(const void *k, const void *v, void *k_pages, void *v_p
  * K and V of a sequence's own kv_len tokens must be finite; what lies behind them
  * in the last page, and in pages the window has passed, may hold anything.
  * H % Hk == 0 and H / Hk <= 128.
+ * Speed: the kernel's form is chosen on the host, from T * H / (N * Hk), the query rows
+ * that a sequence and key head have on average: at most 16 (with D > 64, 24) mean single
+ * tokens and tiles of few rows. A long chunk in such a call takes an item for each such
+ * tile, and is faster in a call of its own (255 single tokens over 1000 keys with a chunk of
+ * 256 over 8000, H = 64, Hk = 8: 616 us in one call, 246 in two). Single tokens in a call of
+ * mostly chunks take tiles of 128 rows, which costs them 3 to 13%. Rows of no sequence
+ * count in T too.
  */
 xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
                         const int32_t *q_start, const int32_t *kv_len, void *out, int N, int T, int H, int Hk, int D,

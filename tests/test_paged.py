@@ -271,6 +271,21 @@ def test_paged_few_rows(D, G, q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_len,G,spare", (([1] * 30 + [50] + [1] * 30, 4, 0), ([60] + [1] * 20, 5, 3), ([1] * 9 + [0, 17], 8, 0),
+                                           ([1] * 12, 4, 150), ([1] * 12, 4, 400)))
+@pytest.mark.parametrize("D", (64, 96, 128))
+def test_paged_chunk_among_single_tokens(D, q_len, G, spare):
+    """A chunk of many few-rows tiles in a batch of single tokens, and single tokens with many rows of no sequence: the
+    form follows the average, the results do not."""
+    kv = [n + 37 * i % 500 for i, n in enumerate(q_len)]
+    kv[q_len.index(max(q_len))] += 700
+    for span in ((-1, 0, 0), (90, 5, 3)):
+        b = Batch(q_len, kv, 2 * G, 2, D, 32, spare=spare, seed=D + G)
+        b.call(*span)
+        b.verify(*span, what=f"{span}")
+
+
+@pytest.mark.gpu
 def test_paged_graph_follows_lengths():
     """A captured call follows table, lengths and starts that change between replays; two captured calls take turns in
     one workspace."""
@@ -323,7 +338,7 @@ def test_paged_pool_past_32_bits():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H,Hk,D,keys", ((1, 152, 152, 64, 2 ** 23 - 77), (1, 190, 190, 128, 2 ** 21 + 5),
-                                           (3, 304, 38, 64, 2 ** 22 + 1), (100, 170, 170, 64, 2 ** 21 - 9),
+                                           (3, 304, 38, 96, 2 ** 22 + 1), (100, 170, 170, 64, 2 ** 21 - 9),
                                            (256, 160, 160, 64, 2 ** 22 - 300), (200, 152, 152, 128, 2 ** 20 + 900)))
 def test_paged_very_many_keys(T, H, Hk, D, keys):
     """Millions of keys a sequence in every form, whole items and pieces: sums in tensor memory truncate, so they are taken
