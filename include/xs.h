@@ -385,6 +385,10 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
  * times an infinity or NaN next to keys that it sees is NaN.
  * A row of q that is not finite gives an output row of no particular values, and
  * changes no other.
+ * Rounding: scores, row maxima, sums and outputs are held in fp32; the softmax's weights
+ * are rounded to bf16 (by at most 2^-8 each) before their product with v, the output once
+ * at the end. Outputs differ from exact ones by 0.0021 to 0.0024 of their norm, 0.0017
+ * being the output's own rounding.
  * left, right >= -1, sinks >= 0, S <= 2^24. D = 64, 96 or 128 (XS_ERR_UNSUPPORTED otherwise).
  */
 xs_status xs_attn_window(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P,
@@ -439,7 +443,8 @@ xs_status xs_cache_append(const void *k, const void *v, void *k_pages, void *v_p
  *   workspace, workspace_bytes : required (unless the call is empty), as for
  *            xs_attn_window, of xs_attn_paged_workspace_size bytes.
  * K and V of a sequence's own kv_len tokens must be finite; what lies behind them
- * in the last page, and in pages the window has passed, may hold anything.
+ * in the last page, and in pages the window has passed, may hold anything. Rows of
+ * q that are not finite, and rounding: as for xs_attn_window.
  * H % Hk == 0 and H / Hk <= 128.
  * Speed: the kernel's form is chosen on the host, from T * H / (N * Hk), the query rows
  * that a sequence and key head have on average: at most 16 (with D > 64, 24) mean single
