@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(512, 1)
             for (bool more = true; more;) {
                 SpanSeg g;
                 more = span_next<PAGED>(p, *sched, w, g);
-                if (!more) g.n = 0;  // (and no rest)
                 if (more && g.flags && g.j0 == 0) pieces = span_pieces_of(*sched, g);  // its first piece: this CTA's last part
                 if (LONG) span_cut(g, p.stretch);
                 bool ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
@@ -322,7 +321,6 @@ __global__ void __launch_bounds__(512, 1)
                     d.j0 = g.j0;
                     d.dual = g.dual;
                     d.flags = g.flags;
-                    if (LONG) d.rest = g.rest;
                     d.hi = g.hi;
                     d.nw = g.nw;
                     d.ns = g.ns;
@@ -348,7 +346,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (LONG) __syncwarp();
                 ++seg_it;
 #pragma unroll 1
-                while (LONG && segs[(seg_it - 1) % kSegs].rest) {  // the segments behind it
+                while (LONG && segs[(seg_it - 1) % kSegs].flags & SPAN_MORE) {  // the segments behind it
                     ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
                     if (!ok) break;
                     if (lane == 0) {

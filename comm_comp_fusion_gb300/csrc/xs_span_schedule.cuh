@@ -294,14 +294,14 @@ struct SpanWalk {
 enum : int {
     SPAN_PIECE = 1,  // the part is not the whole item
     SPAN_ADD = 2,    // not the part's first segment
-    SPAN_MORE = 4    // nor its last
+    SPAN_MORE = 4,   // not its last: the steps behind it
+    SPAN_REST = 3    // are flags >> SPAN_REST
 };
-// What the roles need to know of a segment.
+// What the roles need to know of a segment (96 bytes: with 100, mixed paged batch 80.7 us instead of 80.3).
 struct SpanSeg {
     int n;            // steps; 0: no segment, the roles are done
     int j0;           // the item's step that it starts with
     int dual, flags;
-    int rest;         // the part's steps behind it
     int hi, nw, ns, s0, e1;
     int seq, head;
     int q0, tok0, ntok;  // the sequence's first packed row; the item's first token, their number
@@ -313,7 +313,7 @@ struct SpanSeg {
     // c0 < all_lo[t] and the tile's keys are not all sinks
     int all_hi[2], all_lo[2];
 };
-static_assert(sizeof(SpanSeg) == 100, "segment ring");
+static_assert(sizeof(SpanSeg) == 96, "segment ring");
 __device__ __forceinline__ int span_tile(const volatile SpanSeg &g, int y) {
     const int nw = g.nw;
     return y < nw ? g.hi - y : g.ns - 1 - (y - nw);
@@ -357,9 +357,10 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
     span_lengths<PAGED>(p, 0, w.q0, w.q_len, w.keys);
     span_skip(p, w, (int)blockIdx.x);
 }
-// The next part, as one segment.
+// The next part, as one segment; no steps and no flags if there is none.
 template <bool PAGED>
 __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
+    g.n = g.flags = 0;
     if ((PAGED || w.rounds == 0) && w.rem <= 0) return false;
     if (PAGED)
         while (w.q_len == 0) {
@@ -422,21 +423,20 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
 
 // Cuts what follows the first `stretch` steps off a part.
 __device__ __forceinline__ void span_cut(SpanSeg &g, int stretch) {
-    g.rest = max(g.n - stretch, 0);
-    g.n -= g.rest;
-    if (g.rest) g.flags |= SPAN_MORE;
+    const int rest = max(g.n - stretch, 0);
+    g.n -= rest;
+    if (rest) g.flags |= SPAN_MORE | rest << SPAN_REST;
 }
 // The segment d that follows segment o in its part.
 __device__ __forceinline__ void span_continue(volatile SpanSeg &d, const volatile SpanSeg &o, int stretch) {
 #pragma unroll 1
     for (int i = 0; i < (int)(sizeof(SpanSeg) / sizeof(int)); ++i)
         reinterpret_cast<volatile int *>(&d)[i] = reinterpret_cast<const volatile int *>(&o)[i];
-    const int rest = o.rest;
+    const int rest = o.flags >> SPAN_REST;
     d.j0 = o.j0 + o.n;
     d.n = min(rest, stretch);
-    d.rest = max(rest - stretch, 0);
     d.fix = -1;
-    d.flags = (o.flags & SPAN_PIECE) | SPAN_ADD | (rest > stretch ? SPAN_MORE : 0);
+    d.flags = (o.flags & SPAN_PIECE) | SPAN_ADD | (rest > stretch ? SPAN_MORE | (rest - stretch) << SPAN_REST : 0);
 }
 
 // Written by each CTA for span_merge_kernel: the item whose first piece is the

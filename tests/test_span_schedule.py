@@ -129,11 +129,13 @@ template <bool PAGED> static void call(SpanParams &p) {
             if (g.flags && g.j0 == 0) pieces = span_pieces_of(s[0], g);
             span_cut(g, p.stretch);
             for (bool more = true; more;) {
-                std::printf("s %u %d %d %d %d %d %d %d %d\n", c, g.seq, g.head, g.tok0, g.j0, g.n, g.nw + g.ns, g.flags, g.slot);
+                std::printf("s %u %d %d %d %d %d %d %d %d\n", c, g.seq, g.head, g.tok0, g.j0, g.n, g.nw + g.ns, g.flags & 7, g.slot);
                 const SpanSeg o = g;
-                if ((more = o.rest > 0)) span_continue(g, o, p.stretch);
+                if ((more = o.flags & SPAN_MORE)) span_continue(g, o, p.stretch);
             }
         }
+        span_cut(g, p.stretch);  // what ends the roles' loops
+        if (g.n || g.flags) std::printf("CTA %u does not end\n", c);
         if (pieces.pieces) std::printf("p %u %d %d %d %d %d\n", c, pieces.seq, pieces.head, pieces.tok0, pieces.pieces, pieces.slot);
     }
 }
