@@ -21,10 +21,12 @@ void span_workspace_parts(void *ws, int D, int num_sms, SpanParams *p) {
 cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int num_sms, cudaStream_t stream) {
     SpanParams q = p;
     // 2^18 keys: what a sum loses by truncation, about 2^-10, stays well below an output's rounding.
-    // Where no sequence can hold more, the instances without stretches (their code costs short
+    // Where no item can walk over more, the instances without stretches (their code costs short
     // items 1 to 3%: mixed paged batch 82.9 us, 80.4 without).
     constexpr int kStretch = 2048;
-    q.stretch = p.rec && (p.table ? (long long)p.max_pages * p.page : p.S) > 128 * kStretch ? kStretch : 0;
+    const long long held = p.table ? (long long)p.max_pages * p.page : p.S;
+    const long long window = (long long)p.left + p.right + p.item_tok + p.sinks + 3 * 128;  // and whole tiles at its ends
+    q.stretch = p.rec && std::min(held, window) > 128 * kStretch ? kStretch : 0;
     // The least part of a CTA: one step with few rows (4 sequences of 4 tokens over 1165 to 2941
     // keys, one key head: 15.6 us, 17.1 with two), two for other chunks (5 of 267 to 669
     // tokens over 996 keys: 20.9 us, 24.9 with four), four of whole sequences.

@@ -286,6 +286,25 @@ def test_paged_chunk_among_single_tokens(D, q_len, G, spare):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_len,kv_len,H,Hk,D", (([1, 1, 1], [700, 2900, 1], 8, 2, 128), ([6, 3, 0, 5], [400, 1300, 70, 5], 6, 2, 64),
+                                                 ([5, 5], [3000, 2000], 8, 2, 96), ([300, 1], [1900, 700], 4, 2, 96),
+                                                 ([140, 9], [3000, 3], 6, 2, 128), ([257, 600], [900, 1500], 4, 4, 64)))
+def test_paged_wide_tables(q_len, kv_len, H, Hk, D):
+    """A table that could hold more than 2^18 keys a sequence, around ordinary lengths, in every form, without and with a
+    window."""
+    import torch
+    b = Batch(q_len, kv_len, H, Hk, D, 32, spare=1, seed=D)
+    wide = torch.full((b.N, 9000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :b.max_pages] = b.table
+    b.table, b.max_pages = wide, 9000
+    for span in ((-1, 0, 0), (-1, -1, 0), (300, 0, 4)):
+        b.ws.fill_(255)
+        b.out.fill_(-1)
+        b.call(*span)
+        b.verify(*span, what=f"{span}")
+
+
+@pytest.mark.gpu
 def test_paged_graph_follows_lengths():
     """A captured call follows table, lengths and starts that change between replays; two captured calls take turns in
     one workspace."""
