@@ -870,7 +870,8 @@ __global__ void __launch_bounds__(512, 1)
                     if (y >= nw) c_end = INT_MIN;
                 }
                 // Rows whose keys end in an earlier tile than the first see none in it, so the
-                // maxima are taken over the first two steps.
+                // maxima are taken over the first two steps (mixed paged batch 80.6 us; over the first one
+                // 88.5; over three 80.6, and S = 1000 14.3 us instead of 14.2).
                 const int settled = steps - 2;
 #pragma unroll 1
                 for (; steps > 0; --steps) {
