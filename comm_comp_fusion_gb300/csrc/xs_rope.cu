@@ -21,7 +21,8 @@
 // of one token in registers while it walks heads of q and then of k, four at a
 // time (eight 16-byte loads in flight). Measured on one GB300: B = 2, S = 16384, H = 40,
 // D = 128 199 us, 6.75 TB/s (with one unit of a random row per step instead of a
-// thread's own token, 251 us); S = 4096, H = 24 to the head partition 21 us, 4.8 TB/s.
+// thread's own token, 251 us); S = 4096, H = 24 to the head partition 26 us with changing inputs,
+// 3.9 TB/s (21 replayed on buffers that stay in the L2).
 #include <algorithm>
 
 #include "xs_internal.h"

@@ -30,9 +30,10 @@
 //     turned round, S^T = K Q^T and O^T = V^T P^T, so that the 128 rows of an MMA
 //     are keys (or columns of V) and the query rows are its N. A softmax thread
 //     then holds one key's scores of all rows: 16 exponentials a step where the
-//     other form spends 128 on rows that mostly do not exist (four sequences of 300
-//     to 1200 keys: 12.6 us against 15.9; 8 of 4000 to 9000 keys, D = 96: 58
-//     against 66; 32 of 4000 to 32768, D = 128: 345 against 352).
+//     other form spends 128 on rows that mostly do not exist (16 single tokens of 8
+//     heads a key head over 4000 keys, D = 128: 48.3 us against 52.9, D = 64 32.9
+//     against 35.9; four over 1000 keys, 14 rows, 12.7 against 13.9; both sides of
+//     the choice at xs_attn_paged in xs_ops_api.cpp).
 //
 // Schedule. The steps (items x K/V tiles) of the whole call form one sequence,
 // ordered by sequence, head and query rows, and each CTA takes an equal,
@@ -60,8 +61,8 @@
 // of 32 tokens and more: 305 us, 6.9 TB/s; D = 64 and 96 reach 5.4; pages of 16 tokens
 // 5.9, their boxes' issue being the limit). Long chunks and windows: the chain S -
 // softmax - P V of a step, about 2850 cycles for two tiles at D = 128 (chunks of 2048
-// over 16K keys, 32 heads: 634 us, 1.69 PFLOP/s). Items of few steps (a two-sided window of
-// 512: 10): what lies between two items, about 6000 cycles of first loads, masked steps
+// over 16K keys, 32 heads: 638 us at best, 1.68 PFLOP/s, and 731 in a stream of calls, at the
+// power limit). Items of few steps (a two-sided window of 512: 10): what lies between two items, about 6000 cycles of first loads, masked steps
 // and cold code, and steps that few rows need whole. Short calls: about 8 us of
 // set-up, first loads and first steps, whose instructions are fetched cold.
 //
