@@ -358,7 +358,8 @@ def test_paged_pool_past_32_bits():
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H,Hk,D,keys", ((1, 152, 152, 64, 2 ** 23 - 77), (1, 190, 190, 128, 2 ** 21 + 5),
                                            (3, 304, 38, 96, 2 ** 22 + 1), (100, 170, 170, 64, 2 ** 21 - 9),
-                                           (256, 160, 160, 64, 2 ** 22 - 300), (200, 152, 152, 128, 2 ** 20 + 900)))
+                                           (256, 160, 160, 64, 2 ** 22 - 300), (200, 152, 152, 128, 2 ** 20 + 900),
+                                           (2, 2432, 19, 96, 2 ** 21 - 1)))
 def test_paged_very_many_keys(T, H, Hk, D, keys):
     """Millions of keys a sequence in every form, whole items and pieces: sums in tensor memory truncate, so they are taken
     in stretches. Values around 1, where that shows. Four pages stand for all, so a key's weight counts as often as it

@@ -291,6 +291,30 @@ def test_window_of_very_many_keys(S, H, span):
             check(got[i:i + 1, h], ref, bound + 2.0 ** -9 * np.abs(ref), f"row {i} head {h}")
 
 
+@pytest.mark.gpu
+def test_window_of_very_many_keys_scatters():
+    """The same with the All-to-All, whole items and pieces: bit for bit the permuted one."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    S, H, D, P = 2 ** 18 + 2048, 2, 64, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(P, 1, S, H // P, D, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    ws = guarded(xs.attn_window_workspace_size(1, S, H, D, P), torch.uint8, 0xFF)
+    head, fused, serial = (guarded(q.numel()) for _ in range(3))
+    xs.attn_window(q, k, v, head, 1, S, H, D, P, D ** -0.5, -1, -1, 0, ws)
+    xs.attn_window_a2a(q, k, v, fused, 1, S, H, D, P, D ** -0.5, -1, -1, 0, ws)
+    xs.a2a_permute(head, serial, 1, S, H, D, P)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    assert torch.equal(fused, serial)
+    got = head_to_tokens(from_dev(head).reshape(P, 1, S, H // P, D))
+    for i in (0, 130000, S - 1):
+        for h in range(H):
+            x = [y[h, 0, :, 0].double().cpu().numpy() for y in (q, k, v)]
+            ref, bound = attend(x[0][i:i + 1], x[1], x[2], np.ones((1, S), bool), D ** -0.5)
+            check(got[0, i:i + 1, h], ref, bound, f"row {i} head {h}")
+
+
 def test_window_without_workspace_takes_no_more_keys_than_it_can_add_up():
     import __graft_entry__
     __graft_entry__.build()
