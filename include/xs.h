@@ -324,8 +324,8 @@ xs_status xs_attn_trace_layout(int B, int S, int H, int D, int P, int *ctas, int
  * model keeps its keys and values in a paged cache. The common rules above hold
  * unless a call says otherwise. None of these calls synchronises, allocates or
  * keeps anything between calls, so each can be captured into a CUDA graph and
- * replayed (make one call of each kind on a device before the first capture:
- * it loads the kernels); calls or replays that may run at the same time must not
+ * replayed (make one call of each kind, of the same sizes, on a device before the
+ * first capture: it loads the kernels); calls or replays that may run at the same time must not
  * share a workspace or write the same memory.
  */
 
