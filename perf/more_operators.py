@@ -163,6 +163,7 @@ def prepare(case, seed):
     st = {"case": case, "T": T, "q_start": _starts(ql), "kv_len": torch.tensor(kl, dtype=torch.int32, device="cuda")}
     if op == "mask":
         rows = _packed_rows(_parents(ql, gen), ql)
+        st["kv_len"] += torch.randint(0, 1000, (N,), generator=gen, device="cuda", dtype=torch.int32)
         st["parents"] = torch.cat((rows, torch.zeros(case["spare"], dtype=torch.int32, device="cuda")))
         st["mask"] = torch.zeros((T, case["words"]), dtype=torch.int32, device="cuda")
         st["pos"] = torch.zeros(T, dtype=torch.int32, device="cuda")
@@ -491,7 +492,7 @@ def exact(case, seed):
     if case["op"] == "append":
         return _exact_append(case, st, ql, kl)
     if case["op"] == "mask":
-        return _exact_mask(case, st, ql, kl)
+        return _exact_mask(case, st, ql, st["kv_len"].tolist())
     G, scale, t = case["H"] // case["Hk"], case["D"] ** -0.5, 0
     out = st["out"].double()
     for n in range(case["N"]):
