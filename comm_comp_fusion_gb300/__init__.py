@@ -18,7 +18,9 @@ All-to-Alls fused); ``a2a_permute_inverse`` maps sequence- to head-partitioned.
 The operators around the attention: ``rope`` (rotary positions, ``RopeAxes``; either
 partition, or from the sequence to the head partition), ``attn_window`` and
 ``attn_window_a2a`` (sliding window with sinks), and for a paged cache
-``cache_append`` and ``attn_paged``:
+``cache_append``, ``cache_append_rope`` (rotary positions on the way), ``attn_paged``,
+``tree_mask`` and ``attn_tree`` (drafted token trees); ``attn_packed`` for whole prompts
+packed one after the other:
 
     k_pages, v_pages : pools [n_pages][page][Hk][D] bf16
     page_table       : [N][max_pages] int32; q_start [N + 1], kv_len [N] int32
@@ -51,7 +53,8 @@ EXPORTS = ("xs_attn_a2a", "xs_attn", "xs_a2a_permute", "xs_a2a_permute_inverse",
            "xs_attn_causal_a2a", "xs_attn_causal", "xs_attn_a2a_q8", "xs_attn_q8",
            "xs_attn_a2a_qkv8", "xs_attn_qkv8", "xs_attn_a2a_host", "xs_attn_host",
            "xs_rope", "xs_attn_window", "xs_attn_window_a2a", "xs_attn_window_workspace_size", "xs_cache_append",
-           "xs_attn_paged", "xs_attn_paged_workspace_size",
+           "xs_attn_paged", "xs_attn_paged_workspace_size", "xs_cache_append_rope", "xs_tree_mask", "xs_attn_tree",
+           "xs_attn_tree_workspace_size", "xs_attn_packed", "xs_attn_packed_workspace_size",
            # include/xs_burst.h
            "xs_burst_rec_bytes", "xs_burst_gap")
 
@@ -134,6 +137,19 @@ def _load() -> ctypes.CDLL:
     lib.xs_attn_paged.restype = i
     lib.xs_attn_paged_workspace_size.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
     lib.xs_attn_paged_workspace_size.restype = i
+    i64 = ctypes.c_int64
+    lib.xs_cache_append_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
+                                         i, ctypes.POINTER(i), ctypes.POINTER(ctypes.c_double), i, vp]
+    lib.xs_cache_append_rope.restype = i
+    lib.xs_tree_mask.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp]
+    lib.xs_tree_mask.restype = i
+    lib.xs_attn_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, f, vp, sz, vp]
+    lib.xs_attn_tree.restype = i
+    lib.xs_attn_packed.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i, i, i, i, i, f, i, i, i, vp, sz, vp]
+    lib.xs_attn_packed.restype = i
+    for fn in (lib.xs_attn_tree_workspace_size, lib.xs_attn_packed_workspace_size):
+        fn.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
+        fn.restype = i
     lib.xs_last_error.argtypes = []
     lib.xs_last_error.restype = ctypes.c_char_p
     lib.xs_device_status.argtypes = [vp, i]
@@ -459,6 +475,85 @@ def attn_paged_workspace_size(N, T, H, Hk, D) -> int:
     """``xs_attn_paged_workspace_size`` for the current device, in bytes."""
     n = ctypes.c_size_t(0)
     _check(lib.xs_attn_paged_workspace_size(N, T, H, Hk, D, ctypes.byref(n)))
+    return n.value
+
+
+def _rows(x, name, T, heads, D):
+    """The address of T rows of `heads` heads of D elements and the elements from one row to the next: a contiguous
+    tensor, or one of [T, heads * D] or [T, heads, D] whose rows lie further apart (a column range of a projection)."""
+    row = heads * D
+    if x is None or isinstance(x, int):
+        return x, row
+    if not x.is_contiguous() and x.dim() in (2, 3) and x.shape[0] >= T and (
+            (x.shape[1:] == (row,) and x.stride(1) == 1)
+            or (x.shape[1:] == (heads, D) and (x.stride(2) == 1 or D == 1) and (x.stride(1) == D or heads == 1))):
+        if T <= 1 or x.stride(0) >= row:
+            if x.dtype not in _BF16:
+                _bf16(x[:0], name, 0)
+            return x.data_ptr(), x.stride(0) if T > 1 else row
+    return _bf16(x, name, T * row), row
+
+
+def cache_append_rope(q, k, v, q_out, k_pages, v_pages, page_table, q_start, kv_len, N, T, H, Hk, D, page, n_pages,
+                      max_pages, axes, pos=None, k_out=None, stream=None, check=True):
+    """Turns the new tokens' q into ``q_out`` and writes their turned k and their v into their pages
+    (``xs_cache_append_rope``); ``axes`` is a ``RopeAxes``. q, k and v may be column ranges of one projection. ``pos``:
+    int32 [T][axes], by default the tokens' places in their sequences. ``k_out`` takes the turned keys in rows as well.
+    ``q`` and ``q_out`` may be None with H = 0."""
+    n, pool = len(axes.axis_dims), n_pages * page * Hk * D
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", T, H, D), _rows(k, "k", T, Hk, D), _rows(v, "v", T, Hk, D)
+    st = lib.xs_cache_append_rope(qp, kp, vp, qs, ks, vs, _bf16(q_out, "q_out", T * H * D), _bf16(k_out, "k_out", T * Hk * D),
+                                  _bf16(k_pages, "k_pages", pool), _bf16(v_pages, "v_pages", pool),
+                                  _int32(page_table, "page_table", N * max_pages), _int32(q_start, "q_start", N + 1),
+                                  _int32(kv_len, "kv_len", N), _int32(pos, "pos", T * n), N, T, H, Hk, D, page, n_pages,
+                                  max_pages, n, axes._dims, axes._freqs, XS_ROPE_HALVES if axes.halves else 0,
+                                  _stream(stream, k, k_pages))
+    return _check(st) if check else st
+
+
+def tree_mask(parents, q_start, kv_len, mask, pos, N, T, words, stream=None, check=True):
+    """Masks [T][words] and positions [T] of drafted trees from their tokens' parents (``xs_tree_mask``); ``pos`` may be
+    None."""
+    st = lib.xs_tree_mask(_int32(parents, "parents", T), _int32(q_start, "q_start", N + 1), _int32(kv_len, "kv_len", N),
+                          _int32(mask, "mask", T * words), _int32(pos, "pos", T), N, T, words, _stream(stream, parents, mask))
+    return _check(st) if check else st
+
+
+def attn_tree(q, k_pages, v_pages, page_table, q_start, kv_len, mask, out, N, T, H, Hk, D, page, n_pages, max_pages, words,
+              scale, workspace=None, workspace_bytes=None, stream=None, check=True):
+    """Attention of drafted token trees over a paged cache (``xs_attn_tree``); ``mask``: int32 [T][words], as from
+    ``tree_mask``. The workspace is required."""
+    rows, pool = T * H * D, n_pages * page * Hk * D
+    st = lib.xs_attn_tree(_bf16(q, "q", rows), _bf16(k_pages, "k_pages", pool), _bf16(v_pages, "v_pages", pool),
+                          _int32(page_table, "page_table", N * max_pages), _int32(q_start, "q_start", N + 1),
+                          _int32(kv_len, "kv_len", N), _int32(mask, "mask", T * words), _bf16(out, "out", rows), N, T, H, Hk,
+                          D, page, n_pages, max_pages, words, float(scale), _workspace(workspace),
+                          _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
+    return _check(st) if check else st
+
+
+def attn_tree_workspace_size(N, T, H, Hk, D) -> int:
+    """``xs_attn_tree_workspace_size`` for the current device, in bytes."""
+    n = ctypes.c_size_t(0)
+    _check(lib.xs_attn_tree_workspace_size(N, T, H, Hk, D, ctypes.byref(n)))
+    return n.value
+
+
+def attn_packed(q, k, v, q_start, out, N, T, H, Hk, D, scale, left=-1, right=0, sinks=0, workspace=None,
+                workspace_bytes=None, stream=None, check=True):
+    """Attention over whole prompts packed one after the other (``xs_attn_packed``); q, k and v may be column ranges of one
+    projection. The workspace is required."""
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", T, H, D), _rows(k, "k", T, Hk, D), _rows(v, "v", T, Hk, D)
+    st = lib.xs_attn_packed(qp, kp, vp, qs, ks, vs, _int32(q_start, "q_start", N + 1), _bf16(out, "out", T * H * D), N, T, H,
+                            Hk, D, float(scale), left, right, sinks, _workspace(workspace),
+                            _nbytes(workspace, workspace_bytes), _stream(stream, q, out))
+    return _check(st) if check else st
+
+
+def attn_packed_workspace_size(N, T, H, Hk, D) -> int:
+    """``xs_attn_packed_workspace_size`` for the current device, in bytes."""
+    n = ctypes.c_size_t(0)
+    _check(lib.xs_attn_packed_workspace_size(N, T, H, Hk, D, ctypes.byref(n)))
     return n.value
 
 

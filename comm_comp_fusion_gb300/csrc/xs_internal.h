@@ -166,6 +166,41 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 
+// The append with rotary positions on the way (heads of at most 128 elements).
+struct AppendRopeParams {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_out, *k_pages, *v_pages;  // k_out NULL: keys go into the pages alone
+    const int *table, *q_start, *kv_len;
+    const int *pos;                               // [T][n_axes]; NULL: a token's place in its sequence
+    int64_t q_stride, k_stride, v_stride;         // elements from one token's row to the next
+    int N, T, H, Hk, page, n_pages, max_pages;
+    int n_axes, n_pairs;
+    int tile;                                     // tokens per block
+    uint64_t frac[kRopeMaxPairs / 2];             // as in RopeParams
+    uint8_t axis[kRopeMaxPairs / 2];
+    uint8_t unit_first[kRopeMaxUnits / 2], unit_half[kRopeMaxUnits / 2];
+};
+cudaError_t launch_append_rope(AppendRopeParams &p, int D, bool halves, int num_sms, cudaStream_t stream);
+
+// ------------------------------------------------------------ drafted trees
+constexpr int kTreeMaxWords = 8;  // 32-bit words of a token's mask
+struct TreeMaskParams {
+    const int *parents, *q_start, *kv_len;
+    int *mask, *pos;  // pos NULL: not wanted (kv_len is not read)
+    int N, T, words;
+};
+cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
+
+struct RowsParams {
+    const uint16_t *q, *k, *v;
+    uint16_t *out;
+    const int *table, *q_start, *kv_len, *mask;  // table NULL: packed prompts
+    int64_t q_stride, k_stride, v_stride;
+    int N, T, H, Hk, page, n_pages, max_pages, words, left, right, sinks;
+    float scale_log2;
+};
+cudaError_t launch_rows(const RowsParams &p, int D, cudaStream_t stream);
+
 // ------------------------------------------------------------ window and paged attention
 struct SpanPieces;
 struct SpanParams {

@@ -6,77 +6,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstring>
 
 #include "xs_internal.h"
+#include "xs_ops_checks.h"
 
 namespace {
 
 using namespace xs;
-
-bool misaligned16(const void *p) { return ((uintptr_t)p & 15u) != 0; }
-bool misaligned4(const void *p) { return ((uintptr_t)p & 3u) != 0; }
-
-struct Buffer {
-    const void *ptr;
-    size_t bytes;
-    const char *name;
-};
-
-// No buffer of `out` may overlap one of `in` or another of `out`.
-int check_disjoint(const Buffer *out, int n_out, const Buffer *in, int n_in) {
-    for (int i = 0; i < n_out; ++i) {
-        for (int j = 0; j < n_in; ++j)
-            if (api_overlaps(out[i].ptr, out[i].bytes, in[j].ptr, in[j].bytes))
-                return api_fail(XS_ERR_ALIAS, "%s overlaps %s", out[i].name, in[j].name);
-        for (int j = 0; j < i; ++j)
-            if (api_overlaps(out[i].ptr, out[i].bytes, out[j].ptr, out[j].bytes))
-                return api_fail(XS_ERR_ALIAS, "%s overlaps %s", out[i].name, out[j].name);
-    }
-    return 0;
-}
-int check_device(const Buffer *b, int n, int dev) {
-    for (int i = 0; i < n; ++i)
-        if (b[i].bytes)
-            if (const int st = api_device_pointer(b[i].ptr, dev, b[i].name)) return st;
-    return 0;
-}
-
-// f (radians per unit of place) in turns, modulo 1, as a 64-bit binary fraction
-// (two's complement for a negative f). |f| / 2 pi is formed in double-double
-// arithmetic (1 / 2 pi in two doubles), so the fraction is as exact as f.
-uint64_t turns_fraction(double f) {
-    const double hi_c = 0.15915494309189535, lo_c = -9.839338337591243e-18;  // 1 / 2 pi
-    const double x = std::fabs(f), hi = x * hi_c, lo = std::fma(x, hi_c, -hi) + x * lo_c;
-    const double frac = hi - std::floor(hi);  // exact, below 1
-    const uint64_t u = (uint64_t)std::ldexp(frac, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
-    return f < 0 ? 0 - u : u;
-}
-
-int span_limits(int left, int right, int sinks, SpanParams *p) {
-    if (left < -1 || right < -1) return api_fail(XS_ERR_SHAPE, "left and right must be >= 0, or -1 for no limit");
-    if (sinks < 0) return api_fail(XS_ERR_SHAPE, "sinks must be >= 0");
-    const int far = 1 << 29;  // past every place
-    p->left = left < 0 || left > far ? far : left;
-    p->right = right < 0 || right > far ? far : right;
-    p->sinks = sinks > far ? far : sinks;
-    return 0;
-}
-int check_scale(float scale) {
-    if (!std::isfinite(scale) || !(scale > 0.0f)) return api_fail(XS_ERR_SHAPE, "scale must be positive and finite");
-    return 0;
-}
-int check_workspace(const void *ws, size_t bytes, const Buffer *others, int n) {
-    if (!ws && bytes) return api_fail(XS_ERR_WORKSPACE, "workspace is NULL but workspace_bytes is %zu", bytes);
-    if (!ws) return 0;
-    if (((uintptr_t)ws & 255u) != 0) return api_fail(XS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    for (int i = 0; i < n; ++i)
-        if (api_overlaps(ws, bytes, others[i].ptr, others[i].bytes))
-            return api_fail(XS_ERR_WORKSPACE, "workspace overlaps %s", others[i].name);
-    return 0;
-}
-float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634073599246810019); }
 
 // Most K/V tiles of a query tile pair without a workspace: 2^20 keys, after which a sum in
 // tensor memory, whose additions truncate, has lost about half a bf16 step. (With a workspace it is
@@ -172,34 +109,6 @@ int window_call(const void *q, const void *k, const void *v, void *out, int B, i
     return e == cudaSuccess ? (int)XS_OK : api_cuda_error("windowed attention launch", e);
 }
 
-// Shape rules of the paged cache; the sizes of one pool and of the table in bytes.
-int check_cache(int N, int T, int Hk, int D, int page, int n_pages, int max_pages, size_t *pool, size_t *table) {
-    if (N < 0 || T < 0) return api_fail(XS_ERR_SHAPE, "N and T must be >= 0 (got N=%d T=%d)", N, T);
-    if (Hk < 1 || n_pages < 1 || max_pages < 1)
-        return api_fail(XS_ERR_SHAPE, "Hk, n_pages and max_pages must be >= 1 (got %d, %d, %d)", Hk, n_pages, max_pages);
-    if (D != 64 && D != 96 && D != 128)
-        return api_fail(XS_ERR_UNSUPPORTED, "the paged cache takes D = 64, 96 or 128 (got D=%d)", D);
-    if (page < 16 || page > 1024 || (page & (page - 1)))
-        return api_fail(XS_ERR_UNSUPPORTED, "page=%d is not a power of two from 16 to 1024", page);
-    if ((long long)max_pages * page > (1ll << 29))
-        return api_fail(XS_ERR_SHAPE, "max_pages * page = %lld exceeds 2^29 keys", (long long)max_pages * page);
-    const unsigned long long rows = (unsigned long long)n_pages * page;
-    if (Hk > (1 << 16) || rows * (unsigned long long)Hk * D * 2 >= (1ull << 40))
-        return api_fail(XS_ERR_SHAPE, "a pool of %d pages exceeds 2^40 bytes", n_pages);
-    if (T > (1 << 29)) return api_fail(XS_ERR_SHAPE, "T=%d exceeds 2^29 rows", T);
-    if (N > (1 << 16)) return api_fail(XS_ERR_SHAPE, "N=%d exceeds 65536 sequences", N);
-    *pool = (size_t)rows * Hk * D * 2;
-    *table = (size_t)N * max_pages * sizeof(int);
-    return 0;
-}
-// The query heads of the attention over it.
-int check_heads(int T, int H, int Hk) {
-    if (H < 1 || H % Hk) return api_fail(XS_ERR_SHAPE, "H=%d is not a positive multiple of Hk=%d", H, Hk);
-    if (H / Hk > 128) return api_fail(XS_ERR_UNSUPPORTED, "H/Hk=%d query heads a key head exceed 128", H / Hk);
-    if ((long long)T * H >= (1ll << 31)) return api_fail(XS_ERR_SHAPE, "T * H exceeds 2^31-1 rows");
-    return 0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -216,8 +125,6 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
     if (!st && Hk > 0) st = api_shape(B, S, Hk, D, P, &kb);
     if (st) return (xs_status)st;
     if (H + Hk > (1 << 16)) return (xs_status)api_fail(XS_ERR_SHAPE, "H + Hk = %d exceeds 65536 heads", H + Hk);
-    if (n_axes < 1 || n_axes > kRopeMaxAxes)
-        return (xs_status)api_fail(XS_ERR_SHAPE, "n_axes must be 1 to %d (got %d)", kRopeMaxAxes, n_axes);
     if (pos_batches != 1 && pos_batches != B)
         return (xs_status)api_fail(XS_ERR_SHAPE, "pos_batches must be 1 or B (got %d)", pos_batches);
     if (flags & ~(XS_ROPE_HALVES | XS_ROPE_INVERSE | XS_ROPE_IN_SEQ | XS_ROPE_OUT_SEQ))
@@ -225,32 +132,7 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
     const bool halves = flags & XS_ROPE_HALVES;
     RopeParams p;
     memset(&p, 0, sizeof p);
-    int rot = 0;
-    for (int a = 0; a < n_axes; ++a) {
-        const int d = axis_dims[a];
-        if (d < 2 || d > D || d % 2)
-            return (xs_status)api_fail(XS_ERR_SHAPE, "axis_dims[%d]=%d is not an even number from 2 to D", a, d);
-        if (halves && d % 16)
-            return (xs_status)api_fail(XS_ERR_UNSUPPORTED,
-                                       "pairs half an axis apart need axis_dims in multiples of 16 (axis_dims[%d]=%d)", a, d);
-        if (rot + d > D) return (xs_status)api_fail(XS_ERR_SHAPE, "axis_dims add up to more than D=%d", D);
-        for (int j = 0; j < d / 2; ++j) p.axis[rot / 2 + j] = (uint8_t)a;
-        for (int u = 0; halves && u < d / 16; ++u) {
-            p.unit_first[rot / 16 + u] = (uint8_t)(rot + 8 * u);
-            p.unit_half[rot / 16 + u] = (uint8_t)(d / 2);
-        }
-        rot += d;
-    }
-    for (int j = 0; j < rot / 2; ++j) {
-        if (!std::isfinite(freqs[j]) || std::fabs(freqs[j]) > 1e6)
-            return (xs_status)api_fail(XS_ERR_SHAPE, "freqs[%d] is not finite or beyond 1e6", j);
-        p.frac[j] = turns_fraction(freqs[j]);
-    }
-    p.n_pairs = rot / 2;
-    for (int u = rot / 16; halves && u < D / 16; ++u) {  // copied
-        p.unit_first[u] = (uint8_t)(16 * u);
-        p.unit_half[u] = 8;
-    }
+    if ((st = rope_table(n_axes, axis_dims, freqs, halves, D, &p))) return (xs_status)st;
     p.seq_in = flags & XS_ROPE_IN_SEQ;
     p.seq_out = flags & XS_ROPE_OUT_SEQ;
     p.inverse = flags & XS_ROPE_INVERSE;
@@ -283,7 +165,6 @@ xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const 
     p.Hkl = Hk / P;
     p.Sl = S / P;
     p.D = D;
-    p.n_axes = n_axes;
     const cudaError_t e = launch_rope(p, halves, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : (xs_status)api_cuda_error("rotary launch", e);
 }

@@ -26,43 +26,11 @@
 #include <algorithm>
 
 #include "xs_internal.h"
-#include "xs_ptx.cuh"
+#include "xs_rope.cuh"
 
 namespace xs {
 
 constexpr int kRopeUnroll = 4;
-
-__device__ __forceinline__ uint4 rope_load(const uint16_t *ptr) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(ptr));
-    return v;
-}
-
-// Turns the pair (a, b); fp32 throughout, rounded to bf16 once by the caller.
-__device__ __forceinline__ void rope_turn(float &a, float &b, float2 cs) {
-    const float x = a * cs.x - b * cs.y;
-    b = fmaf(a, cs.y, b * cs.x);
-    a = x;
-}
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-
-// Neighbouring pairs: one word holds a pair.
-__device__ __forceinline__ uint32_t turn_word(uint32_t w, float2 cs) {
-    float a = lo_f(w), b = hi_f(w);
-    rope_turn(a, b, cs);
-    return pack_bf16x2(a, b);
-}
-// Pairs half an axis apart: two words hold two pairs.
-__device__ __forceinline__ void turn_words(uint32_t &u, uint32_t &v, float2 c0, float2 c1) {
-    float a0 = lo_f(u), a1 = hi_f(u), b0 = lo_f(v), b1 = hi_f(v);
-    rope_turn(a0, b0, c0);
-    rope_turn(a1, b1, c1);
-    u = pack_bf16x2(a0, a1);
-    v = pack_bf16x2(b0, b1);
-}
 
 // The rows of one token in a tensor of nh heads: heads in order, `hop` elements
 // apart, with a jump of `jump` more after every nhl (head partition: the next rank's
@@ -111,11 +79,7 @@ __global__ void __launch_bounds__(D == 96 ? 192 : 256) rope_kernel(const __grid_
     auto sines = [&](int i) {
         const int t = i / (D / 2), j = i - t * (D / 2);
         if (j >= p.n_pairs) return;
-        const uint64_t phase = (uint64_t)(int64_t)pos[t * p.n_axes + p.axis[j]] * p.frac[j];
-        const int turns = (int)(uint32_t)((phase + 0x80000000ull) >> 32);  // nearest multiple of 2^-32 turns
-        float sn, cn;
-        sincospif((float)turns * 0x1p-31f, &sn, &cn);
-        cs_tab[i] = make_float2(cn, p.inverse ? -sn : sn);
+        cs_tab[i] = rope_sines(pos[t * p.n_axes + p.axis[j]], p.frac[j], p.inverse);
     };
     const int n = nt * (D / 2);
     if (p.tile > 8) {  // several a thread: their places are fetched together
@@ -157,23 +121,7 @@ __global__ void __launch_bounds__(D == 96 ? 192 : 256) rope_kernel(const __grid_
 #pragma unroll
             for (int u = 0; u < kRopeUnroll; ++u)
                 if (h + u * lanes < nh) {
-                    if (HALVES) {
-                        if (pairs > 0) {
-                            turn_words(x[u].x, y[u].x, cs[0], cs[1]);
-                            turn_words(x[u].y, y[u].y, cs[2], cs[3]);
-                            turn_words(x[u].z, y[u].z, cs[4], cs[5]);
-                            turn_words(x[u].w, y[u].w, cs[6], cs[7]);
-                        }
-                    } else {
-                        if (pairs > 0) x[u].x = turn_word(x[u].x, cs[0]);
-                        if (pairs > 1) x[u].y = turn_word(x[u].y, cs[1]);
-                        if (pairs > 2) x[u].z = turn_word(x[u].z, cs[2]);
-                        if (pairs > 3) x[u].w = turn_word(x[u].w, cs[3]);
-                        if (pairs > 4) y[u].x = turn_word(y[u].x, cs[4]);
-                        if (pairs > 5) y[u].y = turn_word(y[u].y, cs[5]);
-                        if (pairs > 6) y[u].z = turn_word(y[u].z, cs[6]);
-                        if (pairs > 7) y[u].w = turn_word(y[u].w, cs[7]);
-                    }
+                    rope_unit<HALVES>(x[u], y[u], cs, pairs);
                     *reinterpret_cast<uint4 *>(dst + out.at + c0) = x[u];
                     *reinterpret_cast<uint4 *>(dst + out.at + c1) = y[u];
                     rope_advance(out, lanes, nhl);

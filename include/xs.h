@@ -460,6 +460,99 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
                         void *workspace, size_t workspace_bytes, void *stream);
 xs_status xs_attn_paged_workspace_size(int N, int T, int H, int Hk, int D, size_t *bytes);
 
+/*
+ * The append with rotary positions on the way: of the new tokens, q is turned into
+ * q_out, k is turned and written into its pages, v is written into its pages, in one
+ * pass. It equals xs_rope of q and k followed by xs_cache_append, to the bit.
+ *   q, k, v : rows of T tokens with H, Hk and Hk heads of D elements; a token's heads
+ *            lie one after the other, and one token's row begins q_stride (k_stride,
+ *            v_stride) elements behind the one before, so that q, k and v may be
+ *            columns of one [T][(H + 2 Hk) D] projection. 0: H * D (Hk * D), rows
+ *            without a gap. A stride is a multiple of 8, at least a row, at most 2^30.
+ *   q_out  : [T][H][D] bf16. H = 0: no queries, q and q_out are ignored.
+ *   k_out  : [T][Hk][D] bf16, the turned keys once more in packed rows (for
+ *            xs_attn_packed); NULL: not wanted.
+ *   pos    : device, [T][n_axes] int32, a token's place on each axis (any 32-bit
+ *            value), as the trees of xs_tree_mask need; NULL, with one axis: its
+ *            place in its sequence, kv_len[n] - new tokens + i.
+ *   axis_dims, freqs, flags : as for xs_rope; of the flags XS_ROPE_HALVES alone.
+ * Rows of no sequence are left as they are in q_out and k_out. A token whose place
+ * lies before its sequence or whose page outside the pool is turned in q_out and k_out
+ * and written into no page. q_out may be q, and k_out k, when their rows have no
+ * gap; any other overlap of an output with another buffer is XS_ERR_ALIAS.
+ * Extra rules: H + Hk <= 65536, T * max(H, Hk) < 2^31.
+ */
+xs_status xs_cache_append_rope(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, void *q_out, void *k_out, void *k_pages, void *v_pages,
+                               const int32_t *page_table, const int32_t *q_start, const int32_t *kv_len,
+                               const int32_t *pos, int N, int T, int H, int Hk, int D, int page, int n_pages,
+                               int max_pages, int n_axes, const int *axis_dims, const double *freqs, int flags,
+                               void *stream);
+
+/*
+ * Drafted token trees. The new tokens of a sequence may be a tree: each follows
+ * the sequence's last token or another new token before it in the rows. All of them
+ * are appended to the cache, one place each in the rows' order, and verified by one
+ * attention call in which a token sees the context and the tokens that it follows.
+ *
+ * xs_tree_mask makes a tree's masks and positions from its tokens' parents, once for
+ * all layers of a step:
+ *   parents : device [T] int32, the parent's place among the sequence's new tokens;
+ *            -1, or anything else that is not an earlier token of the sequence: the
+ *            token follows the context.
+ *   mask   : device [T][words] int32, overwritten: bit j % 32 of word j / 32 of row i
+ *            is set iff j = i or token i follows token j, directly or not.
+ *   pos    : device [T] int32, overwritten: the context's length (kv_len[n] - new
+ *            tokens) plus the token's depth, 0 for those that follow the context; NULL:
+ *            not wanted, and kv_len is not read (and may be NULL).
+ *   q_start, kv_len, N, T : as below xs_cache_append.
+ *   words  : 1 to 8. The first 32 * words new tokens of a sequence form its tree. Rows
+ *            behind those get an empty mask and the context's length as position.
+ * Rows of no sequence are left as they are. A branch of d tokens costs d steps of
+ * about 30 ns.
+ */
+xs_status xs_tree_mask(const int32_t *parents, const int32_t *q_start, const int32_t *kv_len, int32_t *mask, int32_t *pos,
+                       int N, int T, int words, void *stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their own keys too) under
+ * masks of bits. With c = kv_len[n] - new tokens, token i of sequence n sees the keys
+ * 0 .. c - 1, and key c + j iff bit j % 32 of word j / 32 of its row of mask is set;
+ * bits of places at or past kv_len[n] are not looked at, and keys from c + 32 * words
+ * on are not seen. The masks may be any, those of xs_tree_mask or not.
+ *   mask   : device [T][words] int32, words 1 to 8.
+ *   everything else: as for xs_attn_paged, without limits to the left. Keys and
+ *            values of the new tokens must be finite, seen or not.
+ *   workspace, workspace_bytes : as there, of xs_attn_tree_workspace_size bytes.
+ */
+xs_status xs_attn_tree(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,
+                       const int32_t *q_start, const int32_t *kv_len, const int32_t *mask, void *out, int N, int T, int H,
+                       int Hk, int D, int page, int n_pages, int max_pages, int words, float scale, void *workspace,
+                       size_t workspace_bytes, void *stream);
+xs_status xs_attn_tree_workspace_size(int N, int T, int H, int Hk, int D, size_t *bytes);
+
+/*
+ * Attention over whole prompts of different lengths, packed one after the other.
+ * Sequence n is the rows q_start[n] .. q_start[n + 1] - 1 of q, k, v and out, and its
+ * token i sees its token j under the rule of xs_attn_window; (-1, 0, 0) is causal,
+ * (-1, -1, 0) sees everything.
+ *   q, k, v : rows of T tokens with H, Hk and Hk heads of D elements and the strides of
+ *            xs_cache_append_rope; query head h reads key head h / (H / Hk).
+ *   out    : [T][H][D] bf16. Rows of no sequence are left as they are.
+ *   q_start, N, T : as below xs_cache_append; read by the kernels, so a captured call
+ *            follows it when it changes between replays.
+ *   workspace, workspace_bytes : required (unless the call is empty), as for
+ *            xs_attn_window, of xs_attn_packed_workspace_size bytes.
+ * k and v of a sequence's rows must be finite; rows of no sequence may hold anything,
+ * and what one sequence holds touches no other. Rows of q that are not finite, and
+ * rounding: as for xs_attn_window. H % Hk == 0 and H / Hk <= 128; N <= 65536;
+ * T <= 2^29, T * H < 2^31; D = 64, 96 or 128.
+ */
+xs_status xs_attn_packed(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         const int32_t *q_start, void *out, int N, int T, int H, int Hk, int D, float scale, int left,
+                         int right, int sinks, void *workspace, size_t workspace_bytes, void *stream);
+xs_status xs_attn_packed_workspace_size(int N, int T, int H, int Hk, int D, size_t *bytes);
+
 /* Human-readable description of the last non-OK status returned on this host
  * thread (empty string if none). The pointer stays valid until the next call
  * on this thread. */
