@@ -24,7 +24,8 @@ ROOT = os.path.dirname(PKG)
 
 SOURCES = ["xs_attn_d128.cu", "xs_attn_f8.cu", "xs_attn_d256.cu", "xs_attn_d96.cu", "xs_attn_d64.cu", "xs_attn.cu", "xs_permute.cu", "xs_api.cpp", "xs_schedule.cpp",
            "xs_noalloc.cu", "xs_burst.cu", "xs_rope.cu", "xs_cache.cu", "xs_span.cu", "xs_span_d128.cu", "xs_span_d96.cu",
-           "xs_span_d64.cu", "xs_ops_api.cpp", "xs_append_rope.cu", "xs_tree.cu", "xs_rows.cu", "xs_serve_api.cpp"]
+           "xs_span_d64.cu", "xs_ops_api.cpp", "xs_append_rope.cu", "xs_tree.cu", "xs_serve_api.cpp",
+           "xs_span_serve_d128.cu", "xs_span_serve_d96.cu", "xs_span_serve_d64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

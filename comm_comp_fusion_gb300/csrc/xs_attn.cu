@@ -87,7 +87,9 @@ cudaError_t read_device_error(unsigned int *value, bool clear, cudaStream_t stre
     cudaError_t (*const per_d[])(unsigned int *, bool) = {read_error_word_d64, read_error_word_d96,
                                                           read_error_word_d128, read_error_word_d256,
                                                           read_error_word_f8, read_error_word_span_d64,
-                                                          read_error_word_span_d96, read_error_word_span_d128};
+                                                          read_error_word_span_d96, read_error_word_span_d128,
+                                                          read_error_word_span_serve_d64, read_error_word_span_serve_d96,
+                                                          read_error_word_span_serve_d128};
     for (auto fn : per_d) {
         if ((e = fn(&w, clear)) != cudaSuccess) return e;
         all |= w;

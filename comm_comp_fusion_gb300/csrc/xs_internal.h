@@ -191,21 +191,17 @@ struct TreeMaskParams {
 };
 cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
 
-struct RowsParams {
-    const uint16_t *q, *k, *v;
-    uint16_t *out;
-    const int *table, *q_start, *kv_len, *mask;  // table NULL: packed prompts
-    int64_t q_stride, k_stride, v_stride;
-    int N, T, H, Hk, page, n_pages, max_pages, words, left, right, sinks;
-    float scale_log2;
-};
-cudaError_t launch_rows(const RowsParams &p, int D, cudaStream_t stream);
-
 // ------------------------------------------------------------ window and paged attention
 struct SpanPieces;
+// What a span call works on: whole sequences of equal lengths, head-partitioned; new tokens over a paged
+// cache; whole sequences packed one after the other; new tokens over a paged cache under masks of bits.
+enum SpanKind : int { SPAN_WHOLE = 0, SPAN_PAGED = 1, SPAN_PACKED = 2, SPAN_TREE = 3 };
 struct SpanParams {
     uint16_t *out;
-    const int *table, *q_start, *kv_len;  // table NULL: whole sequences, head-partitioned
+    int kind;                             // a SpanKind
+    const int *table, *q_start, *kv_len;  // SPAN_PACKED: no table and no kv_len (and page = 128)
+    const int *mask;                      // SPAN_TREE: [T][words]
+    int words;
     int N, T, H, Hk, G;         // whole sequences: T = B * S rows of H heads
     int page, page_log2, n_pages, max_pages;
     int B, S, P, Hl, Sl, head_out;  // whole sequences only
@@ -237,6 +233,13 @@ cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int nu
 XS_DECLARE_SPAN_ENTRY(64)
 XS_DECLARE_SPAN_ENTRY(96)
 XS_DECLARE_SPAN_ENTRY(128)
+// SPAN_PACKED and SPAN_TREE (xs_span_serve_d*.cu)
+#define XS_DECLARE_SPAN_SERVE_ENTRY(D)                                                                           \
+    cudaError_t launch_span_serve_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream); \
+    cudaError_t read_error_word_span_serve_d##D(unsigned int *value, bool clear);
+XS_DECLARE_SPAN_SERVE_ENTRY(64)
+XS_DECLARE_SPAN_SERVE_ENTRY(96)
+XS_DECLARE_SPAN_SERVE_ENTRY(128)
 
 // ------------------------------------------------------------ host helpers of the C ABI (xs_api.cpp)
 // Each records the thread's last error and returns a status (0: fine).

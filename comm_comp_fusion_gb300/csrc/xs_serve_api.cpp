@@ -176,26 +176,20 @@ xs_status xs_attn_tree(const void *q, const void *k_pages, const void *v_pages, 
     if ((st = api_device(&dev, &sms)) || (st = check_device(all, 8, dev)) ||
         (st = check_workspace_size(workspace, workspace_bytes, span_workspace_bytes(D, sms), dev)))
         return (xs_status)st;
-    RowsParams p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint16_t *>(k_pages);
-    p.v = static_cast<const uint16_t *>(v_pages);
+    SpanParams p{};
+    if ((st = span_limits(-1, -1, 0, &p))) return (xs_status)st;
+    p.kind = SPAN_TREE;
     p.out = static_cast<uint16_t *>(out);
     p.table = page_table;
     p.q_start = q_start;
     p.kv_len = kv_len;
     p.mask = mask;
-    p.q_stride = (int64_t)H * D;
-    p.N = N;
-    p.T = T;
-    p.H = H;
-    p.Hk = Hk;
-    p.page = page;
-    p.n_pages = n_pages;
-    p.max_pages = max_pages;
     p.words = words;
     p.scale_log2 = scale_log2(scale);
-    const cudaError_t e = launch_rows(p, D, static_cast<cudaStream_t>(stream));
+    span_workspace_parts(workspace, D, sms, &p);
+    SpanMaps maps;
+    if ((st = span_paged(q, k_pages, v_pages, N, T, H, Hk, D, page, n_pages, max_pages, &p, &maps))) return (xs_status)st;
+    const cudaError_t e = launch_span(D, maps, p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : (xs_status)api_cuda_error("tree attention launch", e);
 }
 
@@ -209,8 +203,8 @@ xs_status xs_attn_packed(const void *q, const void *k, const void *v, int64_t q_
     if (!q || !k || !v || !q_start || !out) return (xs_status)api_fail(XS_ERR_NULL, "q, k, v, q_start and out must be non-NULL");
     int st = check_packed(N, T, H, Hk, D);
     if (st || (st = check_scale(scale))) return (xs_status)st;
-    SpanParams sp{};
-    if ((st = span_limits(left, right, sinks, &sp))) return (xs_status)st;
+    SpanParams p{};
+    if ((st = span_limits(left, right, sinks, &p))) return (xs_status)st;
     size_t qb, kb, vb;
     if ((st = check_rows("q", T, H, D, &q_stride, &qb)) || (st = check_rows("k", T, Hk, D, &k_stride, &kb)) ||
         (st = check_rows("v", T, Hk, D, &v_stride, &vb)))
@@ -229,24 +223,35 @@ xs_status xs_attn_packed(const void *q, const void *k, const void *v, int64_t q_
     if ((st = api_device(&dev, &sms)) || (st = check_device(all, 5, dev)) ||
         (st = check_workspace_size(workspace, workspace_bytes, span_workspace_bytes(D, sms), dev)))
         return (xs_status)st;
-    RowsParams p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint16_t *>(k);
-    p.v = static_cast<const uint16_t *>(v);
+    p.kind = SPAN_PACKED;
     p.out = static_cast<uint16_t *>(out);
     p.q_start = q_start;
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
     p.N = N;
     p.T = T;
     p.H = H;
     p.Hk = Hk;
-    p.left = sp.left;
-    p.right = sp.right;
-    p.sinks = sp.sinks;
+    p.G = H / Hk;
+    p.page = 128;  // K/V tiles come in one box
     p.scale_log2 = scale_log2(scale);
-    const cudaError_t e = launch_rows(p, D, static_cast<cudaStream_t>(stream));
+    p.tile_tok = 128 / p.G;
+    p.item_tok = 2 * p.tile_tok;
+    p.g_magic = (65536u + (uint32_t)p.G - 1u) / (uint32_t)p.G;
+    p.heads = Hk;
+    span_workspace_parts(workspace, D, sms, &p);
+    SpanMaps maps;
+    const uint64_t d = (uint64_t)D * 2;
+    const uint64_t q_dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)Hk, (uint64_t)T};
+    const uint64_t q_strides[3] = {d, p.G * d, (uint64_t)q_stride * 2};
+    const uint32_t q_box[4] = {64, (uint32_t)p.G, 1, (uint32_t)p.tile_tok};
+    const uint64_t kv_dims[4] = {(uint64_t)D, (uint64_t)Hk, (uint64_t)T, 1};
+    const uint64_t k_strides[3] = {d, (uint64_t)k_stride * 2, (uint64_t)k_stride * 2};  // (the last dimension has one place)
+    const uint64_t v_strides[3] = {d, (uint64_t)v_stride * 2, (uint64_t)v_stride * 2};
+    const uint32_t kv_box[4] = {64, 1, 128, 1};
+    if ((st = api_tile_map(&maps.q, q, q_dims, q_strides, q_box, "q")) ||
+        (st = api_tile_map(&maps.k, k, kv_dims, k_strides, kv_box, "k")) ||
+        (st = api_tile_map(&maps.v, v, kv_dims, v_strides, kv_box, "v")))
+        return (xs_status)st;
+    const cudaError_t e = launch_span(D, maps, p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : (xs_status)api_cuda_error("packed attention launch", e);
 }
 

@@ -1,9 +1,11 @@
 // xs_span_kernel.cuh -- attention over a span of keys per token on the tensor
-// cores: a sliding window with sinks over whole sequences (xs_attn_window), and
-// chunks of new tokens over a paged cache (xs_attn_paged, PAGED).
+// cores: a sliding window with sinks over whole sequences of equal lengths
+// (xs_attn_window), or packed ones (xs_attn_packed), chunks of new tokens over a paged
+// cache (xs_attn_paged), drafted trees over it (xs_attn_tree). KIND, a SpanKind, says which.
 //
 // Mathematics. The token at place i sees the key at place j iff
 //   j <= i + right  and  (j >= i - left  or  j < sinks),
+// (a tree's token: iff j lies before the sequence's new tokens, or its mask has the bit of j),
 // and o = sum_j p_j v_j / sum_j p_j, p_j = 2^(s_j scale log2(e) - m) over the keys
 // it sees; a token that sees none gets zeros. S = Q K^T and P V run on tcgen05
 // with fp32 accumulators in tensor memory; row maxima, sums and O stay in fp32;
@@ -76,8 +78,8 @@
 //   warp 2      tensor-memory allocator, then the schedule: it walks the CTA's part
 //               and describes each stretch of an item (SpanSeg) in a ring in shared
 //               memory, ahead of the other roles
-//   warp 3      (PAGED) zeroes the V rows behind the last key, which no one has
-//               written: a weight of 0 times NaN would still be NaN
+//   warp 3      (paged, packed) zeroes the V rows behind the last key, which no one has
+//               written or which are another sequence's: a weight of 0 times NaN would still be NaN
 //   warps 4-11  softmax, one warpgroup per tile or chain, one thread per row
 //   warps 12-15 epilogue
 #pragma once
@@ -144,13 +146,13 @@ enum : int {
 enum SpanSite : uint32_t { kSiteFix = 13, kSiteSeg = 14 };
 
 // FEW: query rows of a tile in the few-rows form; 0: tiles of 128 rows.
-template <int D, bool PAGED, int FEW> struct SpanCfg {
+template <int D, int KIND, int FEW> struct SpanCfg {
     // Registers a thread of warps 0-3, of the softmax warps and of the epilogue's. One split for
     // both calls with 128-row tiles costs 2-3% of one of them (56 / 176 / 104: two-sided window
     // S = 4096 65.1 us, mixed paged batch 83.0; 48 / 184 / 96: 66.3 and 80.6); few rows have few scores.
-    static constexpr int kRegsOther = FEW ? 80 : PAGED ? 48 : 56;
-    static constexpr int kRegsSoftmax = FEW ? 160 : PAGED ? 184 : 176;
-    static constexpr int kRegsEpilogue = FEW ? 112 : PAGED ? 96 : 104;
+    static constexpr int kRegsOther = FEW ? 80 : KIND ? 48 : 56;
+    static constexpr int kRegsSoftmax = FEW ? 160 : KIND ? 184 : 176;
+    static constexpr int kRegsEpilogue = FEW ? 112 : KIND ? 96 : 104;
     static_assert(kRegsOther + 2 * kRegsSoftmax + kRegsEpilogue == 4 * 128, "the registers the block is launched with");
     static constexpr int kNDB = Cfg<D>::kNDB;
     static constexpr uint32_t kBlk = Cfg<D>::kBlk, kTile = Cfg<D>::kTile;
@@ -191,15 +193,15 @@ constexpr float kSpanRise = 16384.0f;  // see the softmax
 constexpr int kMidSteps = 4;           // see the issuer
 
 // row / G of a query tile's row
-template <bool PAGED> __device__ __forceinline__ int span_row_tok(const SpanParams &p, int row) {
-    return PAGED ? (int)((uint32_t)row * p.g_magic >> 16) : row;
+template <int KIND> __device__ __forceinline__ int span_row_tok(const SpanParams &p, int row) {
+    return KIND ? (int)((uint32_t)row * p.g_magic >> 16) : row;
 }
 
 // Element offset of the output row of token `tok` (of the sequence's new tokens,
 // packed rows from q0) and query head g of the group.
-template <int D, bool PAGED>
+template <int D, int KIND>
 __device__ __forceinline__ int64_t span_out_offset(const SpanParams &p, int head, int64_t q0, int tok, int g) {
-    if (PAGED) return ((q0 + tok) * p.H + (int64_t)head * p.G + g) * D;
+    if (KIND) return ((q0 + tok) * p.H + (int64_t)head * p.G + g) * D;
     const int hl = head % p.Hl, rb = head / p.Hl;
     if (p.head_out) return (((int64_t)rb * p.S + tok) * p.Hl + hl) * D;
     const int b = rb % p.B, r = rb / p.B;
@@ -219,11 +221,32 @@ __device__ __forceinline__ uint32_t span_mask_word(int a, int b, int s, int col0
     return le & (ge | lt);
 }
 
-template <int D, bool PAGED, int FEW, bool LONG>
+// Word w of a tree token's mask, for places counted from the sequence's first new token: those before it
+// are seen, those behind the mask are not.
+__device__ __forceinline__ uint32_t span_tree_word(const int *mask, int words, int w) {
+    return w < 0 ? ~0u : w < words ? (uint32_t)mask[w] : 0u;
+}
+// Few rows: the rows of the item (bits) that see the key at place `key`.
+template <int FEW> __device__ __forceinline__ uint32_t span_tree_rows(const SpanParams &p, const volatile SpanSeg &g, int key) {
+    const int at = key - (g.pos0 - g.tok0), ntok = g.ntok;
+    if (key >= g.keys) return 0u;
+    if (at < 0) return ~0u;
+    if (at >= 32 * p.words) return 0u;
+    const int *mask = p.mask + ((int64_t)g.q0 + g.tok0) * p.words + (at >> 5);
+    const uint32_t group = p.G < 32 ? (1u << p.G) - 1u : ~0u;
+    uint32_t rows = 0;
+#pragma unroll 4
+    for (int i = 0; i < ntok; ++i)
+        if (((uint32_t)mask[(int64_t)i * p.words] >> (at & 31)) & 1u) rows |= group << (i * p.G);
+    return rows;
+}
+
+template <int D, int KIND, int FEW, bool LONG>
 __global__ void __launch_bounds__(512, 1)
     span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
-    using C = SpanCfg<D, PAGED, FEW>;
+    using C = SpanCfg<D, KIND, FEW>;
     using R = Rec<D>;
+    constexpr bool kPages = KIND == SPAN_PAGED || KIND == SPAN_TREE;  // K and V lie in pages
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -259,7 +282,7 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(BAR(SPFIX_DONE), 1);
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(SEG_FULL(s), 1);
-            mbar_init(SEG_EMPTY(s), PAGED ? 15 : 14);  // producer, issuer, (V clearing,) 8 softmax warps, 4 epilogue warps
+            mbar_init(SEG_EMPTY(s), KIND ? 15 : 14);  // producer, issuer, (V clearing,) 8 softmax warps, 4 epilogue warps
         }
         misc[1] = 0u;
         fence_mbar_init();
@@ -271,16 +294,16 @@ __global__ void __launch_bounds__(512, 1)
         tmem_alloc(smem_u32(misc), C::kTmemCols);
         tmem_relinquish();
     }
-    const int chunks = ((PAGED ? p.N : p.n_pairs) + 31) / 32;
+    const int chunks = ((KIND ? p.N : p.n_pairs) + 31) / 32;
     long long *sums = reinterpret_cast<long long *>(sm + C::kOffKV);  // the ring is not in use yet
     SpanSched *sched = reinterpret_cast<SpanSched *>(sm + C::kOffSeg + (uint32_t)sizeof(SpanSeg) * kSegs);
-    if (PAGED || p.rec) {
+    if (KIND || p.rec) {
         if (chunks > 1) {
-            span_chunk_sums<PAGED>(p, chunks, sums);
+            span_chunk_sums<KIND>(p, chunks, sums);
             __syncthreads();
         }
         if (warp == 3) {  // here, not by warp 2 in its role: with 48 registers it takes twice as long
-            const SpanSched s = span_schedule<PAGED>(p, chunks, sums, lane);
+            const SpanSched s = span_schedule<KIND>(p, chunks, sums, lane);
             if (lane == 0) *sched = s;
         }
         if (chunks > 1) fence_proxy_async_smem();  // before TMA writes there
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
     const int wg = warp >> 2;
-    if (PAGED || p.rec) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // span_merge_kernel may be set up
+    if (KIND || p.rec) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // span_merge_kernel may be set up
     // The roles walk the ring of segments alike.
     uint32_t seg_it = 0;
 #define SEG (segs[seg_it % kSegs])
@@ -308,10 +331,10 @@ __global__ void __launch_bounds__(512, 1)
             // ---------------------------------------------------------- schedule
             SpanPieces pieces{};
             SpanWalk w;
-            span_walk_init<PAGED>(p, *sched, w);
+            span_walk_init<KIND>(p, *sched, w);
             for (bool more = true; more;) {
                 SpanSeg g;
-                more = span_next<PAGED>(p, *sched, w, g);
+                more = span_next<KIND>(p, *sched, w, g);
                 if (more && g.flags && g.j0 == 0) pieces = span_pieces_of(*sched, g);  // its first piece: this CTA's last part
                 if (LONG) span_cut(g, p.stretch);
                 bool ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
@@ -359,12 +382,12 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (!ok) break;
             }
-            if ((PAGED || p.rec) && lane == 0) p.pieces[blockIdx.x] = pieces;
+            if ((KIND || p.rec) && lane == 0) p.pieces[blockIdx.x] = pieces;
         } else if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0;
             bool ok = true;
-            const int box = PAGED ? min(p.page, 128) : 128;  // rows of a box
+            const int box = KIND ? min(p.page, 128) : 128;  // rows of a box
             while (ok) {
                 ok = SEG_WAIT(span_warp_bwait);
                 volatile SpanSeg &g = SEG;
@@ -373,9 +396,9 @@ __global__ void __launch_bounds__(512, 1)
                 const bool dual = g.dual;
                 // page of this lane's box of step x's tile; n_pages (outside the pool)
                 // where no token of the item sees any of its keys
-                const int *table = PAGED ? p.table + (int64_t)g.seq * p.max_pages : nullptr;
+                const int *table = kPages ? p.table + (int64_t)g.seq * p.max_pages : nullptr;
                 auto page_of = [&](int x) -> int {
-                    if (!PAGED || lane * box >= 128 || x >= n) return 0;
+                    if (!kPages || lane * box >= 128 || x >= n) return 0;
                     const int k0 = span_tile(g, j0 + x) * 128 + lane * box;
                     if (k0 > g.last || (k0 + box <= g.lo && k0 >= p.sinks)) return p.n_pages;
                     const int id = table[k0 >> p.page_log2];
@@ -389,7 +412,7 @@ __global__ void __launch_bounds__(512, 1)
                     if (lane == 0) mbar_arrive_expect_tx(BAR(SPKV_FULL + slot), C::kTile);
                     __syncwarp();
                     const int tile = span_tile(g, j0 + x);
-                    if (PAGED) {
+                    if (kPages) {
                         if (lane * box < 128) {
                             const int row = (tile * 128 + lane * box) & (p.page - 1);
                             const uint32_t dst = sKV + slot * C::kTile + (uint32_t)(lane * box) * 128u;
@@ -397,6 +420,10 @@ __global__ void __launch_bounds__(512, 1)
                             for (int db = 0; db < C::kNDB; ++db)
                                 tma_load_4d(dst + db * C::kBlk, m, BAR(SPKV_FULL + slot), db * 64, head, row, page);
                         }
+                    } else if (KIND == SPAN_PACKED) {  // rows of the next sequence, or zeros, behind this one's last
+                        if (lane < C::kNDB)
+                            tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(SPKV_FULL + slot), lane * 64, head,
+                                        g.q0 + tile * 128, 0);
                     } else if (lane < C::kNDB) {
                         tma_load_4d(sKV + slot * C::kTile + lane * C::kBlk, m, BAR(SPKV_FULL + slot), lane * 64,
                                     head % p.Hl, tile * 128, head / p.Hl);
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                         for (int db = 0; db < C::kNDB; ++db) {
                             const uint32_t dst = sQ + t * C::kQTile + db * C::kQBlk;
-                            if (PAGED)
+                            if (KIND)
                                 tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, 0, head, tok);
                             else
                                 tma_load_4d(dst, &tm.q, BAR(SPQ_FULL + t), db * 64, head % p.Hl, tok, head / p.Hl);
@@ -440,7 +467,7 @@ __global__ void __launch_bounds__(512, 1)
                 while (globaltimer_ns() - t0 < 200000ull) {
                 }
             }
-        } else if (PAGED && warp == 3) {
+        } else if (KIND && warp == 3) {
             // ------------------------------------ V rows behind the last key: zeros
             uint32_t kv_it = 0, fph = 0;
             const int box = min(p.page, 128);
@@ -531,7 +558,7 @@ __global__ void __launch_bounds__(512, 1)
                 volatile SpanSeg &g = SEG;
                 const int n = g.n;
                 if (!ok || n == 0) break;
-                const bool fix = PAGED && g.fix >= 0;
+                const bool fix = KIND && g.fix >= 0;
                 uint32_t ks, vs;
                 const int qb = FEW ? (int)(seg_it & 1u) : 0;  // the tile that holds Q (dual)
                 ok = span_bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
@@ -718,6 +745,8 @@ __global__ void __launch_bounds__(512, 1)
                         c += g.ns - c_end;
                         c_end = INT_MIN;
                     }
+                    uint32_t by_row = ~0u;  // a tree's rows that see this thread's key; fetched before the scores are in
+                    if (KIND == SPAN_TREE && masked) by_row = span_tree_rows<FEW>(p, g, c0 + kl);
                     ok = span_warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                     if (!ok) break;
                     sph ^= 1u;
@@ -728,7 +757,10 @@ __global__ void __launch_bounds__(512, 1)
                         tmem_ld16(tS, s);
                     else
                         tmem_ld32(tS, s);
-                    if (masked) {
+                    if (KIND == SPAN_TREE && masked) {
+#pragma unroll
+                        for (int r = 0; r < FEW; ++r) s[r] = (by_row >> r) & 1u ? s[r] : f2u(-INFINITY);
+                    } else if (masked) {
                         // the key is seen by tokens key - right .. key + left (a sink: by all from there
                         // on), so by rows r0 <= r < r1 of the item
                         const int key = c0 + kl, at = key - g.pos0;
@@ -883,6 +915,14 @@ __global__ void __launch_bounds__(512, 1)
                         c += g.ns - c_end;
                         c_end = INT_MIN;
                     }
+                    uint32_t bits_at[5] = {};  // a tree's words of this row for the tile; fetched before the scores are in
+                    if (KIND == SPAN_TREE && masked && !idle) {
+                        const int tok = min((g.dual ? 0 : t * p.tile_tok) + span_row_tok<KIND>(p, row), g.ntok - 1);
+                        const int *m_row = p.mask + ((int64_t)g.q0 + g.tok0 + tok) * p.words;
+                        const int w0 = (c0 - (g.pos0 - g.tok0)) >> 5;  // (rounded down)
+#pragma unroll
+                        for (int i = 0; i < 5; ++i) bits_at[i] = span_tree_word(m_row, p.words, w0 + i);
+                    }
                     ok = span_warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                     if (!ok) break;
                     sph ^= 1u;
@@ -901,11 +941,19 @@ __global__ void __launch_bounds__(512, 1)
                         // that have to be fetched anew for the one or two tiles of an item with an
                         // edge in them.
                         // Places of this row's token and of the last key it may see:
-                        const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<PAGED>(p, row);
+                        const int pos = g.pos0 + (g.dual ? 0 : t * p.tile_tok) + span_row_tok<KIND>(p, row);
                         const int row_hi = min(pos + p.right, g.keys - 1);
 #pragma unroll 1
                         for (int h = 0; h < 128; h += 32) {
-                            const uint32_t bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, h);
+                            uint32_t bits;
+                            if (KIND == SPAN_TREE) {
+                                bits = __funnelshift_r(bits_at[0], bits_at[1], c0 - (g.pos0 - g.tok0)) &
+                                       span_mask_word(INT_MIN / 2, g.keys - 1 - c0, 0, h);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) bits_at[i] = bits_at[i + 1];
+                            } else {
+                                bits = span_mask_word(pos - p.left - c0, row_hi - c0, p.sinks - c0, h);
+                            }
                             if (__all_sync(0xffffffffu, bits == ~0u)) continue;
                             if (__any_sync(0xffffffffu, bits)) {
                                 uint32_t s[32];
@@ -1049,8 +1097,8 @@ __global__ void __launch_bounds__(512, 1)
             float *rec = p.rec + (size_t)(several() ? 2 * gridDim.x + blockIdx.x : g.slot) * R::kFloats;
             auto row_dst = [&](int t, int rows) -> int64_t {
                 if (row >= rows) return -1;
-                const int r = span_row_tok<PAGED>(p, row);
-                return span_out_offset<D, PAGED>(p, g.head, g.q0, g.tok0 + t * p.tile_tok + r, PAGED ? row - r * p.G : 0);
+                const int r = span_row_tok<KIND>(p, row);
+                return span_out_offset<D, KIND>(p, g.head, g.q0, g.tok0 + t * p.tile_tok + r, KIND ? row - r * p.G : 0);
             };
             auto release_o = [&](int t) {  // O_t fully read: the next item may overwrite it
                 tc_fence_before();
@@ -1137,8 +1185,8 @@ __global__ void __launch_bounds__(512, 1)
                             rec[R::kML + 128 + r] = l;
                         }
                     } else {
-                        const int tk = span_row_tok<PAGED>(p, r);
-                        p.out[span_out_offset<D, PAGED>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
+                        const int tk = span_row_tok<KIND>(p, r);
+                        p.out[span_out_offset<D, KIND>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
                             (uint16_t)pack_bf16x2(l > 0.f ? f * (1.0f / l) : 0.f, 0.f);
                     }
                 }
@@ -1164,8 +1212,8 @@ __global__ void __launch_bounds__(512, 1)
                                 part[R::kML + 128 + r] = l;
                             }
                         } else {
-                            const int tk = span_row_tok<PAGED>(p, r);
-                            p.out[span_out_offset<D, PAGED>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
+                            const int tk = span_row_tok<KIND>(p, r);
+                            p.out[span_out_offset<D, KIND>(p, head, q_row, tok0 + tk, r - tk * p.G) + row] =
                                 (uint16_t)pack_bf16x2(l > 0.f ? f * (1.0f / l) : 0.f, 0.f);
                         }
                     }
@@ -1301,7 +1349,7 @@ __global__ void __launch_bounds__(512, 1)
 // memory and stored whole: 10 us for 152 items of 256 rows in two pieces, D = 128,
 // against 17 with 8 bytes of a row at a time. With few rows the records hold whole
 // rows, and a thread takes 4 columns of one.
-template <int D, bool PAGED, int FEW>
+template <int D, int KIND, int FEW>
 __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__ SpanParams p) {
     using R = Rec<D>;
     constexpr int kPer = FEW ? 1 : D / 32, U = FEW ? 8 : 2;
@@ -1357,8 +1405,8 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     auto row_at = [&](int row) -> uint16_t * {
-        const int tk = span_row_tok<PAGED>(p, row);
-        return p.out + span_out_offset<D, PAGED>(p, s.head, s.q0, s.tok0 + t * p.tile_tok + tk, PAGED ? row - tk * p.G : 0);
+        const int tk = span_row_tok<KIND>(p, row);
+        return p.out + span_out_offset<D, KIND>(p, s.head, s.q0, s.tok0 + t * p.tile_tok + tk, KIND ? row - tk * p.G : 0);
     };
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -1378,28 +1426,28 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     }
 }
 
-template <int D, bool PAGED, int FEW, bool LONG>
+template <int D, int KIND, int FEW, bool LONG>
 static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
-    auto kern = span_attn_kernel<D, PAGED, FEW, LONG>;
+    auto kern = span_attn_kernel<D, KIND, FEW, LONG>;
     static std::atomic<uint64_t> configured{0};  // devices where the shared-memory limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
     if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, PAGED, FEW>::kSmemAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, KIND, FEW>::kSmemAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    kern<<<grid, 512, SpanCfg<D, PAGED, FEW>::kSmemAlloc, stream>>>(maps, p);
+    kern<<<grid, 512, SpanCfg<D, KIND, FEW>::kSmemAlloc, stream>>>(maps, p);
     e = cudaGetLastError();
     if (e == cudaErrorInvalidValue || e == cudaErrorLaunchOutOfResources) {
         // the limit was lost (for instance by a device reset): set it again once
         configured.fetch_and(~bit, std::memory_order_acq_rel);
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, PAGED, FEW>::kSmemAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SpanCfg<D, KIND, FEW>::kSmemAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
-        kern<<<grid, 512, SpanCfg<D, PAGED, FEW>::kSmemAlloc, stream>>>(maps, p);
+        kern<<<grid, 512, SpanCfg<D, KIND, FEW>::kSmemAlloc, stream>>>(maps, p);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
@@ -1414,26 +1462,19 @@ static cudaError_t launch_span_one(const SpanMaps &maps, const SpanParams &p, in
         cfg.stream = stream;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, span_merge_kernel<D, PAGED, FEW>, p);
+        e = cudaLaunchKernelEx(&cfg, span_merge_kernel<D, KIND, FEW>, p);
     }
     return e;
 }
 
-template <int D, bool PAGED, int FEW>
+template <int D, int KIND, int FEW>
 static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {
-    return p.stretch ? launch_span_one<D, PAGED, FEW, true>(maps, p, grid, stream)
-                     : launch_span_one<D, PAGED, FEW, false>(maps, p, grid, stream);
+    return p.stretch ? launch_span_one<D, KIND, FEW, true>(maps, p, grid, stream)
+                     : launch_span_one<D, KIND, FEW, false>(maps, p, grid, stream);
 }
 
-#define XS_DEFINE_SPAN_ENTRY(D)                                                                                       \
-    cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
-        if (!p.table) return launch_span_form<D, false, 0>(maps, p, grid, stream);                                    \
-        if (p.few == 16) return launch_span_form<D, true, 16>(maps, p, grid, stream);                                 \
-        if constexpr (D > 64)                                                                                         \
-            if (p.few == 32) return launch_span_form<D, true, 32>(maps, p, grid, stream);                             \
-        return launch_span_form<D, true, 0>(maps, p, grid, stream);                                                   \
-    }                                                                                                                 \
-    cudaError_t read_error_word_span_d##D(unsigned int *value, bool clear) {                                          \
+#define XS_DEFINE_SPAN_ERROR_WORD(NAME)                                                                               \
+    cudaError_t NAME(unsigned int *value, bool clear) {                                          \
         cudaError_t e = cudaMemcpyFromSymbol(value, g_xs_error, sizeof(unsigned int));                                \
         if (e == cudaSuccess && clear && *value) {                                                                    \
             const unsigned int zero = 0;                                                                              \
@@ -1441,5 +1482,25 @@ static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, i
         }                                                                                                             \
         return e;                                                                                                     \
     }
+
+#define XS_DEFINE_SPAN_ENTRY(D)                                                                                       \
+    cudaError_t launch_span_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {          \
+        if (p.kind == SPAN_WHOLE) return launch_span_form<D, SPAN_WHOLE, 0>(maps, p, grid, stream);                   \
+        if (p.few == 16) return launch_span_form<D, SPAN_PAGED, 16>(maps, p, grid, stream);                           \
+        if constexpr (D > 64)                                                                                         \
+            if (p.few == 32) return launch_span_form<D, SPAN_PAGED, 32>(maps, p, grid, stream);                       \
+        return launch_span_form<D, SPAN_PAGED, 0>(maps, p, grid, stream);                                             \
+    }                                                                                                                 \
+    XS_DEFINE_SPAN_ERROR_WORD(read_error_word_span_d##D)
+
+#define XS_DEFINE_SPAN_SERVE_ENTRY(D)                                                                                 \
+    cudaError_t launch_span_serve_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {    \
+        if (p.kind == SPAN_PACKED) return launch_span_form<D, SPAN_PACKED, 0>(maps, p, grid, stream);                 \
+        if (p.few == 16) return launch_span_form<D, SPAN_TREE, 16>(maps, p, grid, stream);                            \
+        if constexpr (D > 64)                                                                                         \
+            if (p.few == 32) return launch_span_form<D, SPAN_TREE, 32>(maps, p, grid, stream);                        \
+        return launch_span_form<D, SPAN_TREE, 0>(maps, p, grid, stream);                                              \
+    }                                                                                                                 \
+    XS_DEFINE_SPAN_ERROR_WORD(read_error_word_span_serve_d##D)
 
 }  // namespace xs

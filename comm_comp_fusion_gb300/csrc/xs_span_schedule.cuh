@@ -64,15 +64,20 @@ __device__ __forceinline__ SpanItem span_item(const SpanParams &p, int q_len, in
 }
 
 // New tokens and keys of a sequence, cut to what the packed rows and the table hold.
-template <bool PAGED>
+// (KIND: a SpanKind.)
+template <int KIND>
 __device__ __forceinline__ void span_lengths(const SpanParams &p, int seq, int &q0, int &q_len, int &keys) {
-    if (!PAGED) {
+    if (!KIND) {
         q0 = 0;
         q_len = keys = p.S;
         return;
     }
     q0 = min(max(p.q_start[seq], 0), p.T);
     q_len = max(0, min(max(p.q_start[seq + 1], 0), p.T) - q0);
+    if (KIND == SPAN_PACKED) {
+        keys = q_len;
+        return;
+    }
     keys = min(max(p.kv_len[seq], 0), p.max_pages * p.page);
 }
 
@@ -89,12 +94,12 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 // Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
 // is a sequence (all its heads and query rows) or, for whole sequences, which
 // are all alike, a query tile pair of one head.
-template <bool PAGED>
+template <int KIND>
 __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane) {
     const int g = ch * 32 + lane;
-    if (!PAGED) return g < p.n_pairs ? (long long)span_item(p, p.S, p.S, g).n : 0ll;
+    if (!KIND) return g < p.n_pairs ? (long long)span_item(p, p.S, p.S, g).n : 0ll;
     int q0 = 0, q_len = 0, keys = 0;
-    if (g < p.N) span_lengths<true>(p, g, q0, q_len, keys);
+    if (g < p.N) span_lengths<KIND>(p, g, q0, q_len, keys);
     const int pairs = span_pairs(p, q_len);
     long long u = pairs == 1 ? (long long)span_item(p, q_len, keys, 0).n * p.heads : 0ll;
     uint32_t todo = __ballot_sync(0xffffffffu, pairs > 1);  // these the whole warp sums up, one after the other
@@ -142,7 +147,7 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
 // are the call's from step `before` on. `sum`: the steps of one head (whole
 // sequences). `mine`: the steps of this lane's group in the only chunk, when there
 // is one; otherwise the chunks' sums are in `sums`.
-template <typename T, bool PAGED>
+template <typename T, int KIND>
 __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T before, long long sum, long long mine,
                                           int chunks, const long long *sums, int lane) {
     const int c = (int)blockIdx.x;
@@ -154,7 +159,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     s.rem = (long long)(span_first<T>(q, r, s.ctas, c + 1) - u0);
     if (s.rem == 0) return;
     T u = before + u0, base = 0, at = 0;
-    if (!PAGED) {
+    if (!KIND) {
         s.head = (int)(u / (T)sum);
         u -= (T)s.head * (T)sum;
     }
@@ -165,18 +170,18 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
             l = span_locate<T>(ch + lane < chunks ? (T)sums[ch + lane] : (T)0, u, base, at, lane);
         ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
         base = at;
-        mine = span_group_steps<PAGED>(p, ch, lane);
+        mine = span_group_steps<KIND>(p, ch, lane);
     }
     l = span_locate<T>((T)mine, u, base, at, lane);
     u -= at;
-    if (!PAGED) {
+    if (!KIND) {
         s.pair = ch * 32 + l;
         s.j = (int)u;
         return;
     }
     s.seq = ch * 32 + l;
     int q0, q_len, keys;
-    span_lengths<true>(p, s.seq, q0, q_len, keys);
+    span_lengths<KIND>(p, s.seq, q0, q_len, keys);
     const int np = span_pairs(p, q_len);
     if (np == 1) {
         const T n = (T)span_item(p, q_len, keys, 0).n;
@@ -231,45 +236,45 @@ __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long l
 
 // Sums of the steps of 32 groups each, when there are more; by all threads, and
 // followed by a barrier.
-template <bool PAGED> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
+template <int KIND> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int ch = warp; ch < chunks; ch += (int)(blockDim.x >> 5)) {
-        const long long s = warp_sum(span_group_steps<PAGED>(p, ch, lane));
+        const long long s = warp_sum(span_group_steps<KIND>(p, ch, lane));
         if (lane == 0) sums[ch] = s;
     }
 }
 
 // The call's steps, how many CTAs share them and where this CTA's part starts; by one warp.
-template <bool PAGED>
+template <int KIND>
 __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chunks, const long long *sums, int lane) {
     long long mine = 0, sum = 0;
     if (chunks > 1) {
 #pragma unroll 1
         for (int ch = lane; ch < chunks; ch += 32) sum += sums[ch];
     } else {
-        sum = mine = span_group_steps<PAGED>(p, 0, lane);
+        sum = mine = span_group_steps<KIND>(p, 0, lane);
     }
     sum = warp_sum(sum);
-    const long long total = PAGED ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
+    const long long total = KIND ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
     // parts of a few steps or more, or a CTA for each key head of the sequences
-    const long long least = PAGED ? min(total, (long long)p.N * p.heads) : 0ll;
+    const long long least = KIND ? min(total, (long long)p.N * p.heads) : 0ll;
     s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> p.min_steps_log2, least)));
     s.rem = s.q = 0;
     s.r = 0;
     s.rounds = s.seq = s.head = s.pair = s.j = 0;
     long long before = 0;
-    if (!PAGED && s.ctas == (int)gridDim.x) s.rounds = span_rounds(p, s.ctas, sum, lane, before);
+    if (!KIND && s.ctas == (int)gridDim.x) s.rounds = span_rounds(p, s.ctas, sum, lane, before);
     s.shared = total - before;
     // Every CTA that shares them has a step: a part without one between two pieces of an item would
     // have written no record for the merge.
     if (s.shared > 0 && s.shared < s.ctas) s.ctas = (int)s.shared;
     if ((int)blockIdx.x < s.ctas && s.shared > 0) {
         if (total < (1ll << 31))
-            span_find<uint32_t, PAGED>(p, s, (uint32_t)before, sum, mine, chunks, sums, lane);
+            span_find<uint32_t, KIND>(p, s, (uint32_t)before, sum, mine, chunks, sums, lane);
         else
-            span_find<unsigned long long, PAGED>(p, s, (unsigned long long)before, sum, mine, chunks, sums, lane);
+            span_find<unsigned long long, KIND>(p, s, (unsigned long long)before, sum, mine, chunks, sums, lane);
     }
     return s;
 }
@@ -325,21 +330,21 @@ __device__ __forceinline__ void span_skip(const SpanParams &p, SpanWalk &w, int 
     w.pair = at - heads * p.n_pairs;
 }
 // The walk's start in the shared steps.
-template <bool PAGED>
+template <int KIND>
 __device__ __forceinline__ void span_walk_shared(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
     w.rem = s.rem;
     w.seq = s.seq;
     w.head = s.head;
     w.pair = s.pair;
     w.j = s.j;
-    if (w.rem > 0) span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
+    if (w.rem > 0) span_lengths<KIND>(p, w.seq, w.q0, w.q_len, w.keys);
 }
-template <bool PAGED>
+template <int KIND>
 __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
     w.first = true;
     w.rounds = 0;
-    if (PAGED) {
-        span_walk_shared<PAGED>(p, s, w);
+    if (KIND) {
+        span_walk_shared<KIND>(p, s, w);
         return;
     }
     if (p.rec) {
@@ -349,23 +354,23 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
         w.rounds = (int)((items - blockIdx.x + gridDim.x - 1) / gridDim.x);
     }
     if (w.rounds == 0) {
-        span_walk_shared<PAGED>(p, s, w);
+        span_walk_shared<KIND>(p, s, w);
         return;
     }
     w.rem = 0;
     w.seq = w.head = w.pair = w.j = 0;
-    span_lengths<PAGED>(p, 0, w.q0, w.q_len, w.keys);
+    span_lengths<KIND>(p, 0, w.q0, w.q_len, w.keys);
     span_skip(p, w, (int)blockIdx.x);
 }
 // The next part, as one segment; no steps and no flags if there is none.
-template <bool PAGED>
+template <int KIND>
 __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
     g.n = g.flags = 0;
-    if ((PAGED || w.rounds == 0) && w.rem <= 0) return false;
-    if (PAGED)
+    if ((KIND || w.rounds == 0) && w.rem <= 0) return false;
+    if (KIND)
         while (w.q_len == 0) {
             if (++w.seq >= p.N) return false;
-            span_lengths<PAGED>(p, w.seq, w.q0, w.q_len, w.keys);
+            span_lengths<KIND>(p, w.seq, w.q0, w.q_len, w.keys);
         }
     const SpanItem it = span_item(p, w.q_len, w.keys, w.pair);
     const int w_keys = w.keys;
@@ -385,13 +390,13 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
     g.lo = max(0, it.pos0 - p.left);
     g.last = min(w.keys - 1, it.pos0 + it.ntok - 1 + p.right);
     g.slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
-    if (!PAGED && w.rounds > 0) {
+    if (!KIND && w.rounds > 0) {
         g.j0 = 0;
         g.n = it.n;
         if (--w.rounds > 0)
             span_skip(p, w, (int)gridDim.x);
         else if (p.rec)
-            span_walk_shared<PAGED>(p, sched, w);
+            span_walk_shared<KIND>(p, sched, w);
     } else {
         w.first = false;
         g.j0 = w.j;
@@ -404,20 +409,25 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
                 w.pair = 0;
                 if (++w.head == p.heads) {
                     w.head = 0;
-                    w.q_len = PAGED ? 0 : w.q_len;  // the next sequence is looked up when it is needed
+                    w.q_len = KIND ? 0 : w.q_len;  // the next sequence is looked up when it is needed
                 }
             }
         }
     }
     g.flags = g.n < it.n ? SPAN_PIECE : 0;
     for (int t = 0; t < 2; ++t) {
+        if (KIND == SPAN_TREE) {  // every token sees all keys before the sequence's new tokens
+            g.all_hi[t] = it.pos0 - it.tok0 - 128;
+            g.all_lo[t] = INT_MIN;
+            continue;
+        }
         const int tt = it.dual ? 0 : t * p.tile_tok, toks = min(it.ntok - tt, p.tile_tok);
         g.all_hi[t] = min(it.pos0 + tt + p.right, w_keys - 1) - 127;
         g.all_lo[t] = it.pos0 + tt + toks - 1 - p.left;
     }
     // rows behind the last key, in a box that holds keys (boxes without are zeros)
-    const int box = PAGED ? min(p.page, 128) : 128;
-    g.fix = PAGED && g.j0 == 0 && it.hi == w_keys >> 7 && (w_keys & (box - 1)) ? w_keys & 127 : -1;
+    const int box = KIND ? min(p.page, 128) : 128;
+    g.fix = KIND && g.j0 == 0 && it.hi == w_keys >> 7 && (w_keys & (box - 1)) ? w_keys & 127 : -1;
     return true;
 }
 
