@@ -89,6 +89,12 @@
 
 namespace xs {
 
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 // 32 lanes x 32-bit, 16 consecutive columns per thread, to tensor memory.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(512, 1)
 #define SEG_DONE()  /* after the warp's last look at the segment */      \
     do {                                                                \
         if (warp != 1) __syncwarp();                                    \
-        if (lane == 0) mbar_arrive(SEG_EMPTY(seg_it % kSegs));          \
+        if (warp == 1 || lane == 0) mbar_arrive(SEG_EMPTY(seg_it % kSegs));          \
         ++seg_it;                                                       \
     } while (0)
 
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 SEG_DONE();
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1 && elect_one()) {  // (not lane == 0: ptxas then knows of the one thread, and an MMA's set-up takes a third less code)
             // -------------------------------------------------------- MMA issuer
             // few rows: M = 128 keys (or columns of V, bit 15: A MN-major), N = the rows
             constexpr uint32_t idS = idesc_bf16_f32(128, FEW ? FEW : 128, 0);
@@ -526,7 +532,8 @@ __global__ void __launch_bounds__(512, 1)
                 }
             };
             uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0, pph0 = 0, pph1 = 0, fph = 0;
-            bool ok = true;
+            bool ok = true, carried = false;  // carried: the segment's first S has been issued with the one before it
+            enum : uint32_t { NEXT = 1, NEXT_S0 = 2, NEXT_LAST0 = 4, NEXT_S1 = 8, NEXT_LAST1 = 16, NEXT_Q = 32 };
             auto wait_kv = [&](uint32_t &slot) {
                 slot = kv_it % C::kSlots;
                 ok = ok && span_bwait(BAR(SPKV_FULL + slot), (kv_it / C::kSlots) & 1u, abort_flag, kSiteMmaKV);
@@ -561,8 +568,8 @@ __global__ void __launch_bounds__(512, 1)
                 const bool fix = KIND && g.fix >= 0;
                 uint32_t ks, vs;
                 const int qb = FEW ? (int)(seg_it & 1u) : 0;  // the tile that holds Q (dual)
-                ok = span_bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
                 if (FEW || g.dual) {
+                    ok = span_bwait(BAR(SPQ_FULL + qb), (FEW ? seg_it >> 1 : q_it0++) & 1u, abort_flag, kSiteMmaQ);
                     // two chains: even steps in S_0, O_0, odd ones in S_1, O_1
 #pragma unroll 1
                     for (int y = 0; y < n + 2; ++y) {  // S of step y, P V of step y - 2
@@ -586,26 +593,17 @@ __global__ void __launch_bounds__(512, 1)
                     }
                     if (ok && n == 1) no_steps(1);
                 } else {
-                    if (ok) ok = span_bwait(BAR(SPQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
                     // steps (of the segment) of tile 0: from f0 on; of tile 1: below l1 and from m1 on
                     const int f0 = max(g.s0 - g.j0, 0), l1 = min(g.e1 - g.j0, n), m1 = max(g.nw - g.j0, 0);
                     auto on1 = [&](int x) { return x < l1 || x >= m1; };
                     const int first1 = l1 > 0 ? 0 : m1, last1 = m1 < n ? n - 1 : l1 - 1;  // last1 < 0: none
-                    wait_kv(ks);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (f0 == 0) issue_S(0, 0, ks);
-                    if (n == 1) tc_commit(BAR(SPQ_EMPTY + 0));  // after each tile's last S
-                    if (on1(0)) issue_S(1, 1, ks);
-                    if (last1 <= 0) tc_commit(BAR(SPQ_EMPTY + 1));
-                    tc_commit(BAR(SPKV_EMPTY + ks));
                     // Steps in the middle, which both tiles take, as they do the next, have a loop
                     // without decisions: the issuer's own instructions are on the chain of every
                     // step (S = 16384, window of 4096: 516 us, 581 without). It is entered for as few as
                     // four: items of 10 steps with 5 of them here take 63.4 us then, 64.2 from one step
                     // on, 65.0 from six; the mixed paged batch 62.3, 62.5, 63.1, and 66.0 from twelve.
                     const int mid0 = f0 + 1, mid1 = min(l1, n) - 2;  // short of the last S of either tile
-                    for (int x = 0; x < n; ++x) {
+                    for (int x = carried ? 0 : -1; x < n; ++x) {  // P V of step x, S of the step behind it
                         if (x == mid0 && mid1 - x >= kMidSteps) {
 #pragma unroll 1
                             for (; x < mid1; ++x) {
@@ -632,32 +630,58 @@ __global__ void __launch_bounds__(512, 1)
                             }
                             if (!ok) break;
                         }
-                        const bool more = x + 1 < n;
-                        wait_v(vs, fix && x == 0);
-                        if (!ok) break;
-                        if (x >= f0) {
-                            wait_p(0, x == f0);
+                        // The step behind x: this segment's, or the next one's first where that is a pair too, whose
+                        // scores the softmax then finds ready when it has done with this segment.
+                        uint32_t next = 0;
+                        if (x + 1 < n) {
+                            next = NEXT | (x + 1 >= f0 ? NEXT_S0 : 0u) | (x + 2 == n ? NEXT_LAST0 : 0u) |
+                                   (on1(x + 1) ? NEXT_S1 : 0u) |
+                                   ((x < 0 ? last1 <= 0 : x + 1 == last1) ? NEXT_LAST1 : 0u) | (x < 0 ? NEXT_Q : 0u);
+                        } else {
+                            ok = span_bwait(SEG_FULL((seg_it + 1u) % kSegs), ((seg_it + 1u) / kSegs) & 1u, abort_flag, kSiteSeg);
                             if (!ok) break;
-                            issue_PV(0, vs, x > f0);
-                            if (!more) tc_commit(BAR(SPO_FINAL + 0));
+                            volatile SpanSeg &h = segs[(seg_it + 1u) % kSegs];
+                            const int n2 = h.n;
+                            if (n2 > 0 && !h.dual) {
+                                const int j2 = h.j0, l2 = min(h.e1 - j2, n2), m2 = h.nw - j2;
+                                next = NEXT | NEXT_Q | (h.s0 <= j2 ? NEXT_S0 : 0u) | (n2 == 1 ? NEXT_LAST0 : 0u) |
+                                       (l2 > 0 || m2 <= 0 ? NEXT_S1 : 0u) |
+                                       ((m2 < n2 ? n2 == 1 : l2 <= 1) ? NEXT_LAST1 : 0u);
+                            }
+                            carried = next != 0;
                         }
-                        if (more) {
+                        if (x >= 0) {
+                            wait_v(vs, fix && x == 0);
+                            if (!ok) break;
+                            if (x >= f0) {
+                                wait_p(0, x == f0);
+                                if (!ok) break;
+                                issue_PV(0, vs, x > f0);
+                                if (x + 1 == n) tc_commit(BAR(SPO_FINAL + 0));
+                            }
+                        }
+                        if (next) {
+                            if (next & NEXT_Q) ok = span_bwait(BAR(SPQ_FULL + 0), q_it0++ & 1u, abort_flag, kSiteMmaQ);
                             wait_kv(ks);
                             if (!ok) break;
                             tc_fence_after();
-                            if (x + 1 >= f0) issue_S(0, 0, ks);
-                            if (x + 2 == n) tc_commit(BAR(SPQ_EMPTY + 0));
+                            if (next & NEXT_S0) issue_S(0, 0, ks);
+                            if (next & NEXT_LAST0) tc_commit(BAR(SPQ_EMPTY + 0));  // after each tile's last S
                         }
-                        if (on1(x)) {
-                            wait_p(1, x == first1);
+                        if (x >= 0) {
+                            if (on1(x)) {
+                                wait_p(1, x == first1);
+                                if (!ok) break;
+                                issue_PV(1, vs, x > first1);
+                                if (x == last1) tc_commit(BAR(SPO_FINAL + 1));
+                            }
+                            tc_commit(BAR(SPKV_EMPTY + vs));
+                        }
+                        if (next) {
+                            if (next & NEXT_Q) ok = span_bwait(BAR(SPQ_FULL + 1), q_it1++ & 1u, abort_flag, kSiteMmaQ);
                             if (!ok) break;
-                            issue_PV(1, vs, x > first1);
-                            if (x == last1) tc_commit(BAR(SPO_FINAL + 1));
-                        }
-                        tc_commit(BAR(SPKV_EMPTY + vs));
-                        if (more) {
-                            if (on1(x + 1)) issue_S(1, 1, ks);
-                            if (x + 1 == last1) tc_commit(BAR(SPQ_EMPTY + 1));
+                            if (next & NEXT_S1) issue_S(1, 1, ks);
+                            if (next & NEXT_LAST1) tc_commit(BAR(SPQ_EMPTY + 1));
                             tc_commit(BAR(SPKV_EMPTY + ks));
                         }
                     }
