@@ -31,6 +31,10 @@ cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int nu
     // keys, one key head: 15.6 us, 17.1 with two), two for other chunks (5 of 267 to 669
     // tokens over 996 keys: 20.9 us, 24.9 with four), four of whole sequences.
     q.min_steps_log2 = p.few ? 0 : p.kind != SPAN_WHOLE ? 1 : 2;
+    // With 0, 2, 3, 4 and 6: 12 prompts of 130 to 4001 tokens 525, 428, 433, 446, 455 us; one of 2048 50.3, 41.5, 42.5,
+    // 43.2, 43.7; 9 trees of 7 to 61 tokens over 500 to 8000 63.2, 55.3, 56.7, 56.9, 60.0; 16 prompts of 2048 alike 450, 445,
+    // 442, 447, 452.
+    q.item_cost = 2;
     // a merge block adds up 32 rows of an item, or with few rows 256 groups of 4 columns
     const int rows = std::min(p.T, p.item_tok) * p.G, tile = p.tile_tok * p.G;
     q.merge_y = p.few ? (rows * (D / 4) + 255) / 256 : rows > tile ? 8 : (rows + 31) / 32;

@@ -190,7 +190,7 @@ template <int D, int KIND, int FEW> struct SpanCfg {
     static constexpr uint32_t kTmemCols = FEW ? 4 * FEW : 512;
     static_assert(kSmemAlloc <= 232448, "shared memory budget");
     static_assert(kSlots <= SPKV_EMPTY - SPKV_FULL, "barriers of the ring");
-    static_assert(kSlots * kTile >= 8u * 2048u, "the schedule's sums (kSpanMaxChunks)");
+    static_assert(kSlots * kTile >= 16u * kSpanMaxChunks, "the schedule's sums");
     static_assert((kOffSeg + sizeof(SpanSeg) * kSegs) % 8 == 0, "the SpanSched's place");
     static_assert(kOffQ % 1024 == 0 && kOffStage % 1024 == 0, "swizzled tiles");
 };

@@ -22,10 +22,11 @@ struct SpanSched {
     int ctas;
     int rounds;
     int seq, head, pair, j;
+    int cost;  // what an item counts for besides its steps
 };
 static_assert(sizeof(SpanSched) <= 64, "its place in shared memory");
 
-constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory
+constexpr int kSpanMaxChunks = 2048;  // groups of 32 sequences (or query tile pairs) in shared memory, 16 bytes each
 
 // An item's K/V tiles by step y: hi, hi - 1, ... (nw of them, the window's), then
 // ns - 1, ..., 0 (those of the sinks that lie before it).
@@ -91,17 +92,22 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
+// Whether a call's items differ so much that what an item counts for, when its work is shared
+// out, is its K/V steps and p.item_cost more for the change to it (12 prompts of 130 to
+// 4001 tokens: CTAs with short prompts ran for 600 us where the others took 410). Not with fewer
+// items than CTAs: a CTA's first item costs them all the same.
+template <int KIND> __device__ __forceinline__ constexpr bool span_weighs() { return KIND >= SPAN_PACKED; }
 // Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
 // is a sequence (all its heads and query rows) or, for whole sequences, which
-// are all alike, a query tile pair of one head.
+// are all alike, a query tile pair of one head. `cost`: what an item counts for besides its steps.
 template <int KIND>
-__device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane) {
+__device__ __forceinline__ long long span_group_steps(const SpanParams &p, int ch, int lane, int cost) {
     const int g = ch * 32 + lane;
     if (!KIND) return g < p.n_pairs ? (long long)span_item(p, p.S, p.S, g).n : 0ll;
     int q0 = 0, q_len = 0, keys = 0;
     if (g < p.N) span_lengths<KIND>(p, g, q0, q_len, keys);
     const int pairs = span_pairs(p, q_len);
-    long long u = pairs == 1 ? (long long)span_item(p, q_len, keys, 0).n * p.heads : 0ll;
+    long long u = pairs == 1 ? ((long long)span_item(p, q_len, keys, 0).n + cost) * p.heads : 0ll;
     uint32_t todo = __ballot_sync(0xffffffffu, pairs > 1);  // these the whole warp sums up, one after the other
 #pragma unroll 1
     while (todo) {
@@ -111,11 +117,19 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
         const int np = span_pairs(p, ql);
         long long s = 0;
 #pragma unroll 1
-        for (int i = lane; i < np; i += 32) s += span_item(p, ql, kl, i).n;
+        for (int i = lane; i < np; i += 32) s += span_item(p, ql, kl, i).n + cost;
         s = warp_sum(s);
         if (lane == src) u = s * p.heads;
     }
     return u;
+}
+
+// Items of the 32 groups of chunk ch.
+template <int KIND> __device__ __forceinline__ long long span_group_items(const SpanParams &p, int ch, int lane) {
+    int q0, q_len = 0, keys;
+    const int g = ch * 32 + lane;
+    if (g < p.N) span_lengths<KIND>(p, g, q0, q_len, keys);
+    return (long long)span_pairs(p, q_len) * p.heads;
 }
 
 // First step of CTA c's part of the shared steps: floor(c * shared / ctas), with the
@@ -143,6 +157,11 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
 
 // (The loops of the schedule stay rolled: they run once, and their code is fetched cold.)
 
+// Steps of chunk ch and `cost` for each of its items, from what span_chunk_sums has left.
+template <int KIND> __device__ __forceinline__ long long span_chunk_sum(const long long *sums, int chunks, int ch, int cost) {
+    return span_weighs<KIND>() ? sums[ch] + cost * sums[chunks + ch] : sums[ch];
+}
+
 // Where this CTA's part of the shared steps begins, by one warp. The shared steps
 // are the call's from step `before` on. `sum`: the steps of one head (whole
 // sequences). `mine`: the steps of this lane's group in the only chunk, when there
@@ -150,7 +169,7 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
 template <typename T, int KIND>
 __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T before, long long sum, long long mine,
                                           int chunks, const long long *sums, int lane) {
-    const int c = (int)blockIdx.x;
+    const int c = (int)blockIdx.x, cost = span_weighs<KIND>() ? s.cost : 0;
     const T total = (T)s.shared, q = total / (T)s.ctas;
     const uint32_t r = (uint32_t)(total - q * (T)s.ctas);
     s.q = (long long)q;
@@ -167,10 +186,10 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     if (chunks > 1) {
 #pragma unroll 1
         for (; l < 0 && ch < chunks; ch += 32)
-            l = span_locate<T>(ch + lane < chunks ? (T)sums[ch + lane] : (T)0, u, base, at, lane);
+            l = span_locate<T>(ch + lane < chunks ? (T)span_chunk_sum<KIND>(sums, chunks, ch + lane, cost) : (T)0, u, base, at, lane);
         ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
         base = at;
-        mine = span_group_steps<KIND>(p, ch, lane);
+        mine = span_group_steps<KIND>(p, ch, lane, cost);
     }
     l = span_locate<T>((T)mine, u, base, at, lane);
     u -= at;
@@ -184,14 +203,14 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     span_lengths<KIND>(p, s.seq, q0, q_len, keys);
     const int np = span_pairs(p, q_len);
     if (np == 1) {
-        const T n = (T)span_item(p, q_len, keys, 0).n;
+        const T n = (T)(span_item(p, q_len, keys, 0).n + cost);
         s.head = (int)(u / n);
         s.j = (int)(u - (T)s.head * n);
         return;
     }
     T per_head = 0;
 #pragma unroll 1
-    for (int i = lane; i < np; i += 32) per_head += (T)span_item(p, q_len, keys, i).n;
+    for (int i = lane; i < np; i += 32) per_head += (T)(span_item(p, q_len, keys, i).n + cost);
     per_head = warp_sum(per_head);
     s.head = (int)(u / per_head);
     u -= (T)s.head * per_head;
@@ -200,7 +219,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     int i = 0;
 #pragma unroll 1
     for (; l < 0 && i < np; i += 32)
-        l = span_locate<T>(i + lane < np ? (T)span_item(p, q_len, keys, i + lane).n : (T)0, u, base, at, lane);
+        l = span_locate<T>(i + lane < np ? (T)(span_item(p, q_len, keys, i + lane).n + cost) : (T)0, u, base, at, lane);
     s.pair = i - 32 + l;
     s.j = (int)(u - at);
 }
@@ -234,30 +253,48 @@ __device__ __forceinline__ int span_rounds(const SpanParams &p, int grid, long l
     return rounds;
 }
 
-// Sums of the steps of 32 groups each, when there are more; by all threads, and
-// followed by a barrier.
+// Sums of the steps of 32 groups each, when there are more, and behind them of their items where
+// those count; by all threads, and followed by a barrier.
 template <int KIND> __device__ __forceinline__ void span_chunk_sums(const SpanParams &p, int chunks, long long *sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int ch = warp; ch < chunks; ch += (int)(blockDim.x >> 5)) {
-        const long long s = warp_sum(span_group_steps<KIND>(p, ch, lane));
+        const long long s = warp_sum(span_group_steps<KIND>(p, ch, lane, 0));
         if (lane == 0) sums[ch] = s;
+        if (span_weighs<KIND>()) {
+            const long long i = warp_sum(span_group_items<KIND>(p, ch, lane));
+            if (lane == 0) sums[chunks + ch] = i;
+        }
     }
 }
 
 // The call's steps, how many CTAs share them and where this CTA's part starts; by one warp.
 template <int KIND>
 __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chunks, const long long *sums, int lane) {
-    long long mine = 0, sum = 0;
+    long long mine = 0, sum = 0, items = 0;
     if (chunks > 1) {
 #pragma unroll 1
-        for (int ch = lane; ch < chunks; ch += 32) sum += sums[ch];
+        for (int ch = lane; ch < chunks; ch += 32) {
+            sum += sums[ch];
+            if (span_weighs<KIND>()) items += sums[chunks + ch];
+        }
     } else {
-        sum = mine = span_group_steps<KIND>(p, 0, lane);
+        sum = mine = span_group_steps<KIND>(p, 0, lane, 0);
+        if (span_weighs<KIND>()) items = span_group_items<KIND>(p, 0, lane);
     }
     sum = warp_sum(sum);
+    int cost = 0;
+    if (span_weighs<KIND>()) {
+        const long long all = warp_sum(items);
+        if (all > (long long)gridDim.x) {
+            cost = p.item_cost;
+            sum += cost * all;
+            mine += cost * items;
+        }
+    }
     const long long total = KIND ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
+    s.cost = cost;
     // parts of a few steps or more, or a CTA for each key head of the sequences
     const long long least = KIND ? min(total, (long long)p.N * p.heads) : 0ll;
     s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> p.min_steps_log2, least)));
@@ -365,7 +402,7 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
 // The next part, as one segment; no steps and no flags if there is none.
 template <int KIND>
 __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
-    g.n = g.flags = 0;
+    g.n = g.flags = 0;  // (no segment, unless one is described below)
     if ((KIND || w.rounds == 0) && w.rem <= 0) return false;
     if (KIND)
         while (w.q_len == 0) {
@@ -398,12 +435,20 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
         else if (p.rec)
             span_walk_shared<KIND>(p, sched, w);
     } else {
+        // The item's steps lie behind `lead` units, which stand for the change to it.
+        const int lead = span_weighs<KIND>() ? sched.cost : 0;
+        if (span_weighs<KIND>()) {
+            const int skip = max(lead - w.j, 0);
+            if (w.rem <= skip) return false;  // the part ends before them
+            w.rem -= skip;
+            w.j += skip;
+        }
         w.first = false;
-        g.j0 = w.j;
-        g.n = (int)min((long long)(it.n - w.j), w.rem);
+        g.j0 = w.j - lead;
+        g.n = (int)min((long long)(it.n + lead - w.j), w.rem);
         w.rem -= g.n;
         w.j += g.n;
-        if (w.j == it.n) {
+        if (w.j == it.n + lead) {
             w.j = 0;
             if (++w.pair * p.item_tok >= w.q_len) {
                 w.pair = 0;
