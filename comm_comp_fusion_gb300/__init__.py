@@ -343,16 +343,20 @@ def attn_causal(q, k, v, out, B, S, H, D, P, scale, stream=None, check=True):
     return _check(st) if check else st
 
 
-_BF16, _INT32 = [], []   # the types that count as such, once torch has been imported (_dense)
+_BF16, _INT32 = [], []   # the types that count as such, once torch has been imported
+
+
+def _types():
+    import torch
+    _BF16[:] = [torch.bfloat16, torch.int16, torch.uint16]  # bf16 values may also come as their 16 bits
+    _INT32[:] = [torch.int32]
 
 
 def _dense(x, name, numel, kind, types):
     """The address of a tensor argument of the calls below: it must be contiguous, of its documented type and of at least
     `numel` elements."""
     if not types:
-        import torch
-        # bf16 values may also come as their 16 bits
-        types += [torch.bfloat16, torch.int16, torch.uint16] if kind == "bfloat16" else [torch.int32]
+        _types()
     if x.dtype not in types or not x.is_contiguous() or x.numel() < numel:
         raise ValueError(f"{name}: {numel} contiguous {kind} elements are needed, got "
                          f"{tuple(x.shape)} {x.dtype}{'' if x.is_contiguous() else ' (not contiguous)'}")
@@ -484,13 +488,16 @@ def _rows(x, name, T, heads, D):
     row = heads * D
     if x is None or isinstance(x, int):
         return x, row
-    if not x.is_contiguous() and x.dim() in (2, 3) and x.shape[0] >= T and (
-            (x.shape[1:] == (row,) and x.stride(1) == 1)
-            or (x.shape[1:] == (heads, D) and (x.stride(2) == 1 or D == 1) and (x.stride(1) == D or heads == 1))):
-        if T <= 1 or x.stride(0) >= row:
-            if x.dtype not in _BF16:
-                _bf16(x[:0], name, 0)
-            return x.data_ptr(), x.stride(0) if T > 1 else row
+    if not _BF16:
+        _types()
+    if x.dtype in _BF16:
+        shape, step = x.shape, x.stride()
+        if len(shape) == 3:
+            apart = shape[1] == heads and shape[2] == D and step[2] == 1 and (step[1] == D or heads == 1)
+        else:
+            apart = len(shape) == 2 and shape[1] == row and step[1] == 1
+        if apart and shape[0] >= T and (T <= 1 or step[0] >= row):
+            return x.data_ptr(), step[0] if T > 1 else row
     return _bf16(x, name, T * row), row
 
 

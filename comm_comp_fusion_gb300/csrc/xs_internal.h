@@ -173,7 +173,7 @@ struct AppendRopeParams {
     const int *table, *q_start, *kv_len;
     const int *pos;                               // [T][n_axes]; NULL: a token's place in its sequence
     int64_t q_stride, k_stride, v_stride;         // elements from one token's row to the next
-    int N, T, H, Hk, page, n_pages, max_pages;
+    int N, T, H, Hk, page, page_log2, n_pages, max_pages;
     int n_axes, n_pairs;
     int tile;                                     // tokens per block
     uint64_t frac[kRopeMaxPairs / 2];             // as in RopeParams

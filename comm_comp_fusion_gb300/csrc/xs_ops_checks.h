@@ -47,7 +47,7 @@ inline uint64_t turns_fraction(double f) {
     const double hi_c = 0.15915494309189535, lo_c = -9.839338337591243e-18;  // 1 / 2 pi
     const double x = std::fabs(f), hi = x * hi_c, lo = std::fma(x, hi_c, -hi) + x * lo_c;
     const double frac = hi - std::floor(hi);  // exact, below 1
-    const uint64_t u = (uint64_t)std::ldexp(frac, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+    const uint64_t u = (uint64_t)(frac * 0x1p64) + (uint64_t)(int64_t)std::llrint(lo * 0x1p64);  // (exact products)
     return f < 0 ? 0 - u : u;
 }
 
