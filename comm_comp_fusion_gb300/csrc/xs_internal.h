@@ -211,7 +211,7 @@ struct SpanParams {
     int tile_tok;               // tokens of a query tile: 128 / G, or few / G
     int item_tok;               // tokens of an item: two tiles, or one with few rows
     uint32_t g_magic;           // row / G = row * g_magic >> 16 for rows below 128: ceil(2^16 / G)
-    int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (whole sequences)
+    int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (packed prompts: at most so many items)
     int min_steps_log2;         // fewest steps that a CTA is started for
     int item_cost;              // packed prompts, trees: what an item counts for besides its steps (span_cost)
     int stretch;                // most steps that one sum in tensor memory takes; 0: no item has more (LONG = false)

@@ -237,7 +237,12 @@ xs_status xs_attn_packed(const void *q, const void *k, const void *v, int64_t q_
     p.item_tok = 2 * p.tile_tok;
     p.g_magic = (65536u + (uint32_t)p.G - 1u) / (uint32_t)p.G;
     p.heads = Hk;
-    span_workspace_parts(workspace, D, sms, &p);
+    p.n_pairs = T / p.item_tok + std::min(N, T);  // at most so many items a head
+    // A CTA for each item, none cut, where there are no more items than SMs and none is long, whatever the lengths: pieces
+    // and their merge cost more than their balance gains. Whole and cut, us: 4 prompts of 17 to 300 tokens, 8 heads, D = 64
+    // 11.2, 16.0; one of 500, 32 and 8 heads, D = 128 15.9, 20.1; of 900 20.9, 27.6; of 1000, 24 heads, D = 64 18.4, 20.1;
+    // but one of 1000, 8 and 1 heads 21.3, 19.8 and of 1500 26.2, 22.4; of 1500, 16 and 4 heads, D = 64 23.1, 20.9.
+    if ((long long)p.heads * p.n_pairs > sms || T > 1024) span_workspace_parts(workspace, D, sms, &p);
     SpanMaps maps;
     const uint64_t d = (uint64_t)D * 2;
     const uint64_t q_dims[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)Hk, (uint64_t)T};

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 if (!ok) break;
             }
-            if ((KIND || p.rec) && lane == 0) p.pieces[blockIdx.x] = pieces;
+            if ((p.rec || (KIND && KIND != SPAN_PACKED)) && lane == 0) p.pieces[blockIdx.x] = pieces;
         } else if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             uint32_t kv_it = 0, q_it0 = 0, q_it1 = 0;

@@ -97,6 +97,13 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 // 4001 tokens: CTAs with short prompts ran for 600 us where the others took 410). Not with fewer
 // items than CTAs: a CTA's first item costs them all the same.
 template <int KIND> __device__ __forceinline__ constexpr bool span_weighs() { return KIND >= SPAN_PACKED; }
+// Packed prompts without a workspace: whole items are shared out, each a unit.
+template <int KIND> __device__ __forceinline__ bool span_by_items(const SpanParams &p) { return KIND == SPAN_PACKED && !p.rec; }
+// The units of an item of n steps.
+template <int KIND> __device__ __forceinline__ int span_units(const SpanParams &p, int n, int cost) {
+    return span_by_items<KIND>(p) ? 1 : n + cost;
+}
+
 // Steps of the 32 groups of chunk ch, group ch * 32 + lane in each lane. A group
 // is a sequence (all its heads and query rows) or, for whole sequences, which
 // are all alike, a query tile pair of one head. `cost`: what an item counts for besides its steps.
@@ -107,7 +114,7 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
     int q0 = 0, q_len = 0, keys = 0;
     if (g < p.N) span_lengths<KIND>(p, g, q0, q_len, keys);
     const int pairs = span_pairs(p, q_len);
-    long long u = pairs == 1 ? ((long long)span_item(p, q_len, keys, 0).n + cost) * p.heads : 0ll;
+    long long u = pairs == 1 ? (long long)span_units<KIND>(p, span_item(p, q_len, keys, 0).n, cost) * p.heads : 0ll;
     uint32_t todo = __ballot_sync(0xffffffffu, pairs > 1);  // these the whole warp sums up, one after the other
 #pragma unroll 1
     while (todo) {
@@ -117,7 +124,7 @@ __device__ __forceinline__ long long span_group_steps(const SpanParams &p, int c
         const int np = span_pairs(p, ql);
         long long s = 0;
 #pragma unroll 1
-        for (int i = lane; i < np; i += 32) s += span_item(p, ql, kl, i).n + cost;
+        for (int i = lane; i < np; i += 32) s += span_units<KIND>(p, span_item(p, ql, kl, i).n, cost);
         s = warp_sum(s);
         if (lane == src) u = s * p.heads;
     }
@@ -203,14 +210,14 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     span_lengths<KIND>(p, s.seq, q0, q_len, keys);
     const int np = span_pairs(p, q_len);
     if (np == 1) {
-        const T n = (T)(span_item(p, q_len, keys, 0).n + cost);
+        const T n = (T)span_units<KIND>(p, span_item(p, q_len, keys, 0).n, cost);
         s.head = (int)(u / n);
         s.j = (int)(u - (T)s.head * n);
         return;
     }
     T per_head = 0;
 #pragma unroll 1
-    for (int i = lane; i < np; i += 32) per_head += (T)(span_item(p, q_len, keys, i).n + cost);
+    for (int i = lane; i < np; i += 32) per_head += (T)span_units<KIND>(p, span_item(p, q_len, keys, i).n, cost);
     per_head = warp_sum(per_head);
     s.head = (int)(u / per_head);
     u -= (T)s.head * per_head;
@@ -219,7 +226,7 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     int i = 0;
 #pragma unroll 1
     for (; l < 0 && i < np; i += 32)
-        l = span_locate<T>(i + lane < np ? (T)(span_item(p, q_len, keys, i + lane).n + cost) : (T)0, u, base, at, lane);
+        l = span_locate<T>(i + lane < np ? (T)span_units<KIND>(p, span_item(p, q_len, keys, i + lane).n, cost) : (T)0, u, base, at, lane);
     s.pair = i - 32 + l;
     s.j = (int)(u - at);
 }
@@ -286,7 +293,7 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     int cost = 0;
     if (span_weighs<KIND>()) {
         const long long all = warp_sum(items);
-        if (all > (long long)gridDim.x) {
+        if (all > (long long)gridDim.x && !span_by_items<KIND>(p)) {
             cost = p.item_cost;
             sum += cost * all;
             mine += cost * items;
@@ -297,7 +304,7 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     s.cost = cost;
     // parts of a few steps or more, or a CTA for each key head of the sequences
     const long long least = KIND ? min(total, (long long)p.N * p.heads) : 0ll;
-    s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> p.min_steps_log2, least)));
+    s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> (span_by_items<KIND>(p) ? 0 : p.min_steps_log2), least)));
     s.rem = s.q = 0;
     s.r = 0;
     s.rounds = s.seq = s.head = s.pair = s.j = 0;
@@ -399,6 +406,17 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
     span_lengths<KIND>(p, 0, w.q0, w.q_len, w.keys);
     span_skip(p, w, (int)blockIdx.x);
 }
+// The walk's next shared item.
+template <int KIND> __device__ __forceinline__ void span_next_item(const SpanParams &p, SpanWalk &w) {
+    w.j = 0;
+    if (++w.pair * p.item_tok >= w.q_len) {
+        w.pair = 0;
+        if (++w.head == p.heads) {
+            w.head = 0;
+            w.q_len = KIND ? 0 : w.q_len;  // the next sequence is looked up when it is needed
+        }
+    }
+}
 // The next part, as one segment; no steps and no flags if there is none.
 template <int KIND>
 __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &sched, SpanWalk &w, SpanSeg &g) {
@@ -434,6 +452,11 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
             span_skip(p, w, (int)gridDim.x);
         else if (p.rec)
             span_walk_shared<KIND>(p, sched, w);
+    } else if (span_by_items<KIND>(p)) {
+        g.j0 = 0;
+        g.n = it.n;
+        --w.rem;
+        span_next_item<KIND>(p, w);
     } else {
         // The item's steps lie behind `lead` units, which stand for the change to it.
         const int lead = span_weighs<KIND>() ? sched.cost : 0;
@@ -448,16 +471,7 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
         g.n = (int)min((long long)(it.n + lead - w.j), w.rem);
         w.rem -= g.n;
         w.j += g.n;
-        if (w.j == it.n + lead) {
-            w.j = 0;
-            if (++w.pair * p.item_tok >= w.q_len) {
-                w.pair = 0;
-                if (++w.head == p.heads) {
-                    w.head = 0;
-                    w.q_len = KIND ? 0 : w.q_len;  // the next sequence is looked up when it is needed
-                }
-            }
-        }
+        if (w.j == it.n + lead) span_next_item<KIND>(p, w);
     }
     g.flags = g.n < it.n ? SPAN_PIECE : 0;
     for (int t = 0; t < 2; ++t) {

@@ -20,7 +20,8 @@ def walk(tmp_path_factory):
     src, exe = d / "driver.cpp", d / "driver"
     code = DRIVER.replace("template <bool PAGED>", "template <int PAGED>").replace("sums(chunks)", "sums(2 * chunks)")
     code = code.replace("call<true>(p);", "if (std::scanf(\"%d\", &p.item_cost) != 1) return 1;\n"
-                        "if (paged == 1) call<SPAN_PAGED>(p);\nif (paged == 2) call<SPAN_PACKED>(p);\nif (paged == 3) call<SPAN_TREE>(p);")
+                        "if (paged == 1) call<SPAN_PAGED>(p);\nif (paged == 2) call<SPAN_PACKED>(p);\nif (paged == 3) call<SPAN_TREE>(p);\n"
+                        "if (paged == 4) { p.rec = nullptr; call<SPAN_PACKED>(p); }")
     assert "SPAN_TREE" in code and "2 * chunks" in code
     src.write_text(code)
     subprocess.run([gxx, "-std=c++17", "-O2", "-w", "-I", CSRC, "-I", CUDA_INC, str(src), "-o", str(exe)], check=True)
@@ -81,3 +82,22 @@ def test_weights_even_out_item_changes(walk):
             units[x[0]] += x[5] + cost * (x[4] == 0)
     share = (sum(items.values()) + cost * len(items)) / grid
     assert max(units) <= share + cost + 1
+
+
+def test_whole_items_without_workspace(walk):
+    """Packed prompts without a workspace: every item whole, and no CTA more than its share of them."""
+    rng = random.Random(3)
+    text, wants = "", []
+    for _ in range(60):
+        grid, heads, N = rng.choice((1, 3, 20, 152)), rng.randint(1, 6), rng.choice((1, 3, 50))
+        lens = [rng.choice((0, 1, rng.randint(1, 600))) for _ in range(N)]
+        text += f"4 {grid} {heads} 64 32 -1 0 0 1 {WHOLE} 0 {N} " + " ".join(f"{q} {q}" for q in lens) + " 2\n"
+        wants.append((grid, {(n, h, t): steps_of(t, min(64, q - t), q, -1, 0, 0)
+                             for n, q in enumerate(lens) for h in range(heads) for t in range(0, q, 64)}))
+    for (grid, items), lines in zip(wants, walk(text)):
+        verify(lines, items, grid)
+        count = [0] * grid
+        for line in lines:
+            assert line[0] == "s" and line.split()[5] == "0", line
+            count[int(line.split()[1])] += 1
+        assert max(count) <= -(-len(items) // grid)
