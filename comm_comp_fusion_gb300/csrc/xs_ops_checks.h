@@ -163,8 +163,11 @@ inline int span_paged(const void *q, const void *k_pages, const void *v_pages, i
     // and with more parts an item 32 gains more: 3 x 20000, 2 heads, 20 rows, D = 128 21.4 us, 25.7 with
     // tiles of 128. A chunk among single tokens costs: 64 of them over 1000 keys with 400 tokens over 8000
     // (G = 4, so 29 rows) took 244 us in tiles of 32 and 92 in tiles of 128, apart 50 and 52.
+    // Trees take tiles of 16 and of 128 rows only, masks of 32 rows a thread costing what they save: 16, 32 and 128, us, 8 key
+    // heads, D = 128: 16 rows, 16 x 4000 keys 51.0, -, 54.0 (D = 64 33.2, -, 35.1); 24 rows -, 55.3, 55.0, 4 x 1000 -, 16.8, 14.0;
+    // 32 rows -, 58.9, 55.0 and -, 19.5, 14.3.
     const long long rows_avg = ((long long)T * p->G + N - 1) / N;
-    p->few = p->G <= 16 && rows_avg <= 16 ? 16 : D > 64 && p->G <= 32 && rows_avg <= 24 ? 32 : 0;
+    p->few = p->G <= 16 && rows_avg <= 16 ? 16 : p->kind == SPAN_PAGED && D > 64 && p->G <= 32 && rows_avg <= 24 ? 32 : 0;
     p->tile_tok = (p->few ? p->few : 128) / p->G;
     p->item_tok = p->few ? p->tile_tok : 2 * p->tile_tok;
     for (p->page_log2 = 4; 1 << p->page_log2 < page;) ++p->page_log2;

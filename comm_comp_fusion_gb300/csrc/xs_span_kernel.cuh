@@ -1521,8 +1521,6 @@ static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, i
     cudaError_t launch_span_serve_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {    \
         if (p.kind == SPAN_PACKED) return launch_span_form<D, SPAN_PACKED, 0>(maps, p, grid, stream);                 \
         if (p.few == 16) return launch_span_form<D, SPAN_TREE, 16>(maps, p, grid, stream);                            \
-        if constexpr (D > 64)                                                                                         \
-            if (p.few == 32) return launch_span_form<D, SPAN_TREE, 32>(maps, p, grid, stream);                        \
         return launch_span_form<D, SPAN_TREE, 0>(maps, p, grid, stream);                                              \
     }                                                                                                                 \
     XS_DEFINE_SPAN_ERROR_WORD(read_error_word_span_serve_d##D)
