@@ -208,6 +208,46 @@ def test_packed_long_prompts_sampled(span):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,Hk,D,span", (([2 ** 18 + 4000, 700], 2, 1, 64, (-1, 0, 0)), ([300, 2 ** 18 + 129], 1, 1, 128, (-1, -1, 0)),
+                                              ([2 ** 18 + 70000], 3, 1, 96, (2 ** 18 + 1000, 0, 200))))
+def test_packed_very_long_prompt(lens, H, Hk, D, span):
+    """Prompts of more than 2^18 tokens: sums in tensor memory truncate, so they are taken in stretches. Values around 1,
+    where that shows. The bound: that of span_testlib.attend, and 2^14 additions of a stretch that truncate by 2^-23 at
+    most."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = rand(T, H, D).bfloat16(), rand(T, Hk, D).bfloat16(), (1 + 0.25 * rand(T, Hk, D)).bfloat16()
+    start = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+    out = guarded(T * H * D)
+    ws = guarded(xs.attn_packed_workspace_size(len(lens), T, H, Hk, D), torch.uint8, 0xFF)
+    xs.attn_packed(q, k, v, start, out, len(lens), T, H, Hk, D, D ** -0.5, *span, workspace=ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got, t = from_dev(out).reshape(T, H, D), 0
+    for m in lens:
+        rows = torch.cat((torch.arange(m - 1, 0, -m // 11, device="cuda"), torch.tensor([0, 1, m - 2], device="cuda")))
+        j = torch.arange(m, device="cuda").view(1, -1)
+        i = rows.view(-1, 1)
+        seen = torch.ones((len(rows), m), dtype=torch.bool, device="cuda")
+        if span[1] >= 0:
+            seen &= j <= i + span[1]
+        if span[0] >= 0:
+            seen &= (j >= i - span[0]) | (j < span[2])
+        for h in range(H):
+            kd, vd, qd = (x[t:t + m, g].double() for x, g in ((k, h * Hk // H), (v, h * Hk // H), (q, h)))
+            qd = qd[rows]
+            w = (qd @ kd.T * D ** -0.5).masked_fill(~seen, -np.inf).softmax(-1)
+            ref, a = w @ vd, w @ vd.abs()
+            delta = 2.0 ** -18 * (qd.abs() @ kd.abs().T * D ** -0.5).amax(-1, keepdim=True)
+            bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * delta + 2.0 ** -9) * a
+            check(got[t + rows.cpu().numpy(), h], ref.cpu().numpy(), bound.cpu().numpy(), f"head {h}")
+        t += m
+
+
+@pytest.mark.gpu
 def test_packed_graphs_and_streams():
     """A captured call follows starts that change between replays, two of them in one workspace; two on two streams."""
     import torch

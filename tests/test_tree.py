@@ -246,6 +246,90 @@ def test_tree_wide_tables(q_len, H, Hk, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,Hk,D,keys", ((3, 8, 2, 128, 2 ** 21 + 5), (16, 16, 2, 64, 2 ** 20 + 900), (40, 8, 1, 96, 2 ** 20 - 77)))
+def test_tree_very_many_keys(T, H, Hk, D, keys):
+    """Millions of keys before a tree, in every form. Values around 1; four pages stand for all before the tree, so a key's
+    weight counts as often as it comes. The bound: that of span_testlib.attend, and 2^14 additions of a stretch that
+    truncate by 2^-23 at most."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    page, own = 1024, 4096
+    max_pages = -(-keys // page)
+    rng = np.random.default_rng(keys)
+    gen = torch.Generator(device="cuda").manual_seed(keys)
+    rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda")  # noqa: E731
+    n_pages = 6  # the last two hold the tree
+    q, kp, vp = rand(T, H, D).bfloat16(), rand(n_pages, page, Hk, D).bfloat16(), (1 + 0.25 * rand(n_pages, page, Hk, D)).bfloat16()
+    table = (torch.arange(max_pages, device="cuda") % 4).to(torch.int32)
+    table[-2], table[-1] = 4, 5
+    q_start, kv_len = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, T], [keys]))
+    seen = rng.random((T, T)) < 0.5
+    words = (T + 31) // 32
+    mask = torch.from_numpy(to_words(seen, words)).cuda()
+    out = guarded(T * H * D)
+    ws = guarded(xs_size(1, T, H, Hk, D), torch.uint8, 0xFF)
+    xs.attn_tree(q, kp, vp, table, q_start, kv_len, mask, out, 1, T, H, Hk, D, page, n_pages, max_pages, words, D ** -0.5, ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got = from_dev(out).reshape(T, H, D)
+    first = (max_pages - 2) * page                     # place of the two last pages
+    j = torch.arange(own + 2 * page, device="cuda")
+    often = torch.zeros((T, own + 2 * page), dtype=torch.float64, device="cuda")
+    often[:, :own] = ((first - 1 - j[:own]) // own + 1).clamp(min=0).double()
+    place = first + j[own:] - own
+    often[:, own:] = (place < keys - T).double()
+    for i in range(T):
+        often[:, own + keys - T + i - first] = torch.from_numpy(seen[:, i].astype(np.float64)).cuda()
+    for h in sorted({0, 1, H // 2, H - 1}):
+        k, v = kp[:, :, h * Hk // H].reshape(-1, D).double(), vp[:, :, h * Hk // H].reshape(-1, D).double()
+        qd = q[:, h].double()
+        s = qd @ k.T * D ** -0.5
+        w = often * (s - s.amax(-1, keepdim=True)).exp()
+        w = w / w.sum(-1, keepdim=True)
+        ref, a = w @ v, w @ v.abs()
+        delta = 2.0 ** -18 * (qd.abs() @ k.abs().T * D ** -0.5).amax(-1, keepdim=True)
+        bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * delta + 2.0 ** -9) * a
+        check(got[:, h], ref.cpu().numpy(), bound.cpu().numpy(), f"head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,rows", ((1000, 1), (65536, 1), (30000, 3)))
+def test_tree_very_many_sequences(N, rows):
+    """Thousands of short sequences with chains of up to two tokens: the schedule's sums over the whole batch."""
+    import torch
+    import comm_comp_fusion_gb300 as xs
+    H, Hk, D, page, n_pages = 2 * rows, 2, 64, 16, 300
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    rand = lambda *shape: torch.randn(shape, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    kp, vp = rand(n_pages, page, Hk, D), rand(n_pages, page, Hk, D)
+    q_len = torch.randint(0, 3, (N,), generator=gen, device="cuda")
+    kv = torch.randint(2, 2 * page + 1, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    table = torch.randint(0, n_pages, (N, 2), generator=gen, device="cuda", dtype=torch.int32)
+    q_start = torch.cat((torch.zeros(1, dtype=torch.long, device="cuda"), q_len.cumsum(0)))
+    T = int(q_start[-1])
+    seq = torch.repeat_interleave(torch.arange(N, device="cuda"), q_len)
+    i = torch.arange(T, device="cuda") - q_start[seq]
+    mask = torch.where(i == 0, 1, 2).to(torch.int32)   # the second token does not see the first
+    q, out = rand(T, H, D), guarded(T * H * D)
+    ws = guarded(xs_size(N, T, H, Hk, D), torch.uint8)
+    xs.attn_tree(q, kp, vp, table, q_start.to(torch.int32), kv, mask, out, N, T, H, Hk, D, page, n_pages, 2, 1, 0.125, ws)
+    torch.cuda.synchronize()
+    assert xs.device_status() == xs.XS_OK, xs.last_error()
+    got = values(from_dev(out)).reshape(T, H, D)
+    for a in range(0, T, 20000):
+        r = slice(a, min(a + 20000, T))
+        k = kp[table[seq[r]].long()].view(-1, 2 * page, Hk, D).double().repeat_interleave(rows, 2)
+        v = vp[table[seq[r]].long()].view(-1, 2 * page, Hk, D).double().repeat_interleave(rows, 2)
+        s = torch.einsum("thd,tkhd->thk", q[r].double(), k) * 0.125
+        key, c = torch.arange(2 * page, device="cuda"), (kv[seq[r]] - q_len[seq[r]]).view(-1, 1)
+        see = (key < c) | (key == c + i[r].view(-1, 1))
+        w = s.masked_fill(~see.unsqueeze(1), -np.inf).softmax(-1)
+        ref, b = (torch.einsum("thk,tkhd->thd", w, x).cpu().numpy() for x in (v, v.abs()))
+        # the bound of span_testlib.attend; here scale sum |q k| is below 2^5, so the scores' share 2 delta is below 2^-12
+        assert (np.abs(got[r] - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * b + 1e-30).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("q_len,kv_len,H,Hk,D,page", (([1] * 4, [700, 90, 1500, 64], 8, 2, 128, 16), ([9, 300], [300, 900], 4, 2, 96, 64),
                                                       ([16, 1], [400, 33], 16, 2, 64, 32)))
 def test_tree_of_a_triangle_is_causal(q_len, kv_len, H, Hk, D, page):
