@@ -195,12 +195,13 @@ cudaError_t launch_tree_mask(const TreeMaskParams &p, cudaStream_t stream);
 struct SpanPieces;
 // What a span call works on: whole sequences of equal lengths, head-partitioned; new tokens over a paged
 // cache; whole sequences packed one after the other; new tokens over a paged cache under masks of bits.
-enum SpanKind : int { SPAN_WHOLE = 0, SPAN_PAGED = 1, SPAN_PACKED = 2, SPAN_TREE = 3 };
+enum SpanKind : int { SPAN_WHOLE = 0, SPAN_PAGED = 1, SPAN_PACKED = 2, SPAN_TREE = 3, SPAN_TREE_LANES = 4 };  // (span_tree_lanes)
+template <int KIND> constexpr bool kIsTree = KIND >= SPAN_TREE;
 struct SpanParams {
     uint16_t *out;
     int kind;                             // a SpanKind
     const int *table, *q_start, *kv_len;  // SPAN_PACKED: no table and no kv_len (and page = 128)
-    const int *mask;                      // SPAN_TREE: [T][words]
+    const int *mask;                      // trees: [T][words]
     int words;
     int N, T, H, Hk, G;         // whole sequences: T = B * S rows of H heads
     int page, page_log2, n_pages, max_pages;
@@ -234,7 +235,7 @@ cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int nu
 XS_DECLARE_SPAN_ENTRY(64)
 XS_DECLARE_SPAN_ENTRY(96)
 XS_DECLARE_SPAN_ENTRY(128)
-// SPAN_PACKED and SPAN_TREE (xs_span_serve_d*.cu)
+// packed prompts and trees (xs_span_serve_d*.cu)
 #define XS_DECLARE_SPAN_SERVE_ENTRY(D)                                                                           \
     cudaError_t launch_span_serve_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream); \
     cudaError_t read_error_word_span_serve_d##D(unsigned int *value, bool clear);

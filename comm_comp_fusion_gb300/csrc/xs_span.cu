@@ -39,7 +39,10 @@ cudaError_t launch_span(int D, const SpanMaps &maps, const SpanParams &p, int nu
     const int rows = std::min(p.T, p.item_tok) * p.G, tile = p.tile_tok * p.G;
     q.merge_y = p.few ? (rows * (D / 4) + 255) / 256 : rows > tile ? 8 : (rows + 31) / 32;
     const int grid = p.rec ? num_sms : (int)std::min((long long)num_sms, (long long)p.heads * p.n_pairs);
-    if (p.kind == SPAN_PACKED || p.kind == SPAN_TREE) {
+    // Trees of more than an item a key head on average may walk side by side. An instance apart: its schedule costs the
+    // others' short calls 1 to 2 us (4 trees of 8 tokens 16.3 us, 17.1).
+    if (p.kind == SPAN_TREE && !p.few && p.T > (long long)p.N * p.item_tok) q.kind = SPAN_TREE_LANES;
+    if (p.kind >= SPAN_PACKED) {
         if (D == 64) return launch_span_serve_d64(maps, q, grid, stream);
         if (D == 96) return launch_span_serve_d96(maps, q, grid, stream);
         if (D == 128) return launch_span_serve_d128(maps, q, grid, stream);

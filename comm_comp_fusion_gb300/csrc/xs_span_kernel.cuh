@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(512, 1)
     span_attn_kernel(const __grid_constant__ SpanMaps tm, const __grid_constant__ SpanParams p) {
     using C = SpanCfg<D, KIND, FEW>;
     using R = Rec<D>;
-    constexpr bool kPages = KIND == SPAN_PAGED || KIND == SPAN_TREE;  // K and V lie in pages
+    constexpr bool kPages = KIND == SPAN_PAGED || kIsTree<KIND>;  // K and V lie in pages
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(512, 1)
             for (bool more = true; more;) {
                 SpanSeg g;
                 more = span_next<KIND>(p, *sched, w, g);
-                if (more && g.flags && g.j0 == 0) pieces = span_pieces_of(*sched, g);  // its first piece: this CTA's last part
+                if (more && g.flags && g.j0 == 0) pieces = span_pieces_of<KIND>(*sched, g);  // its first piece: this CTA's last part
                 if (LONG) span_cut(g, p.stretch);
                 bool ok = span_warp_bwait(SEG_EMPTY(seg_it % kSegs), ((seg_it / kSegs) & 1u) ^ 1u, abort_flag, kSiteSeg);
                 if (!ok) break;
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(512, 1)
                         c_end = INT_MIN;
                     }
                     uint32_t by_row = ~0u;  // a tree's rows that see this thread's key; fetched before the scores are in
-                    if (KIND == SPAN_TREE && masked) by_row = span_tree_rows<FEW>(p, g, c0 + kl);
+                    if (kIsTree<KIND> && masked) by_row = span_tree_rows<FEW>(p, g, c0 + kl);
                     ok = span_warp_bwait(BAR(SPS_FULL + t), sph, abort_flag, kSiteSoftS);
                     if (!ok) break;
                     sph ^= 1u;
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(512, 1)
                         tmem_ld16(tS, s);
                     else
                         tmem_ld32(tS, s);
-                    if (KIND == SPAN_TREE && masked) {
+                    if (kIsTree<KIND> && masked) {
 #pragma unroll
                         for (int r = 0; r < FEW; ++r) s[r] = (by_row >> r) & 1u ? s[r] : f2u(-INFINITY);
                     } else if (masked) {
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(512, 1)
                         c_end = INT_MIN;
                     }
                     uint32_t bits_at[5] = {};  // a tree's words of this row for the tile; fetched before the scores are in
-                    if (KIND == SPAN_TREE && masked && !idle) {
+                    if (kIsTree<KIND> && masked && !idle) {
                         const int tok = min((g.dual ? 0 : t * p.tile_tok) + span_row_tok<KIND>(p, row), g.ntok - 1);
                         const int *m_row = p.mask + ((int64_t)g.q0 + g.tok0 + tok) * p.words;
                         const int w0 = (c0 - (g.pos0 - g.tok0)) >> 5;  // (rounded down)
@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
                         for (int h = 0; h < 128; h += 32) {
                             uint32_t bits;
-                            if (KIND == SPAN_TREE) {
+                            if (kIsTree<KIND>) {
                                 bits = __funnelshift_r(bits_at[0], bits_at[1], c0 - (g.pos0 - g.tok0)) &
                                        span_mask_word(INT_MIN / 2, g.keys - 1 - c0, 0, h);
 #pragma unroll
@@ -1366,7 +1366,7 @@ __global__ void __launch_bounds__(512, 1)
 
 // Adds up the pieces of the item whose first piece is CTA blockIdx.x's last
 // segment: piece 0 in the record named by the CTA, piece i > 0 in the first
-// record of CTA blockIdx.x + i, in that order. The pieces' loads go out several at
+// record of CTA blockIdx.x + i (trees: + i * lanes), in that order. The pieces' loads go out several at
 // a time (U), their latency being most of what this costs.
 // Records hold neighbouring rows of 4 columns side by side, so a warp reads 32 rows
 // of kPer such groups, block y 32 rows; the output rows are put together in shared
@@ -1381,6 +1381,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the attention kernel is done from here on
     const SpanPieces s = p.pieces[blockIdx.x];
     if (s.pieces < 2) return;
+    const int step = KIND == SPAN_TREE_LANES ? s.lanes : 1;  // CTAs from one piece to the next
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = FEW ? 0 : (int)blockIdx.y >> 2, row0 = FEW ? 0 : ((int)blockIdx.y & 3) * 32;  // this block's rows
     const int rows = min(s.ntok - t * p.tile_tok, p.tile_tok) * p.G - row0;
@@ -1401,7 +1402,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(const __grid_constant__
         for (int u = 0; u < U; ++u) {
             m[u] = -INFINITY;
             if (k0 + u >= s.pieces) continue;
-            const float *rec = p.rec + (size_t)(k0 + u == 0 ? s.slot : 2 * ((int)blockIdx.x + k0 + u)) * R::kFloats;
+            const float *rec = p.rec + (size_t)(k0 + u == 0 ? s.slot : 2 * ((int)blockIdx.x + (k0 + u) * step)) * R::kFloats;
             m[u] = rec[ml_at];
             l[u] = rec[ml_at + 128];
 #pragma unroll
@@ -1521,6 +1522,7 @@ static cudaError_t launch_span_form(const SpanMaps &maps, const SpanParams &p, i
     cudaError_t launch_span_serve_d##D(const SpanMaps &maps, const SpanParams &p, int grid, cudaStream_t stream) {    \
         if (p.kind == SPAN_PACKED) return launch_span_form<D, SPAN_PACKED, 0>(maps, p, grid, stream);                 \
         if (p.few == 16) return launch_span_form<D, SPAN_TREE, 16>(maps, p, grid, stream);                            \
+        if (p.kind == SPAN_TREE_LANES) return launch_span_form<D, SPAN_TREE_LANES, 0>(maps, p, grid, stream);         \
         return launch_span_form<D, SPAN_TREE, 0>(maps, p, grid, stream);                                              \
     }                                                                                                                 \
     XS_DEFINE_SPAN_ERROR_WORD(read_error_word_span_serve_d##D)

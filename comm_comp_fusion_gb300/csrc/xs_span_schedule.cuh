@@ -22,7 +22,8 @@ struct SpanSched {
     int ctas;
     int rounds;
     int seq, head, pair, j;
-    int cost;  // what an item counts for besides its steps
+    int cost;   // what an item counts for besides its steps
+    int lanes;  // trees: CTAs that walk the same keys side by side (span_tree_lanes)
 };
 static_assert(sizeof(SpanSched) <= 64, "its place in shared memory");
 
@@ -99,6 +100,35 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 template <int KIND> __device__ __forceinline__ constexpr bool span_weighs() { return KIND >= SPAN_PACKED; }
 // Packed prompts without a workspace: whole items are shared out, each a unit.
 template <int KIND> __device__ __forceinline__ bool span_by_items(const SpanParams &p) { return KIND == SPAN_PACKED && !p.rec; }
+// The items of a tree's key head walk the same keys. Where all trees have as many items a key head, two to four, that many
+// neighbouring CTAs, the lanes, take the steps of one item each side by side, so that K and V come from HBM once for them
+// all: lane r shares the items r of all heads out over the CTAs r, r + lanes, ... (16 trees of 64 tokens, 8 heads a key
+// head, over 4000 to 16384 keys: 224 us, 249 without; 1315 MB of DRAM reads without, for 671 of K and V).
+__device__ __forceinline__ int span_tree_lanes(const SpanParams &p, int lane) {
+    if (p.N > 1024) return 1;
+    int lo = INT_MAX, hi = 0;
+#pragma unroll 1
+    for (int g = lane; g < p.N; g += 32) {
+        int q0, q_len, keys;
+        span_lengths<SPAN_TREE>(p, g, q0, q_len, keys);
+        const int n = span_pairs(p, q_len);
+        if (n > 0) {
+            lo = min(lo, n);
+            hi = max(hi, n);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+    }
+    return lo == hi && hi >= 2 && hi <= 4 && hi <= (int)gridDim.x ? hi : 1;
+}
+// Lanes of a call, a CTA's place among its lane's, and its lane.
+template <int KIND> __device__ __forceinline__ int span_lanes(const SpanSched &s) { return KIND == SPAN_TREE_LANES ? s.lanes : 1; }
+template <int KIND> __device__ __forceinline__ int span_cta(const SpanSched &s) {
+    return KIND == SPAN_TREE_LANES && s.lanes > 1 ? (int)blockIdx.x / s.lanes : (int)blockIdx.x;
+}
 // The units of an item of n steps.
 template <int KIND> __device__ __forceinline__ int span_units(const SpanParams &p, int n, int cost) {
     return span_by_items<KIND>(p) ? 1 : n + cost;
@@ -165,8 +195,12 @@ template <typename T> __device__ __forceinline__ int span_locate(T v, T u, T &ba
 // (The loops of the schedule stay rolled: they run once, and their code is fetched cold.)
 
 // Steps of chunk ch and `cost` for each of its items, from what span_chunk_sums has left.
-template <int KIND> __device__ __forceinline__ long long span_chunk_sum(const long long *sums, int chunks, int ch, int cost) {
-    return span_weighs<KIND>() ? sums[ch] + cost * sums[chunks + ch] : sums[ch];
+// (A lane's share of them.)
+template <int KIND>
+__device__ __forceinline__ long long span_chunk_sum(const long long *sums, int chunks, int ch, int cost, int lanes) {
+    if (!span_weighs<KIND>()) return sums[ch];
+    const long long sum = sums[ch] + cost * sums[chunks + ch];
+    return KIND == SPAN_TREE_LANES && lanes > 1 ? sum / lanes : sum;
 }
 
 // Where this CTA's part of the shared steps begins, by one warp. The shared steps
@@ -176,7 +210,7 @@ template <int KIND> __device__ __forceinline__ long long span_chunk_sum(const lo
 template <typename T, int KIND>
 __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T before, long long sum, long long mine,
                                           int chunks, const long long *sums, int lane) {
-    const int c = (int)blockIdx.x, cost = span_weighs<KIND>() ? s.cost : 0;
+    const int c = span_cta<KIND>(s), cost = span_weighs<KIND>() ? s.cost : 0, lanes = span_lanes<KIND>(s);
     const T total = (T)s.shared, q = total / (T)s.ctas;
     const uint32_t r = (uint32_t)(total - q * (T)s.ctas);
     s.q = (long long)q;
@@ -193,10 +227,11 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     if (chunks > 1) {
 #pragma unroll 1
         for (; l < 0 && ch < chunks; ch += 32)
-            l = span_locate<T>(ch + lane < chunks ? (T)span_chunk_sum<KIND>(sums, chunks, ch + lane, cost) : (T)0, u, base, at, lane);
+            l = span_locate<T>(ch + lane < chunks ? (T)span_chunk_sum<KIND>(sums, chunks, ch + lane, cost, lanes) : (T)0, u, base, at, lane);
         ch = ch - 32 + l;  // the chunk that holds step u, starting at step `at`
         base = at;
         mine = span_group_steps<KIND>(p, ch, lane, cost);
+        if (lanes > 1) mine /= lanes;
     }
     l = span_locate<T>((T)mine, u, base, at, lane);
     u -= at;
@@ -209,7 +244,8 @@ __device__ __forceinline__ void span_find(const SpanParams &p, SpanSched &s, T b
     int q0, q_len, keys;
     span_lengths<KIND>(p, s.seq, q0, q_len, keys);
     const int np = span_pairs(p, q_len);
-    if (np == 1) {
+    if (np == 1 || lanes > 1) {
+        if (lanes > 1) s.pair = (int)blockIdx.x - c * lanes;
         const T n = (T)span_units<KIND>(p, span_item(p, q_len, keys, 0).n, cost);
         s.head = (int)(u / n);
         s.j = (int)(u - (T)s.head * n);
@@ -299,12 +335,21 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
             mine += cost * items;
         }
     }
-    const long long total = KIND ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     SpanSched s;
+    int grid = (int)gridDim.x;
     s.cost = cost;
+    if (KIND == SPAN_TREE_LANES) {
+        s.lanes = span_tree_lanes(p, lane);
+        if (s.lanes > 1) {  // a lane's: a key head's items are alike
+            sum /= s.lanes;
+            mine /= s.lanes;
+            grid /= s.lanes;
+        }
+    }
+    const long long total = KIND ? sum : sum * p.heads;  // whole sequences: `sum` is one head's
     // parts of a few steps or more, or a CTA for each key head of the sequences
     const long long least = KIND ? min(total, (long long)p.N * p.heads) : 0ll;
-    s.ctas = (int)max(1ll, min((long long)gridDim.x, max(total >> (span_by_items<KIND>(p) ? 0 : p.min_steps_log2), least)));
+    s.ctas = (int)max(1ll, min((long long)grid, max(total >> (span_by_items<KIND>(p) ? 0 : p.min_steps_log2), least)));
     s.rem = s.q = 0;
     s.r = 0;
     s.rounds = s.seq = s.head = s.pair = s.j = 0;
@@ -314,7 +359,7 @@ __device__ __forceinline__ SpanSched span_schedule(const SpanParams &p, int chun
     // Every CTA that shares them has a step: a part without one between two pieces of an item would
     // have written no record for the merge.
     if (s.shared > 0 && s.shared < s.ctas) s.ctas = (int)s.shared;
-    if ((int)blockIdx.x < s.ctas && s.shared > 0) {
+    if (span_cta<KIND>(s) < s.ctas && s.shared > 0) {
         if (total < (1ll << 31))
             span_find<uint32_t, KIND>(p, s, (uint32_t)before, sum, mine, chunks, sums, lane);
         else
@@ -407,10 +452,11 @@ __device__ __forceinline__ void span_walk_init(const SpanParams &p, const SpanSc
     span_skip(p, w, (int)blockIdx.x);
 }
 // The walk's next shared item.
-template <int KIND> __device__ __forceinline__ void span_next_item(const SpanParams &p, SpanWalk &w) {
+template <int KIND> __device__ __forceinline__ void span_next_item(const SpanParams &p, const SpanSched &s, SpanWalk &w) {
     w.j = 0;
-    if (++w.pair * p.item_tok >= w.q_len) {
-        w.pair = 0;
+    const bool lanes = span_lanes<KIND>(s) > 1;  // the item of the next head
+    if (lanes || ++w.pair * p.item_tok >= w.q_len) {
+        if (!lanes) w.pair = 0;
         if (++w.head == p.heads) {
             w.head = 0;
             w.q_len = KIND ? 0 : w.q_len;  // the next sequence is looked up when it is needed
@@ -456,7 +502,7 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
         g.j0 = 0;
         g.n = it.n;
         --w.rem;
-        span_next_item<KIND>(p, w);
+        span_next_item<KIND>(p, sched, w);
     } else {
         // The item's steps lie behind `lead` units, which stand for the change to it.
         const int lead = span_weighs<KIND>() ? sched.cost : 0;
@@ -471,11 +517,11 @@ __device__ __forceinline__ bool span_next(const SpanParams &p, const SpanSched &
         g.n = (int)min((long long)(it.n + lead - w.j), w.rem);
         w.rem -= g.n;
         w.j += g.n;
-        if (w.j == it.n + lead) span_next_item<KIND>(p, w);
+        if (w.j == it.n + lead) span_next_item<KIND>(p, sched, w);
     }
     g.flags = g.n < it.n ? SPAN_PIECE : 0;
     for (int t = 0; t < 2; ++t) {
-        if (KIND == SPAN_TREE) {  // every token sees all keys before the sequence's new tokens
+        if (kIsTree<KIND>) {  // every token sees all keys before the sequence's new tokens
             g.all_hi[t] = it.pos0 - it.tok0 - 128;
             g.all_lo[t] = INT_MIN;
             continue;
@@ -511,13 +557,15 @@ __device__ __forceinline__ void span_continue(volatile SpanSeg &d, const volatil
 // Written by each CTA for span_merge_kernel: the item whose first piece is the
 // CTA's last part (pieces 0: none).
 struct SpanPieces {
-    int pieces, slot, seq, head, tok0, ntok, q0, unused;
+    int pieces, slot, seq, head, tok0, ntok, q0;
+    int lanes;  // trees: the pieces' CTAs are so far apart
 };
 // Of a part that is an item's first piece: its pieces lie in this CTA and the next ones.
+template <int KIND = SPAN_WHOLE>
 __device__ __forceinline__ SpanPieces span_pieces_of(const SpanSched &s, const SpanSeg &g) {
-    const int left = g.nw + g.ns - g.n;
-    const long long end = span_first<unsigned long long>(s.q, s.r, s.ctas, (int)blockIdx.x + 1) + left;  // behind the item's last step
-    return SpanPieces{span_cta_of(s, end - 1) - (int)blockIdx.x + 1, g.slot, g.seq, g.head, g.tok0, g.ntok, g.q0, 0};
+    const int left = g.nw + g.ns - g.n, c = span_cta<KIND>(s);
+    const long long end = span_first<unsigned long long>(s.q, s.r, s.ctas, c + 1) + left;  // behind the item's last step
+    return SpanPieces{span_cta_of(s, end - 1) - c + 1, g.slot, g.seq, g.head, g.tok0, g.ntok, g.q0, KIND == SPAN_TREE_LANES ? s.lanes : 0};
 }
 
 }  // namespace xs

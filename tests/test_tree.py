@@ -214,6 +214,29 @@ def test_tree_few_rows(D, G, q_len):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_len,kv_len,H,Hk,D,page", (([64, 0, 61, 50], [3000, 9, 61, 2000], 16, 2, 128, 64), ([40] * 5, [700, 1500, 40, 41, 5000], 4, 1, 64, 16),
+                                                      ([96, 90], [4000, 1100], 8, 1, 96, 32), ([128] * 3, [2500, 300, 129], 24, 3, 128, 128),
+                                                      ([255, 250, 129], [3000, 250, 900], 4, 2, 64, 64), ([64] * 40, [64 + 37 * i for i in range(40)], 8, 1, 64, 16)))
+@pytest.mark.parametrize("wide", (False, True))
+def test_tree_alike_trees_side_by_side(q_len, kv_len, H, Hk, D, page, wide):
+    """Trees of two to four items a key head each, whose items neighbouring CTAs take side by side, whole and in pieces."""
+    import torch
+    b = Trees(q_len, kv_len, H, Hk, D, page, 8, spare=1, seed=D + len(q_len))
+    if wide:  # a table that could hold more than 2^18 keys
+        t = torch.full((b.N, 2 ** 18 // page + 100), -5, dtype=torch.int32, device="cuda")
+        t[:, :b.max_pages] = b.table
+        b.table, b.max_pages = t, t.shape[1]
+    b.ws.fill_(255)
+    b.call()
+    b.verify()
+    first = from_dev(b.out).copy()
+    b.out.fill_(-1)
+    b.call()
+    torch.cuda.synchronize()
+    assert np.array_equal(first, from_dev(b.out))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ctx", (0, 1, 31, 32, 33, 95, 96, 97, 127, 128, 129, 250))
 def test_tree_borders(ctx):
     """Every alignment of the tree's first bit in a tile of keys, for trees of one to four words."""
