@@ -139,7 +139,7 @@ def _load() -> ctypes.CDLL:
     lib.xs_attn_paged_workspace_size.restype = i
     i64 = ctypes.c_int64
     lib.xs_cache_append_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
-                                         i, ctypes.POINTER(i), ctypes.POINTER(ctypes.c_double), i, vp]
+                                         i, vp, vp, i, vp]
     lib.xs_cache_append_rope.restype = i
     lib.xs_tree_mask.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp]
     lib.xs_tree_mask.restype = i
@@ -513,8 +513,8 @@ def cache_append_rope(q, k, v, q_out, k_pages, v_pages, page_table, q_start, kv_
                                   _bf16(k_pages, "k_pages", pool), _bf16(v_pages, "v_pages", pool),
                                   _int32(page_table, "page_table", N * max_pages), _int32(q_start, "q_start", N + 1),
                                   _int32(kv_len, "kv_len", N), _int32(pos, "pos", T * n), N, T, H, Hk, D, page, n_pages,
-                                  max_pages, n, axes._dims, axes._freqs, XS_ROPE_HALVES if axes.halves else 0,
-                                  _stream(stream, k, k_pages))
+                                  max_pages, n, ctypes.addressof(axes._dims), ctypes.addressof(axes._freqs),
+                                  XS_ROPE_HALVES if axes.halves else 0, _stream(stream, k, k_pages))
     return _check(st) if check else st
 
 
