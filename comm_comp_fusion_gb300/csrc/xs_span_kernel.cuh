@@ -23,7 +23,9 @@
 // has any.
 //   * Two tiles (pair): each K/V tile is used by both, one tile's softmax running
 //     under the other's MMAs. A K/V tile that only one of them sees (at the
-//     window's ends) costs the other nothing.
+//     window's ends) costs the other nothing. Where a pair follows a pair, its first S
+//     is issued with the last step before it (12 packed prompts 631 us, 536 with it and
+//     the elected issuer; two-sided window S = 4096 64.0, 61.7).
 //   * One tile (dual; the last rows of a chunk): the even and the odd K/V tiles
 //     form two chains with an O of their own each, which the epilogue adds up. A
 //     chain's step is a long dependent sequence (MMA, softmax, MMA), so two of
@@ -49,6 +51,8 @@
 // An item that a part's border cuts is computed in pieces; each piece writes its
 // unnormalised O, row maxima and sums to the workspace, and span_merge_kernel
 // adds them up in piece order (no atomics: the result is the same every time).
+// Packed prompts and trees: an item counts for two steps more than it has, short packed
+// calls take whole items, and alike trees walk side by side (xs_span_schedule.cuh).
 //
 // Long items (LONG). The tensor cores' additions to O truncate: with values of 1, one sum over
 // 2^18 keys still rounds to 1, after 2^20 0.4% are missing, after 2^22 2.3%. Where a
@@ -62,11 +66,14 @@
 // Bounds. Single new tokens: HBM (32 sequences of 16000 keys, 8 key heads, D = 128, pages
 // of 32 tokens and more: 305 us, 6.9 TB/s; D = 64 and 96 reach 5.4; pages of 16 tokens
 // 5.9, their boxes' issue being the limit). Long chunks and windows: the chain S -
-// softmax - P V of a step, about 2850 cycles for two tiles at D = 128 (chunks of 2048
-// over 16K keys, 32 heads: 638 us at best, 1.68 PFLOP/s, and 731 in a stream of calls, at the
-// power limit). Items of few steps (a two-sided window of 512: 10): what lies between two items, about 6000 cycles of first loads, masked steps
-// and cold code, and steps that few rows need whole. Short calls: about 8 us of
-// set-up, first loads and first steps, whose instructions are fetched cold.
+// softmax - P V of a step, 2600 to 2850 cycles for two tiles at D = 128 (chunks of 2048
+// over 16K keys, 32 heads: 630 us at best, 1.70 PFLOP/s, and 742 in a stream of calls, at the
+// power limit; one packed prompt of 16384, 40 and 8 heads, causal: 1560, 1.76 PFLOP/s, and
+// 1693). Items of few steps (a two-sided window of 512: 10; packed prompts of 4000 tokens, 4
+// heads a key head: 16 on average): what lies between two items, about 5400 cycles of masked
+// steps and cold code (a line of instructions not met lately takes some 120), and steps that
+// few rows need whole. Short calls: about 8 us of set-up, first loads and first steps, whose
+// instructions are fetched cold.
 //
 // Roles of the 512 threads:
 //   warp 0      TMA producer: Q tiles, then K and V tiles into a 128 KB ring. Pages
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 SEG_DONE();
             }
-        } else if (warp == 1 && elect_one()) {  // (not lane == 0: ptxas then knows of the one thread, and an MMA's set-up takes a third less code)
+        } else if (warp == 1 && elect_one()) {  // (with lane == 0 ptxas does not know of the one thread: half as much code again)
             // -------------------------------------------------------- MMA issuer
             // few rows: M = 128 keys (or columns of V, bit 15: A MN-major), N = the rows
             constexpr uint32_t idS = idesc_bf16_f32(128, FEW ? FEW : 128, 0);

@@ -18,6 +18,8 @@ CASES = [  # q_len, kv_len, H, Hk, D, page, spare, axes, halves, positions given
     ([700, 0, 1300], [700, 0, 9000], 2, 1, 64, 256, 5, (64,), True, False, True, True),         # many tokens a block
     ([4000, 3500], [4000, 8000], 4, 2, 96, 128, 0, (96,), False, False, True, False),
     ([33, 2], [33, 40], 0, 2, 128, 16, 1, (128,), True, False, False, False),                   # keys and values alone
+    ([3, 1], [70, 9], 200, 100, 64, 16, 0, (32, 32), True, True, True, True),                   # many heads
+    ([25, 3], [25, 90], 12, 4, 96, 16, 2, (16, 48), True, True, True, False),
     ([9, 40], [3, 39], 4, 2, 128, 16, 2, (128,), True, False, False, True),                     # places before the sequence
 ]
 

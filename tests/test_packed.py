@@ -77,6 +77,9 @@ CASES = [  # lengths, H, Hk, D, spare, one projection, (left, right, sinks)
     ([2100], 16, 16, 128, 0, True, (-1, 0, 0)),
     ([1500, 700], 24, 24, 64, 0, False, (300, 0, 0)),
     (list(range(1, 200, 3)), 6, 6, 96, 4, False, (-1, 0, 0)),
+    ([9, 0, 12] * 20, 3, 1, 64, 0, True, (-1, 0, 0)),             # whole items of more sequences than a warp's lanes
+    ([1024], 4, 1, 128, 0, False, (-1, 0, 0)),                    # the longest call of whole items, and one more token
+    ([1000, 25], 4, 1, 128, 0, True, (-1, 0, 0)),
 ]
 
 
