@@ -508,8 +508,7 @@ xs_status xs_cache_append_rope(const void *q, const void *k, const void *v, int6
  *   q_start, kv_len, N, T : as below xs_cache_append.
  *   words  : 1 to 8. The first 32 * words new tokens of a sequence form its tree. Rows
  *            behind those get an empty mask and the context's length as position.
- * Rows of no sequence are left as they are. A branch of d tokens costs d steps of
- * about 30 ns.
+ * Rows of no sequence are left as they are.
  */
 xs_status xs_tree_mask(const int32_t *parents, const int32_t *q_start, const int32_t *kv_len, int32_t *mask, int32_t *pos,
                        int N, int T, int words, void *stream);

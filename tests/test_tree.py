@@ -47,6 +47,8 @@ MASKS = [  # q_len, kv_len, words, spare, late
     ([90, 96, 100], [2000, 96, 100], 3, 5, 1),
     ([256], [300], 8, 0, 60),                                    # nearly a chain
     ([7] * 400, [40] * 400, 2, 1, 2),
+    ([14, 15, 16, 17, 18, 33, 34, 100, 255, 256], [300] * 10, 8, 2, 4000),   # chains
+    ([32, 31, 17], [300] * 3, 1, 0, 4000),
 ]
 
 
