@@ -354,9 +354,9 @@ xs_status attention_call(const void *q, const void *k, const void *v, void *out,
     void *const ws = o.ws, *const trace = o.trace;
     const size_t ws_bytes = o.ws_bytes, trace_bytes = o.trace_bytes;
     const bool causal = o.causal;
-    if (!q || !k || !v || !out) return fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
+    if (B && S && (!q || !k || !v || !out)) return fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
     const bool host = o.hq || o.hk || o.hv || o.hout;
-    if (host && (!o.hq || !o.hk || !o.hv || !o.hout))
+    if (host && B && S && (!o.hq || !o.hk || !o.hv || !o.hout))
         return fail(XS_ERR_NULL, "host q, k, v and out must all be non-NULL");
     size_t bytes = 0;
     xs_status st = check_shape(B, S, H, D, P, true, &bytes);
@@ -715,7 +715,7 @@ xs_status xs_attn_workspace_size(int B, int S, int H, int D, int P, size_t *byte
 namespace {
 
 xs_status permute_call(const void *in, void *out, int B, int S, int H, int D, int P, void *stream, bool inverse) {
-    if (!in || !out) return fail(XS_ERR_NULL, "in and out must be non-NULL");
+    if (B && S && (!in || !out)) return fail(XS_ERR_NULL, "in and out must be non-NULL");
     size_t bytes = 0;
     xs_status st = check_shape(B, S, H, D, P, false, &bytes);
     if (st) return st;

@@ -57,7 +57,7 @@ int check_window(int B, int S, int H, int D, int P, size_t *bytes) {
 
 int window_call(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D, int P, float scale,
                 int left, int right, int sinks, void *ws, size_t ws_bytes, void *stream, bool a2a) {
-    if (!q || !k || !v || !out) return api_fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
+    if (B && S && (!q || !k || !v || !out)) return api_fail(XS_ERR_NULL, "q, k, v and out must be non-NULL");
     size_t bytes = 0;
     int st = check_window(B, S, H, D, P, &bytes);
     if (st || (st = check_scale(scale))) return st;
@@ -116,10 +116,11 @@ extern "C" {
 xs_status xs_rope(const void *q, const void *k, void *q_out, void *k_out, const int32_t *pos, int pos_batches, int B,
                   int S, int H, int Hk, int D, int P, int n_axes, const int *axis_dims, const double *freqs, int flags,
                   void *stream) {
-    if (!q || !q_out || !pos || !axis_dims || !freqs)
+    const bool work = B && S;
+    if (!axis_dims || !freqs || (work && (!q || !q_out || !pos)))
         return (xs_status)api_fail(XS_ERR_NULL, "q, q_out, pos, axis_dims and freqs must be non-NULL");
     if (Hk < 0) return (xs_status)api_fail(XS_ERR_SHAPE, "Hk must be >= 0 (got %d)", Hk);
-    if (Hk > 0 && (!k || !k_out)) return (xs_status)api_fail(XS_ERR_NULL, "k and k_out must be non-NULL unless Hk is 0");
+    if (work && Hk > 0 && (!k || !k_out)) return (xs_status)api_fail(XS_ERR_NULL, "k and k_out must be non-NULL unless Hk is 0");
     size_t qb = 0, kb = 0;
     int st = api_shape(B, S, H, D, P, &qb);
     if (!st && Hk > 0) st = api_shape(B, S, Hk, D, P, &kb);
@@ -199,7 +200,7 @@ xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_
 xs_status xs_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, const int32_t *page_table,
                           const int32_t *q_start, const int32_t *kv_len, int N, int T, int Hk, int D, int page,
                           int n_pages, int max_pages, void *stream) {
-    if (!k || !v || !k_pages || !v_pages || !page_table || !q_start || !kv_len)
+    if (N && T && (!k || !v || !k_pages || !v_pages || !page_table || !q_start || !kv_len))
         return (xs_status)api_fail(XS_ERR_NULL, "k, v, k_pages, v_pages, page_table, q_start and kv_len must be non-NULL");
     size_t pool, table;
     int st = check_cache(N, T, Hk, D, page, n_pages, max_pages, &pool, &table);
@@ -240,7 +241,7 @@ xs_status xs_attn_paged(const void *q, const void *k_pages, const void *v_pages,
                         const int32_t *q_start, const int32_t *kv_len, void *out, int N, int T, int H, int Hk, int D,
                         int page, int n_pages, int max_pages, float scale, int left, int right, int sinks,
                         void *workspace, size_t workspace_bytes, void *stream) {
-    if (!q || !k_pages || !v_pages || !page_table || !q_start || !kv_len || !out)
+    if (N && T && (!q || !k_pages || !v_pages || !page_table || !q_start || !kv_len || !out))
         return (xs_status)api_fail(XS_ERR_NULL, "q, k_pages, v_pages, page_table, q_start, kv_len and out must be non-NULL");
     size_t pool, table;
     int st = check_cache(N, T, Hk, D, page, n_pages, max_pages, &pool, &table);

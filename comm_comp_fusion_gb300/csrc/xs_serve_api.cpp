@@ -57,11 +57,12 @@ xs_status xs_cache_append_rope(const void *q, const void *k, const void *v, int6
                                const int32_t *pos, int N, int T, int H, int Hk, int D, int page, int n_pages,
                                int max_pages, int n_axes, const int *axis_dims, const double *freqs, int flags,
                                void *stream) {
-    if (!k || !v || !k_pages || !v_pages || !page_table || !q_start || !kv_len || !axis_dims || !freqs)
+    const bool work = N && T;
+    if (!axis_dims || !freqs || (work && (!k || !v || !k_pages || !v_pages || !page_table || !q_start || !kv_len)))
         return (xs_status)api_fail(XS_ERR_NULL, "k, v, k_pages, v_pages, page_table, q_start, kv_len, axis_dims and freqs "
                                                 "must be non-NULL");
     if (H < 0) return (xs_status)api_fail(XS_ERR_SHAPE, "H must be >= 0 (got %d)", H);
-    if (H > 0 && (!q || !q_out)) return (xs_status)api_fail(XS_ERR_NULL, "q and q_out must be non-NULL unless H is 0");
+    if (work && H > 0 && (!q || !q_out)) return (xs_status)api_fail(XS_ERR_NULL, "q and q_out must be non-NULL unless H is 0");
     size_t pool, table, qb, kb, vb;
     int st = check_cache(N, T, Hk, D, page, n_pages, max_pages, &pool, &table);
     if (st) return (xs_status)st;
@@ -74,7 +75,7 @@ xs_status xs_cache_append_rope(const void *q, const void *k, const void *v, int6
     AppendRopeParams p;
     memset(&p, 0, sizeof p);
     if ((st = rope_table(n_axes, axis_dims, freqs, (flags & XS_ROPE_HALVES) != 0, D, &p))) return (xs_status)st;
-    if (!pos && n_axes > 1) return (xs_status)api_fail(XS_ERR_NULL, "pos must be non-NULL with more than one axis");
+    if (work && !pos && n_axes > 1) return (xs_status)api_fail(XS_ERR_NULL, "pos must be non-NULL with more than one axis");
     if ((H && (misaligned16(q) || misaligned16(q_out))) || misaligned16(k) || misaligned16(v) || misaligned16(k_out) ||
         misaligned16(k_pages) || misaligned16(v_pages))
         return (xs_status)api_fail(XS_ERR_ALIGN, "q, k, v, q_out, k_out, k_pages and v_pages must be 16-byte aligned");
@@ -127,8 +128,10 @@ xs_status xs_cache_append_rope(const void *q, const void *k, const void *v, int6
 
 xs_status xs_tree_mask(const int32_t *parents, const int32_t *q_start, const int32_t *kv_len, int32_t *mask, int32_t *pos,
                        int N, int T, int words, void *stream) {
-    if (!parents || !q_start || !mask) return (xs_status)api_fail(XS_ERR_NULL, "parents, q_start and mask must be non-NULL");
-    if (pos && !kv_len) return (xs_status)api_fail(XS_ERR_NULL, "kv_len must be non-NULL unless pos is NULL");
+    const bool work = N && T;
+    if (work && (!parents || !q_start || !mask))
+        return (xs_status)api_fail(XS_ERR_NULL, "parents, q_start and mask must be non-NULL");
+    if (work && pos && !kv_len) return (xs_status)api_fail(XS_ERR_NULL, "kv_len must be non-NULL unless pos is NULL");
     if (N < 0 || T < 0) return (xs_status)api_fail(XS_ERR_SHAPE, "N and T must be >= 0 (got N=%d T=%d)", N, T);
     if (N > (1 << 16)) return (xs_status)api_fail(XS_ERR_SHAPE, "N=%d exceeds 65536 sequences", N);
     if (T > (1 << 29)) return (xs_status)api_fail(XS_ERR_SHAPE, "T=%d exceeds 2^29 rows", T);
@@ -153,7 +156,7 @@ xs_status xs_attn_tree(const void *q, const void *k_pages, const void *v_pages, 
                        const int32_t *q_start, const int32_t *kv_len, const int32_t *mask, void *out, int N, int T, int H,
                        int Hk, int D, int page, int n_pages, int max_pages, int words, float scale, void *workspace,
                        size_t workspace_bytes, void *stream) {
-    if (!q || !k_pages || !v_pages || !page_table || !q_start || !kv_len || !mask || !out)
+    if (N && T && (!q || !k_pages || !v_pages || !page_table || !q_start || !kv_len || !mask || !out))
         return (xs_status)api_fail(XS_ERR_NULL, "q, k_pages, v_pages, page_table, q_start, kv_len, mask and out must be non-NULL");
     size_t pool, table;
     int st = check_cache(N, T, Hk, D, page, n_pages, max_pages, &pool, &table);
@@ -200,7 +203,8 @@ xs_status xs_attn_tree_workspace_size(int N, int T, int H, int Hk, int D, size_t
 xs_status xs_attn_packed(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                          const int32_t *q_start, void *out, int N, int T, int H, int Hk, int D, float scale, int left,
                          int right, int sinks, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!q || !k || !v || !q_start || !out) return (xs_status)api_fail(XS_ERR_NULL, "q, k, v, q_start and out must be non-NULL");
+    if (N && T && (!q || !k || !v || !q_start || !out))
+        return (xs_status)api_fail(XS_ERR_NULL, "q, k, v, q_start and out must be non-NULL");
     int st = check_packed(N, T, H, Hk, D);
     if (st || (st = check_scale(scale))) return (xs_status)st;
     SpanParams p{};

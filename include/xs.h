@@ -40,7 +40,7 @@
  *     non-zero xs_status, enqueues nothing and leaves `out` untouched;
  *     xs_last_error() then describes it.
  *   - Shapes: B >= 0, S >= 0 (B == 0 or S == 0 is a valid empty call that
- *     enqueues nothing), H >= 1, P >= 1, H % P == 0, S % P == 0, D in {64, 96, 128, 256},
+ *     enqueues nothing; its device pointers may be NULL), H >= 1, P >= 1, H % P == 0, S % P == 0, D in {64, 96, 128, 256},
  *     scale positive and finite. Every tensor must stay below 2^40 bytes. S need
  *     not be a multiple of 128: the last query tile is then partial (rows past
  *     S are neither computed into nor stored) and the keys past S in the last
@@ -64,7 +64,7 @@ extern "C" {
 
 typedef enum {
     XS_OK = 0,
-    XS_ERR_NULL = 1,        /* a required pointer is NULL */
+    XS_ERR_NULL = 1,        /* a pointer that the call needs is NULL */
     XS_ERR_SHAPE = 2,       /* a shape rule above is violated */
     XS_ERR_ALIGN = 3,       /* a pointer is not 16-byte aligned */
     XS_ERR_UNSUPPORTED = 4, /* D not in {64,96,128,256}, wrong GPU, or a pointer that is not device memory */
@@ -421,7 +421,8 @@ xs_status xs_attn_window_workspace_size(int B, int S, int H, int D, int P, size_
  * the append. With a kv_len past the table's end the new tokens stand at the
  * table's last places, are written there and attend from there.
  * page: a power of two from 16 to 1024; max_pages * page <= 2^29; N <= 65536;
- * T <= 2^29; D = 64, 96 or 128.
+ * T <= 2^29; D = 64, 96 or 128. N == 0 or T == 0 is an empty call, here and in the calls
+ * below: it enqueues nothing, and its device pointers may be NULL.
  *
  * xs_cache_append writes the new tokens' keys and values,
  *   k, v : [T][Hk][D] bf16,
