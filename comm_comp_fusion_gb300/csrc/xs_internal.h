@@ -214,7 +214,7 @@ struct SpanParams {
     uint32_t g_magic;           // row / G = row * g_magic >> 16 for rows below 128: ceil(2^16 / G)
     int heads, n_pairs;         // key heads of a sequence; query tile pairs of a head (packed prompts: at most so many items)
     int min_steps_log2;         // fewest steps that a CTA is started for
-    int item_cost;              // packed prompts, trees: what an item counts for besides its steps (span_cost)
+    int item_cost;              // packed prompts, trees: what an item counts for besides its steps (span_weighs)
     int stretch;                // most steps that one sum in tensor memory takes; 0: no item has more (LONG = false)
     int merge_y;                // blocks per item in the merge
     float *rec;                 // workspace: 2 records a CTA (Rec<D>), one more a CTA for the segment at hand of a part in

@@ -93,17 +93,20 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
-// Whether a call's items differ so much that what an item counts for, when its work is shared
-// out, is its K/V steps and p.item_cost more for the change to it (12 prompts of 130 to
+// Packed prompts and trees come in any lengths. What an item of theirs counts for, when the work
+// is shared out, is its K/V steps and p.item_cost more for the change to it (12 prompts of 130 to
 // 4001 tokens: CTAs with short prompts ran for 600 us where the others took 410). Not with fewer
-// items than CTAs: a CTA's first item costs them all the same.
+// items than CTAs: a CTA's first item costs them all the same (span_schedule).
 template <int KIND> __device__ __forceinline__ constexpr bool span_weighs() { return KIND >= SPAN_PACKED; }
 // Packed prompts without a workspace: whole items are shared out, each a unit.
 template <int KIND> __device__ __forceinline__ bool span_by_items(const SpanParams &p) { return KIND == SPAN_PACKED && !p.rec; }
 // The items of a tree's key head walk the same keys. Where all trees have as many items a key head, two to four, that many
-// neighbouring CTAs, the lanes, take the steps of one item each side by side, so that K and V come from HBM once for them
-// all: lane r shares the items r of all heads out over the CTAs r, r + lanes, ... (16 trees of 64 tokens, 8 heads a key
-// head, over 4000 to 16384 keys: 224 us, 249 without; 1315 MB of DRAM reads without, for 671 of K and V).
+// neighbouring CTAs, the lanes, take the steps of one item each side by side and find in the L2 what the first of them has
+// read: lane r shares the items r of all heads out over the CTAs r, r + lanes, ... 16 trees over 4000 to 16384 keys, 8 heads
+// a key head, D = 128, so 32 tokens an item, us with lanes and without: 64 tokens 225, 246; 70 316, 340; 96 322, 354; 100
+// 418, 446; 128 420, 471; but 40 tokens, whose second item holds 8, 236, 233, and 70 tokens of 4 heads a key head, D = 64,
+// 185, 176. DRAM reads for 671 MB of K and V: 64 tokens 697 MB, 1317 without; 70 tokens, whose third item of 6 tokens soon
+// runs ahead of the others, 1236.
 __device__ __forceinline__ int span_tree_lanes(const SpanParams &p, int lane) {
     if (p.N > 1024) return 1;
     int lo = INT_MAX, hi = 0;
