@@ -659,7 +659,7 @@ xs_status xs_attn_host(const void *q_host, const void *k_host, const void *v_hos
 
 xs_status xs_attn_a2a_trace(const void *q, const void *k, const void *v, void *out, int B, int S, int H, int D,
                             int P, float scale, void *trace, size_t trace_bytes, void *stream) {
-    if (!trace) return fail(XS_ERR_NULL, "trace must be non-NULL");
+    if (B && S && !trace) return fail(XS_ERR_NULL, "trace must be non-NULL");
     CallOpts o;
     o.epi = 1;
     o.trace = trace;

@@ -68,7 +68,7 @@ xs_status scratch_for_current_device(ScratchState *out) {
 
 extern "C" xs_status xs_attn_a2a_noalloc(const void *q, const void *k, const void *v, void *out, int B, int S,
                                          int H, int D, int P, float scale, void *stream) {
-    if (!q || !k || !v || !out)
+    if (B && S && (!q || !k || !v || !out))
         return (xs_status)xs::report_error(XS_ERR_NULL, "q, k, v and out must be non-NULL");
     // shapes and device first (no launch yet); bytes is the balanced schedule's need
     size_t need = 0;

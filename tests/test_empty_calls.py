@@ -58,6 +58,10 @@ def test_whole_sequence_calls_without_work(xs, B, S):
         assert fn(*args, *((None, 0) if fn in (xs.attn_ws, xs.attn_a2a_ws) else ())) == xs.XS_OK, fn.__name__
     for fn in (xs.a2a_permute, xs.a2a_permute_inverse):
         assert fn(q, out, B, S, H, D, 1) == xs.XS_OK, fn.__name__
+    assert xs.attn_a2a_noalloc(*args) == xs.XS_OK
+    assert xs.attn_a2a_trace(q, k, v, out, B, S, H, 128, 1, 0.1, torch.zeros(0, dtype=torch.uint8)) == xs.XS_OK
+    for fn in (xs.attn_q8, xs.attn_a2a_q8, xs.attn_qkv8, xs.attn_a2a_qkv8):
+        assert fn(q, k, v, out, B, S, H, 128, 1, 0.1) == xs.XS_OK, fn.__name__
     host = torch.zeros(0, dtype=torch.bfloat16)
     for fn in (xs.attn_host, xs.attn_a2a_host):
         assert fn(host, host, host, host, *args) == xs.XS_OK, fn.__name__
